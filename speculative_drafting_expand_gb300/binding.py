@@ -1,4 +1,4 @@
-"""ctypes binding of libpeagle.so (include/peagle.h): argument marshalling only.
+"""ctypes binding of libpeagle.so (include/peagle*.h): argument marshalling only.
 
 Every step of the drafting path runs in the library's CUDA kernels; PyTorch
 is used here for device memory and streams.  Importing this module does not
@@ -29,6 +29,14 @@ PE_DTYPE_F32 = 1
 PE_MASK_BOOL_U8 = 0
 PE_MASK_ADDITIVE_BF16 = 1
 
+PE_KV_BF16 = 0
+PE_KV_F32 = 1
+PE_KV_E4M3 = 2
+
+PE_DEV_BAD_BLOCK = 2
+PE_DEV_BAD_POSITION = 3
+PE_DEV_BAD_ROW = 6
+
 # include/peagle.h and include/peagle_train.h (pe_status_string last: it is
 # the one that does not return a pe_status)
 EXPORTED = ("pe_create", "pe_destroy", "pe_expand_batch", "pe_draft_forward",
@@ -42,8 +50,12 @@ EXPORTED = ("pe_create", "pe_destroy", "pe_expand_batch", "pe_draft_forward",
             "pe_train_build_mask",
             "pe_train_mask_view", "pe_train_partition", "pe_status_string")
 
+# include/peagle_cache.h
+CACHE_EXPORTED = ("pe_kv_append", "pe_attn_decode_workspace", "pe_attn_decode", "pe_kv_evict")
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 
 class pe_model_desc(ctypes.Structure):
@@ -68,6 +80,12 @@ class pe_expanded(ctypes.Structure):
                                    "new_idx", "hidden_map", "cu_out", "seq_lens", "hidden")] + \
                [("B", _i32), ("K", _i32), ("T", _i32), ("T_out", _i32),
                 ("target_hidden", _vp)]
+
+
+class pe_kv_pool(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("scores", _vp), ("num_blocks", _i32),
+                ("n_kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 class PeError(RuntimeError):
@@ -112,8 +130,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                        _vp, _vp, _vp, _vp, ctypes.c_int64, _vp]
     lib.pe_status_string.argtypes = [_i32]
     lib.pe_status_string.restype = ctypes.c_char_p
-    for name in EXPORTED[:-1]:
+    lib.pe_kv_append.argtypes = [P(pe_kv_pool), _i32, _i32, _i32, ctypes.c_float, _vp, _i64, _vp,
+                                 _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
+    lib.pe_attn_decode_workspace.argtypes = [_i32, _i32, _i32, _i32]
+    lib.pe_attn_decode.argtypes = [P(pe_kv_pool), _i32, _i32, ctypes.c_float, _vp, _i64, _vp,
+                                   _i32, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp]
+    lib.pe_kv_evict.argtypes = [_i32, P(pe_kv_pool), _i32, _vp, _i32, _vp, _i32, _i32, _i32,
+                                ctypes.c_float, _vp, _i32, _vp, _vp, _vp, _vp]
+    for name in EXPORTED[:-1] + CACHE_EXPORTED:
         getattr(lib, name).restype = _i32
+    lib.pe_attn_decode_workspace.restype = _i64
     return lib
 
 
@@ -452,3 +478,216 @@ def pe_train_partition(n: int, K: int, r: float, u, bounds: Sequence[int], strea
         ptr(out["counts"]), ptr(out["offsets"]), ptr(out["rows"]), ptr(out["owned"]), cap,
         stream_ptr(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# paged KV cache operators (include/peagle_cache.h)
+# ---------------------------------------------------------------------------
+
+class KvPool:
+    """One layer's paged pools, borrowed: k, v [num_blocks, n_kv_heads, 16,
+    head_dim] (bfloat16, float32, or e4m3 codes as uint8 / float8_e4m3fn) and
+    scores, None or float32 [num_blocks, n_kv_heads, 16]."""
+
+    def __init__(self, k, v, scores=None, k_scale: float = 1.0, v_scale: float = 1.0):
+        torch = _torch()
+        kinds = {torch.bfloat16: PE_KV_BF16, torch.float32: PE_KV_F32, torch.uint8: PE_KV_E4M3,
+                 torch.float8_e4m3fn: PE_KV_E4M3}
+        if k.dim() != 4 or k.shape[2] != 16 or v.shape != k.shape:
+            raise ValueError("k and v must be [num_blocks, n_kv_heads, 16, head_dim]")
+        if k.dtype not in kinds or v.dtype != k.dtype:
+            raise ValueError("k and v must both be bfloat16, float32 or e4m3 codes")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous")
+        if scores is not None and (scores.dtype != torch.float32 or not scores.is_contiguous()
+                                   or scores.shape != k.shape[:3]):
+            raise ValueError("scores must be contiguous float32 [num_blocks, n_kv_heads, 16]")
+        if any(t is not None and t.device != k.device for t in (v, scores)):
+            raise ValueError("k, v and scores must be on one device")
+        self.k, self.v, self.scores, self.device = k, v, scores, k.device
+        self.num_blocks, self.n_kv_heads, _, self.head_dim = k.shape
+        self.dtype = kinds[k.dtype]
+        self.act_dtype = torch.float32 if self.dtype == PE_KV_F32 else torch.bfloat16
+        self.struct = pe_kv_pool(ptr(k), ptr(v), ptr(scores), self.num_blocks, self.n_kv_heads,
+                                 self.head_dim, self.dtype, k_scale, v_scale)
+        self._ref = ctypes.byref(self.struct)
+
+
+def _cache_rows(pool: KvPool, name: str, t, rows: int, heads: int) -> int:
+    """Row stride (elements) of a [rows, heads, head_dim] tensor whose heads
+    are contiguous."""
+    if t.shape != (rows, heads, pool.head_dim) or t.dtype != pool.act_dtype:
+        raise ValueError(f"{name} must be {pool.act_dtype} [{rows}, {heads}, {pool.head_dim}]")
+    row, head, one = t.stride()
+    if one != 1 or (head != pool.head_dim and heads > 1):
+        raise ValueError(f"{name} must have contiguous heads")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on the pool's device")
+    return row if rows > 1 else heads * pool.head_dim
+
+
+def _cache_i32(device, name: str, t, shape) -> None:
+    torch = _torch()
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device}")
+
+
+def _cache_table(device, name: str, t, B: int) -> int:
+    torch = _torch()
+    if (t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or t.device != device
+            or (t.shape[1] > 1 and t.stride(1) != 1)):
+        raise ValueError(f"{name} must be int32 [{B}, pages] with contiguous rows on {device}")
+    # a row's length is its stride: entries between rows belong to no request
+    if B > 1 and t.stride(0) != t.shape[1]:
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape[1]
+
+
+def _cache_ints(**values) -> None:
+    """ctypes takes an integer modulo 2^32: refuse what that would change."""
+    for name, x in values.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} must be a 32-bit integer")
+
+
+def _cache_call(device, stream, name, fn, *args) -> None:
+    """Call into the library with `device` current; `stream` None is that
+    device's current stream."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs tensors on a GPU")
+    s = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(name, fn(*args, s))
+    else:
+        with torch.cuda.device(device):
+            _check(name, fn(*args, s))
+
+
+def pe_kv_append(pool: KvPool, q, k, v, pos, block_table, rope_theta: float = 0.0, req=None,
+                 q_out=None, err=None, stream=None):
+    """Rotate the new rows q [T, n_heads, head_dim] (or None) and k [T,
+    n_kv_heads, head_dim] to positions pos [T] and write k and v into the
+    pages of their requests (req [T]; None: row t is request t's).  Returns
+    q_out (made when None)."""
+    T, B = k.shape[0], block_table.shape[0]
+    ks = _cache_rows(pool, "k", k, T, pool.n_kv_heads)
+    vs = _cache_rows(pool, "v", v, T, pool.n_kv_heads)
+    dev = pool.device
+    _cache_i32(dev, "pos", pos, (T,))
+    if req is not None:
+        _cache_i32(dev, "req", req, (T,))
+    pages = _cache_table(dev, "block_table", block_table, B)
+    n_heads = qs = qos = 0
+    if q is not None:
+        n_heads = q.shape[1]
+        qs = _cache_rows(pool, "q", q, T, n_heads)
+        if q_out is None:
+            q_out = _torch().empty((T, n_heads, pool.head_dim), dtype=q.dtype, device=dev)
+            if stream is not None:
+                q_out.record_stream(stream)
+        qos = _cache_rows(pool, "q_out", q_out, T, n_heads)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if err is not None:
+        _cache_i32(dev, "err", err, (1,))
+    _cache_call(dev, stream, "pe_kv_append", lib().pe_kv_append, pool._ref, T, B, n_heads,
+                rope_theta, ptr(q), qs, ptr(k), ks, ptr(v), vs, ptr(pos), ptr(req),
+                ptr(block_table), pages, ptr(q_out), qos, ptr(err))
+    return q_out
+
+
+def pe_attn_decode_workspace(B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of a pe_attn_decode call on the current device."""
+    n = lib().pe_attn_decode_workspace(B, n_heads, n_kv_heads, head_dim)
+    if n <= 0:
+        raise ValueError("pe_attn_decode_workspace: bad sizes")
+    return n
+
+
+def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float] = None,
+                   window: int = 0, accumulate: bool = False, out=None, lse=None,
+                   workspace=None, err=None, stream=None):
+    """Attention of one new token per request, q [B, n_heads, head_dim], over
+    its seq_lens [B] cached positions (the last `window` of them unless 0).
+    scale None: head_dim ** -0.5.  accumulate: each position's weight is added
+    to pool.scores.  Returns out and lse [B, n_heads] float32 (made when
+    None).  The workspace (uint8, pe_attn_decode_workspace bytes) is allocated
+    for the call when None."""
+    torch = _torch()
+    _cache_ints(window=window)
+    B, n_heads = q.shape[0], q.shape[1]
+    dev, dh = pool.device, pool.head_dim
+    qs = _cache_rows(pool, "q", q, B, n_heads)
+    pages = _cache_table(dev, "block_table", block_table, B)
+    _cache_i32(dev, "seq_lens", seq_lens, (B,))
+    made = []
+    if out is None:
+        out = torch.empty((B, n_heads, dh), dtype=q.dtype, device=dev)
+        made.append(out)
+    if lse is None:
+        lse = torch.empty((B, n_heads), dtype=torch.float32, device=dev)
+        made.append(lse)
+    elif (lse.dtype != torch.float32 or lse.shape != (B, n_heads) or not lse.is_contiguous()
+          or lse.device != dev):
+        raise ValueError(f"lse must be contiguous float32 [{B}, {n_heads}]")
+    os_ = _cache_rows(pool, "out", out, B, n_heads)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous on the pool's device")
+    if err is not None:
+        _cache_i32(dev, "err", err, (1,))
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    _cache_call(dev, stream, "pe_attn_decode", lib().pe_attn_decode, pool._ref, B, n_heads,
+                dh ** -0.5 if scale is None else scale, ptr(q), qs, ptr(block_table), pages,
+                ptr(seq_lens), window, ptr(out), os_, ptr(lse), int(accumulate), ptr(workspace),
+                workspace.numel() * workspace.element_size(), ptr(err))
+    return out, lse
+
+
+def pe_kv_evict(pools: Sequence[KvPool], block_table, seq_lens, budget: int, sinks: int = 0,
+                recent: int = 0, rope_theta: float = 0.0, dst_table=None, kept=None,
+                new_lens=None, err=None, stream=None):
+    """Trim every request of more than `budget` positions to that many, the
+    first `sinks`, the last `recent` and the heaviest of the rest by
+    pool.scores, per layer (one pool each) and kv head.  In place, or into
+    the pages of dst_table.  Returns kept [layers, B, n_kv_heads, budget] and
+    new_lens [B], int32 (made when None)."""
+    torch = _torch()
+    pools = list(pools)
+    if not pools:
+        raise ValueError("no pools")
+    _cache_ints(budget=budget, sinks=sinks, recent=recent)
+    p0, B = pools[0], block_table.shape[0]
+    dev = p0.device
+    if any(p.device != dev for p in pools):
+        raise ValueError("the pools must be on one device")
+    pages = _cache_table(dev, "block_table", block_table, B)
+    _cache_i32(dev, "seq_lens", seq_lens, (B,))
+    dst_pages = _cache_table(dev, "dst_table", dst_table, B) if dst_table is not None else 0
+    shape = (len(pools), B, p0.n_kv_heads, budget)
+    if budget < 1:
+        raise ValueError("budget must be positive")
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+        if stream is not None:
+            kept.record_stream(stream)
+    _cache_i32(dev, "kept", kept, shape)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        if stream is not None:
+            new_lens.record_stream(stream)
+    _cache_i32(dev, "new_lens", new_lens, (B,))
+    if err is not None:
+        _cache_i32(dev, "err", err, (1,))
+    arr = (pe_kv_pool * len(pools))(*[p.struct for p in pools])
+    _cache_call(dev, stream, "pe_kv_evict", lib().pe_kv_evict, len(pools), arr, B,
+                ptr(block_table), pages, ptr(seq_lens), budget, sinks, recent, rope_theta,
+                ptr(dst_table), dst_pages, ptr(kept), ptr(new_lens), ptr(err))
+    return kept, new_lens
