@@ -2,9 +2,38 @@
 // cache (include/peagle_cache.h):
 //   out = sum_j p_j v_j,  p_j = exp(z_j - lse),  z_j = scale q.k_j,
 //   lse = ln sum_j exp(z_j),
-// with one pass over K and V (running maximum m and sum l; a new maximum
-// scales what was summed by exp(m_old - m_new)) and, where asked, each
-// position's weight summed over the query heads of its kv head.
+// and, where asked, each position's weight summed over the query heads of its
+// kv head.
+//
+// One pass over K and V with a running maximum m and sum l (a new maximum
+// scales what was summed by 2^(m_old - m_new); logits are kept in units of
+// ln 2).  Bound by the bytes of K and V: a page row is used once per query
+// head of its group, 2 flops a byte and head.
+//
+// Work.  The unit is one page (16 positions) of one kv head; an item is the
+// run of pages of one (request, kv head, tile of query heads), and the items
+// lie one after another on a line that the CTAs cut into equal pieces, and
+// their warps those: every warp gets the same number of pages whatever the
+// lengths are.  An item that lies in one warp's piece is finished there.
+// Otherwise its parts (m, l, sum of p v) are joined: the warps' of one CTA
+// through shared memory, the CTAs' by a second launch (attn_join_kernel)
+// that starts as the first drains.  Joins run in the order of the positions:
+// results do not depend on timing.
+//
+// Tiles.  A warp owns its pages alone: its lanes copy them into a ring of
+// shared memory with 16-byte asynchronous copies, each lane (almost) only
+// what it reads itself, so no barrier stands between copy and use.  For 16-
+// and 8-bit pools S = Q K^T and O += P V are m16n8k16 matrix instructions of
+// the warp: M the query heads of the group (8 used, or 16), N positions or
+// elements.  A tcgen05 tile would hold 128 query rows where a group has 8;
+// the warp instruction needs no staging through tensor memory, and at two
+// bytes an element and 8 heads it is far from its rate.  The orders of the
+// elements along k and of the positions are free as long as both operands
+// share them: they are chosen such that every lane's operand is 16 contiguous
+// bytes of a row.  P enters as two 16-bit numbers (value and remainder, 2^-17
+// of it); with 8 heads the remainders are the otherwise unused rows 8..15.
+// e4m3 pools go through fp16, which holds every code; q is scaled there by a
+// power of two to [1, 2) so that fp16's range does not matter.
 #include <algorithm>
 
 #include "cache_common.cuh"
@@ -12,157 +41,1162 @@
 
 namespace pe {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxWarps = 8;  // warps a CTA
+constexpr int kMinPages = 2;  // pages a warp, where there are fewer than the grid could take
+
+// ------------------------------------------------------------------ shapes
+
+template <int DT, int DH, int GT>
+struct DecodeShape {
+  static constexpr int EB = DT == PE_KV_F32 ? 4 : DT == PE_KV_BF16 ? 2 : 1;
+  static constexpr int ROWB = DH * EB;
+  static constexpr int PAGEB = kPage * ROWB;       // a page of one head of K or V
+  static constexpr int CH = PAGEB / 512;           // 16-byte chunks a lane copies of it
+  // query heads a tile: the rows of the matrix instruction that are used, or
+  // what the registers of the fp32 path hold
+  static constexpr int ROWS = DT == PE_KV_F32 ? (DH == 64 ? 8 : 4) : 8 * GT;
+  static constexpr int WARPS = DT == PE_KV_F32 && DH == 128 ? 4 : 8;
+  static constexpr int STAGES = DT == PE_KV_E4M3 ? 6 : 3;
+  static constexpr int RING = STAGES * 2 * PAGEB;  // a warp's ring
+  static constexpr int REC = ROWS * (DH + 2);      // a partial result, floats: m, l, O
+  static constexpr int SCRATCH = DT == PE_KV_F32 ? (ROWS * DH + kPage * ROWS + ROWS) * 4 : 0;
+  static constexpr int SMEM = WARPS * (RING + SCRATCH);
+  static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;  // a SM
+  static_assert(REC * 4 <= RING, "a warp leaves its last partial in its ring");
+};
+
 struct DecodeArgs {
   CachePool pool;
-  int B, Hq, Hkv, bt_stride, window;
-  float scale;
+  int B, Hq, Hkv, G, bt_stride, window;
+  int tiles;       // tiles of query heads a kv head
+  float scale;     // of the logits, with ln 2 and the K scale divided in
+  float v_scale;
   const void* q;
   long long q_stride, out_stride;
   const int32_t* block_table;
   const int32_t* seq_lens;
   void* out;
-  float* lse;    // caller's, or NULL
-  float* lse_w;  // workspace [B, Hq]
+  float* lse;      // caller's, or NULL
   int* err;
-  float k_scale, v_scale;
+  // workspace
+  float* lse_w;    // [B, Hq], in units of ln 2
+  int4* meta;      // [grid]: item and flags of the CTA's first and last partial
+  float* part;     // [grid][2][REC]
+  float* head;     // [grid * WARPS][2][REC]
 };
 
-template <typename S>
-__device__ __forceinline__ float load_kv(const void* base, size_t at);
-template <>
-__device__ __forceinline__ float load_kv<float>(const void* base, size_t at) {
-  return static_cast<const float*>(base)[at];
-}
-template <>
-__device__ __forceinline__ float load_kv<bf16>(const void* base, size_t at) {
-  return __bfloat162float(static_cast<const bf16*>(base)[at]);
-}
-template <>
-__device__ __forceinline__ float load_kv<uint8_t>(const void* base, size_t at) {
-  const uint32_t h = e4m3x2_to_f16x2(static_cast<const uint8_t*>(base)[at]);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffff)));
-}
-
-__device__ __forceinline__ int request_len(const DecodeArgs& a, int b, bool record) {
+// A request's positions and pages: lo..n-1 attended, pages pf..pe-1.
+struct Span {
+  int n, lo, pf, pe;
+};
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, bool record) {
   const long long cap = static_cast<long long>(a.bt_stride) * kPage;
-  int n = a.seq_lens[b];
-  if (n < 0 || n > cap) {
+  Span s;
+  s.n = a.seq_lens[b];
+  if (s.n < 0 || s.n > cap) {
     if (record) record_error(a.err, PE_DEV_BAD_POSITION);
-    n = n < 0 ? 0 : static_cast<int>(cap);
+    s.n = s.n < 0 ? 0 : static_cast<int>(cap);
   }
-  return n;
+  s.lo = a.window > 0 ? max(0, s.n - a.window) : 0;
+  s.pf = s.lo / kPage;
+  s.pe = s.n > s.lo ? (s.n - 1) / kPage + 1 : s.pf;
+  return s;
 }
 
-// A CTA per (request, query head): its warps take every fourth position, a
-// warp's lanes the elements of a row; joined through shared memory.
-template <typename A, typename S, int DH>
-__global__ void __launch_bounds__(128) attn_decode_kernel(const DecodeArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  constexpr int E = DH / 32;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][DH];
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int hk = h / (a.Hq / a.Hkv);
-  const int n = request_len(a, b, threadIdx.x == 0);
-  const int lo = a.window > 0 ? max(0, n - a.window) : 0;
-  const A* q = static_cast<const A*>(a.q) + static_cast<size_t>(b) * a.q_stride + h * DH;
-  float qv[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_f(q[lane + 32 * e]) * (a.scale * a.k_scale);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo + w; j < n; j += 4) {
-    const int blk = a.block_table[static_cast<size_t>(b) * a.bt_stride + j / kPage];
-    if (blk < 0 || blk >= a.pool.num_blocks) {
-      if (lane == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
-      continue;
+// The line of pages: where unit u lies.  Every thread sums the pages of an
+// equal share of the requests; the shares' prefix sums stay in shared memory
+// and a warp searches them, then its share.
+struct Line {
+  long long total;  // units
+  int per;          // requests a share
+};
+template <int THREADS>
+__device__ __forceinline__ Line line_setup(const DecodeArgs& a, int heads, long long* prefix,
+                                           bool record) {
+  __shared__ long long warp_sum[THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  Line ln;
+  ln.per = (a.B + THREADS - 1) / THREADS;
+  long long mine = 0;
+  for (int i = 0; i < ln.per; ++i) {
+    const int b = tid * ln.per + i;
+    if (b < a.B) {
+      const Span s = span_of(a, b, record);
+      mine += s.pe - s.pf;
     }
-    const size_t at = ((static_cast<size_t>(blk) * a.Hkv + hk) * kPage + j % kPage) * DH;
-    float z = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) z += qv[e] * load_kv<S>(a.pool.k, at + lane + 32 * e);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-    const float mn = fmaxf(m, z);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float c = __expf(m - base), p = __expf(z - base);
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * c + p * load_kv<S>(a.pool.v, at + lane + 32 * e);
-    m = mn;
   }
-  if (lane == 0) {
-    sm_m[w] = m;
-    sm_l[w] = l;
-  }
+  mine *= heads;
+  long long x = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[w][lane + 32 * e] = o[e];
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[tid >> 5] = x;
   __syncthreads();
-  const float mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-  const float base = mt == -INFINITY ? 0.f : mt;
-  float lt = 0.f, c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = __expf(sm_m[i] - base);
-    lt += c[i] * sm_l[i];
+  long long base = 0;
+  for (int w = 0; w < (tid >> 5); ++w) base += warp_sum[w];
+  prefix[tid] = base + x - mine;
+  ln.total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) ln.total += warp_sum[w];
+  __syncthreads();
+  return ln;
+}
+
+// A place on the line: page p of head tile hh of request b.
+struct Place {
+  int b, hh;
+  Span s;
+  int p;
+};
+template <int THREADS>
+__device__ __forceinline__ Place place_of(const DecodeArgs& a, const Line& ln, int heads,
+                                          const long long* prefix, long long u) {
+  int lo = 0, hi = THREADS - 1;  // last share with prefix <= u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= u) lo = mid;
+    else hi = mid - 1;
   }
-  const float inv = lt == 0.f ? 0.f : a.v_scale / lt;
-  A* out = static_cast<A*>(a.out) + static_cast<size_t>(b) * a.out_stride + h * DH;
-  for (int d = threadIdx.x; d < DH; d += 128) {
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x += c[i] * sm_o[i][d];
-    out[d] = from_f<A>(x * inv);
+  Place pl;
+  long long left = u - prefix[lo];
+  pl.b = lo * ln.per;
+  pl.s = span_of(a, pl.b, false);
+  while (left >= static_cast<long long>(pl.s.pe - pl.s.pf) * heads) {
+    left -= static_cast<long long>(pl.s.pe - pl.s.pf) * heads;
+    pl.s = span_of(a, ++pl.b, false);
   }
-  if (threadIdx.x == 0) {
-    const float s = lt == 0.f ? -INFINITY : mt + logf(lt);
-    a.lse_w[b * a.Hq + h] = s;
-    if (a.lse) a.lse[b * a.Hq + h] = s;
+  pl.hh = static_cast<int>(left / (pl.s.pe - pl.s.pf));
+  pl.p = pl.s.pf + static_cast<int>(left % (pl.s.pe - pl.s.pf));
+  return pl;
+}
+// The first page of the next item (there is one).
+__device__ __forceinline__ void next_item(const DecodeArgs& a, int heads, Place& pl) {
+  if (++pl.hh == heads) {
+    pl.hh = 0;
+    do pl.s = span_of(a, ++pl.b, false);
+    while (pl.s.pe == pl.s.pf);
+  }
+  pl.p = pl.s.pf;
+}
+
+// ------------------------------------------------------------------ copies
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Lane (g = lane / 4, t = lane % 4).  K: rows key_of(j, g), j = 0, 1, elements
+// of chunks t + 4 i.  V: rows t + 4 i, chunks g + 8 i.  key_of() is the order
+// of the positions along the logits' columns: column n of half j.
+__device__ __forceinline__ int key_of(int j, int n) { return 8 * j + (n >> 1) + 4 * (n & 1); }
+
+template <class SH, int DT, int DH, bool WITH_V>
+__device__ __forceinline__ void copy_page(uint32_t stage, const CachePool& pool, int blk, int Hkv,
+                                          int hk, int v_lo, int v_hi, int lane) {
+  // positions v_lo <= offset < v_hi of the page are attended; the others
+  // read as zeros whatever lies there
+  const int g = lane >> 2, t = lane & 3;
+  const size_t base = (static_cast<size_t>(blk) * Hkv + hk) * SH::PAGEB;
+  const char* kp = static_cast<const char*>(pool.k) + base;
+  constexpr int KI = SH::CH / 2;  // chunks a row and lane
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = key_of(j, g);
+    const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+      cp_async16(stage + ((j * KI + i) * 32 + lane) * 16, kp + r * SH::ROWB + (t + 4 * i) * 16, n);
+  }
+  if (!WITH_V) return;
+  const char* vp = static_cast<const char*>(pool.v) + base;
+  stage += SH::PAGEB;
+  if constexpr (DT == PE_KV_E4M3 && DH == 64) {
+    // rows of 64 bytes, 8 a lane: the page as it lies, shared by the lanes
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      cp_async16(stage + (i * 32 + lane) * 16, vp + (i * 32 + lane) * 16,
+                 r >= v_lo && r < v_hi ? 16u : 0u);
+    }
+  } else {
+    constexpr int VI = SH::CH / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = t + 4 * i;
+      const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
+#pragma unroll
+      for (int c = 0; c < VI; ++c)
+        cp_async16(stage + ((i * VI + c) * 32 + lane) * 16, vp + r * SH::ROWB + (g + 8 * c) * 16,
+                   n);
+    }
   }
 }
 
-// Weights of a page's positions, a warp per (request, kv head, page slice).
-template <typename A, typename S, int DH>
-__global__ void __launch_bounds__(128) attn_scores_kernel(const DecodeArgs a) {
+// The copying side of a warp: pages of the line in order, a commit each.
+template <class SH, int DT, int DH, bool WITH_V>
+struct Feeder {
+  Place pl;
+  long long left;  // units still to copy
+  int ids;         // this lane's page of the 32 from ids_at on
+  int ids_at;      // -1: none
+  int stage;
+  uint32_t bad;    // stages whose page is none
+
+  __device__ __forceinline__ void step(const DecodeArgs& a, int heads, uint32_t ring, int lane,
+                                       bool record) {
+    if (left > 0) {
+      if (pl.p == pl.s.pe) {
+        next_item(a, heads, pl);
+        ids_at = -1;
+      }
+      if (ids_at < 0 || pl.p >= ids_at + 32) {
+        ids_at = pl.p;
+        ids = -1;
+        if (pl.p + lane < pl.s.pe)
+          ids = a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + lane];
+      }
+      const int blk = __shfl_sync(0xffffffffu, ids, pl.p - ids_at);
+      const bool ok = blk >= 0 && blk < a.pool.num_blocks;
+      if (!ok && record && lane == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
+      bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
+      const int first = pl.p * kPage;
+      copy_page<SH, DT, DH, WITH_V>(ring + stage * 2 * SH::PAGEB, a.pool, ok ? blk : 0, a.Hkv,
+                                    pl.hh / a.tiles, ok ? pl.s.lo - first : kPage,
+                                    ok ? pl.s.n - first : 0, lane);
+      ++pl.p;
+      --left;
+    }
+    cp_async_commit();
+    if (++stage == SH::STAGES) stage = 0;
+  }
+};
+
+// ------------------------------------------------------------ 16 and 8 bits
+
+template <int DT>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (DT == PE_KV_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two weights as a 16-bit pair and the pair of their remainders.
+template <int DT>
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  if constexpr (DT == PE_KV_BF16) {
+    hi = pack_bf16x2(x, y);
+    lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+  } else {
+    hi = pack_f16x2(x, y);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack_f16x2(x - f.x, y - f.y);
+  }
+}
+
+// The query heads of a tile as the A operand: for each chunk of 16 bytes of
+// a K row (8 or 16 elements), the words that meet its words.
+template <int DT, int DH, int GT>
+struct QueryTile {
+  static constexpr int STEPS = DH / 16;  // k steps of 16 elements
+  uint32_t a[GT][STEPS][2];
+  float factor[GT];  // logit = sum * factor (units of ln 2)
+
+  __device__ __forceinline__ void load(const DecodeArgs& A, int b, int h0, int rows, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      const int r = g + 8 * x;
+      const bool on = r < rows;
+      const bf16* q = static_cast<const bf16*>(A.q) + static_cast<size_t>(b) * A.q_stride +
+                      static_cast<size_t>(h0 + (on ? r : 0)) * DH;
+      factor[x] = A.scale;
+      if constexpr (DT == PE_KV_BF16) {
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          uint4 v = *reinterpret_cast<const uint4*>(q + (t + 4 * i) * 8);
+          if (!on) v = make_uint4(0, 0, 0, 0);
+          a[x][2 * i][0] = v.x;
+          a[x][2 * i][1] = v.y;
+          a[x][2 * i + 1][0] = v.z;
+          a[x][2 * i + 1][1] = v.w;
+        }
+      } else {
+        uint32_t w[STEPS][2];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < DH / 64; ++i) {
+          const uint4* p = reinterpret_cast<const uint4*>(q + (t + 4 * i) * 16);
+          const uint4 u = p[0], v = p[1];
+          const uint32_t z[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[4 * i + e / 2][e & 1] = on ? z[e] : 0u;
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(z[e] << 16)),
+                                   fabsf(__uint_as_float(z[e] & 0xffff0000u))));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent
+        const bool norm = ex > 1 && ex < 253;
+        const float down = norm ? __uint_as_float(static_cast<uint32_t>(254 - ex) << 23) : 1.f;
+        factor[x] *= norm ? __uint_as_float(static_cast<uint32_t>(ex) << 23) : 1.f;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            a[x][s][e] = pack_f16x2(__uint_as_float(w[s][e] << 16) * down,
+                                    __uint_as_float(w[s][e] & 0xffff0000u) * down);
+      }
+    }
+  }
+
+  // Logits of a page (units of ln 2): z[x][j][e], head g + 8 x, position
+  // key_of(j, 2 t + e).
+  template <class SH>
+  __device__ __forceinline__ void logits(uint32_t stage, int lane, float (&z)[GT][2][2]) const {
+    float c[2][4] = {};
+    constexpr int KI = SH::CH / 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const uint4 v = lds16(stage + ((j * KI + i) * 32 + lane) * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (DT == PE_KV_BF16) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            mma16816<DT>(c[j], a[0][2 * i + s][0], GT > 1 ? a[GT - 1][2 * i + s][0] : 0u,
+                         a[0][2 * i + s][1], GT > 1 ? a[GT - 1][2 * i + s][1] : 0u, w[2 * s],
+                         w[2 * s + 1]);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma16816<DT>(c[j], a[0][4 * i + s][0], GT > 1 ? a[GT - 1][4 * i + s][0] : 0u,
+                         a[0][4 * i + s][1], GT > 1 ? a[GT - 1][4 * i + s][1] : 0u,
+                         e4m3x2_to_f16x2(w[s]), e4m3x2_to_f16x2(w[s] >> 16));
+        }
+      }
+#pragma unroll
+    for (int x = 0; x < GT; ++x)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) z[x][j][e] = c[j][2 * x + e] * factor[x];
+  }
+};
+
+template <int DT, int DH, int GT>
+struct MmaTile {
+  using SH = DecodeShape<DT, DH, GT>;
+  static constexpr int NT = DH / 8;  // tiles of 8 elements
+  QueryTile<DT, DH, GT> q;
+  float m[GT], l[GT];                // head g + 8 x; l of this lane's positions
+  float o[NT][4];
+
+  __device__ __forceinline__ void start(const DecodeArgs& A, int b, int h0, int rows, char*,
+                                        int lane) {
+    q.load(A, b, h0, rows, lane);
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+
+  __device__ __forceinline__ void page(uint32_t stage, int v_lo, int v_hi, char*, int lane) {
+    const int t = lane & 3;
+    float z[GT][2][2];
+    q.template logits<SH>(stage, lane, z);
+    if (v_lo > 0 || v_hi < kPage) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = key_of(j, 2 * t + e);
+          if (r < v_lo || r >= v_hi)
+#pragma unroll
+            for (int x = 0; x < GT; ++x) z[x][j][e] = -INFINITY;
+        }
+    }
+    float top[GT];
+    bool grow = false;
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      top[x] = fmaxf(fmaxf(z[x][0][0], z[x][0][1]), fmaxf(z[x][1][0], z[x][1][1]));
+      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+      grow |= top[x] > m[x];
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+      float c[GT];
+#pragma unroll
+      for (int x = 0; x < GT; ++x) {
+        const float mn = fmaxf(m[x], top[x]);
+        c[x] = mn == -INFINITY ? 1.f : fast_exp2(m[x] - mn);
+        m[x] = mn;
+        l[x] *= c[x];
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        o[i][0] *= c[0];
+        o[i][1] *= c[0];
+        o[i][2] *= c[GT - 1];
+        o[i][3] *= c[GT - 1];
+      }
+    }
+    uint32_t hi[GT][2], lo[GT][2];
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      const float base = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float p0 = fast_exp2(z[x][j][0] - base), p1 = fast_exp2(z[x][j][1] - base);
+        l[x] += p0 + p1;
+        split2<DT>(p0, p1, hi[x][j], lo[x][j]);
+      }
+    }
+    auto pv = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
+      if constexpr (GT == 1) {
+        mma16816<DT>(c, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+      } else {
+        mma16816<DT>(c, hi[0][0], hi[1][0], hi[0][1], hi[1][1], b0, b1);
+        mma16816<DT>(c, lo[0][0], lo[1][0], lo[0][1], lo[1][1], b0, b1);
+      }
+    };
+    const uint32_t vs = stage + SH::PAGEB;
+    if constexpr (DT == PE_KV_BF16) {
+#pragma unroll
+      for (int c = 0; c < DH / 64; ++c) {
+        constexpr int VI = SH::CH / 4;
+        uint4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = lds16(vs + ((i * VI + c) * 32 + lane) * 16);
+        const uint32_t* w0 = &r[0].x;
+        const uint32_t* w1 = &r[1].x;
+        const uint32_t* w2 = &r[2].x;
+        const uint32_t* w3 = &r[3].x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          pv(o[8 * c + 2 * k], __byte_perm(w0[k], w1[k], 0x5410), __byte_perm(w2[k], w3[k], 0x5410));
+          pv(o[8 * c + 2 * k + 1], __byte_perm(w0[k], w1[k], 0x7632),
+             __byte_perm(w2[k], w3[k], 0x7632));
+        }
+      }
+    } else {
+      uint32_t w[4][DH / 32];
+      if constexpr (DH == 64) {
+        const int g = lane >> 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint2 u = lds8(vs + (t + 4 * i) * 64 + g * 8);
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = lds16(vs + (i * 32 + lane) * 16);
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+          w[i][DH / 32 - 2] = u.z;
+          w[i][DH / 32 - 1] = u.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k) {
+        const uint32_t x0 = __byte_perm(w[0][k], w[1][k], 0x5140);
+        const uint32_t x1 = __byte_perm(w[0][k], w[1][k], 0x7362);
+        const uint32_t y0 = __byte_perm(w[2][k], w[3][k], 0x5140);
+        const uint32_t y1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+        pv(o[4 * k], e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
+        pv(o[4 * k + 1], e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
+        pv(o[4 * k + 2], e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
+        pv(o[4 * k + 3], e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+      }
+    }
+  }
+
+  // Element of the rows that tile i, column n holds.
+  static __device__ __forceinline__ int elem(int i, int n) {
+    if constexpr (DT == PE_KV_BF16) return (n + 8 * (i >> 3)) * 8 + (i & 7);
+    else return n * NT + i;
+  }
+
+  // The partial result as a record: m[ROWS], l[ROWS], O[ROWS][DH].
+  __device__ __forceinline__ void store(float* rec, char*, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      float s = l[x];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      const int r = g + 8 * x;
+      if (t == 0) {
+        rec[r] = m[x];
+        rec[SH::ROWS + r] = s;
+      }
+      float* row = rec + 2 * SH::ROWS + r * DH;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          row[elem(i, 2 * t + e)] = GT == 1 ? o[i][e] + o[i][2 + e] : o[i][2 * x + e];
+    }
+  }
+};
+
+// ------------------------------------------------------------------ 32 bits
+// No matrix instruction keeps fp32 operands: each lane sums 16 (32) elements
+// of two positions for all heads of the tile, four lanes join their sums, and
+// the weights go through shared memory to the lanes that hold V.
+
+template <int DH>
+struct F32Tile {
+  using SH = DecodeShape<PE_KV_F32, DH, 1>;
+  static constexpr int R = SH::ROWS;
+  static constexpr int C = DH / 32;  // 16-byte chunks of a V row a lane
+  float m[R / 4], l[R / 4];          // heads (R / 4) t + x, this lane's positions
+  float o[R][C][4];                  // this lane's positions
+
+  // scratch of the warp: q [R][DH], p [16][R], c [R]
+  __device__ __forceinline__ void start(const DecodeArgs& A, int b, int h0, int rows, char* scratch,
+                                        int lane) {
+    float* q = reinterpret_cast<float*>(scratch);
+    const float* src = static_cast<const float*>(A.q) + static_cast<size_t>(b) * A.q_stride +
+                       static_cast<size_t>(h0) * DH;
+    __syncwarp();
+    for (int i = lane; i < R * DH; i += 32) q[i] = i < rows * DH ? src[i] * A.scale : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[h][c][e] = 0.f;
+  }
+
+  // z[x][j]: head (R / 4) t + x at position key_of(j, g)
+  static __device__ __forceinline__ void logits(uint32_t stage, const char* scratch, int lane,
+                                                float (&z)[R / 4][2]) {
+    const float* q = reinterpret_cast<const float*>(scratch);
+    const int t = lane & 3;
+    constexpr int KI = SH::CH / 2;
+    float s[R][2] = {};
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      float4 k[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 v = lds16(stage + ((j * KI + i) * 32 + lane) * 16);
+        k[j] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                           __uint_as_float(v.w));
+      }
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float4 qq = *reinterpret_cast<const float4*>(q + h * DH + (t + 4 * i) * 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          s[h][j] = fmaf(qq.x, k[j].x, fmaf(qq.y, k[j].y, fmaf(qq.z, k[j].z,
+                                                               fmaf(qq.w, k[j].w, s[h][j]))));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[h][j] += __shfl_xor_sync(0xffffffffu, s[h][j], 1);
+        s[h][j] += __shfl_xor_sync(0xffffffffu, s[h][j], 2);
+      }
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v = s[x][j];
+#pragma unroll
+        for (int u = 1; u < 4; ++u) v = t == u ? s[u * (R / 4) + x][j] : v;
+        z[x][j] = v;
+      }
+  }
+
+  __device__ __forceinline__ void page(uint32_t stage, int v_lo, int v_hi, char* scratch,
+                                       int lane) {
+    float* p = reinterpret_cast<float*>(scratch) + R * DH;
+    float* cs = p + kPage * R;
+    const int g = lane >> 2, t = lane & 3;
+    float z[R / 4][2];
+    logits(stage, scratch, lane, z);
+    bool grow = false;
+    float top[R / 4];
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = key_of(j, g);
+        if (r < v_lo || r >= v_hi) z[x][j] = -INFINITY;
+      }
+      top[x] = fmaxf(z[x][0], z[x][1]);
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1)
+        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], s));
+      grow |= top[x] > m[x];
+    }
+    const bool scale = __any_sync(0xffffffffu, grow);
+    if (scale) {
+#pragma unroll
+      for (int x = 0; x < R / 4; ++x) {
+        const float mn = fmaxf(m[x], top[x]);
+        const float c = mn == -INFINITY ? 1.f : fast_exp2(m[x] - mn);
+        m[x] = mn;
+        l[x] *= c;
+        if (g == 0) cs[t * (R / 4) + x] = c;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x) {
+      const float base = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float w = fast_exp2(z[x][j] - base);
+        l[x] += w;
+        p[key_of(j, g) * R + t * (R / 4) + x] = w;
+      }
+    }
+    __syncwarp();
+    if (scale)
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float c = cs[h];
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][i][e] *= c;
+      }
+    const uint32_t vs = stage + SH::PAGEB;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float w[R];
+#pragma unroll
+      for (int h = 0; h < R; h += 4)
+        *reinterpret_cast<float4*>(w + h) =
+            *reinterpret_cast<const float4*>(p + (t + 4 * i) * R + h);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 v = lds16(vs + ((i * C + c) * 32 + lane) * 16);
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          o[h][c][0] = fmaf(w[h], __uint_as_float(v.x), o[h][c][0]);
+          o[h][c][1] = fmaf(w[h], __uint_as_float(v.y), o[h][c][1]);
+          o[h][c][2] = fmaf(w[h], __uint_as_float(v.z), o[h][c][2]);
+          o[h][c][3] = fmaf(w[h], __uint_as_float(v.w), o[h][c][3]);
+        }
+      }
+    }
+    __syncwarp();  // p is rewritten by the next page
+  }
+
+  __device__ __forceinline__ void store(float* rec, char*, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x) {
+      float s = l[x];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if (g == 0) {
+        rec[t * (R / 4) + x] = m[x];
+        rec[R + t * (R / 4) + x] = s;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = o[h][c][e];
+          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 1);
+          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 2);
+        }
+        if (t == (c & 3))
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rec[2 * R + h * DH + (g + 8 * c) * 4 + e] = v[e];
+      }
+  }
+};
+
+template <int DT, int DH, int GT>
+struct TileOf {
+  using type = MmaTile<DT, DH, GT>;
+};
+template <int DH, int GT>
+struct TileOf<PE_KV_F32, DH, GT> {
+  using type = F32Tile<DH>;
+};
+
+// ----------------------------------------------------------------- results
+
+struct ActOf {
+  static __device__ __forceinline__ void put(void* out, size_t at, float x, bool f32) {
+    if (f32) static_cast<float*>(out)[at] = x;
+    else static_cast<bf16*>(out)[at] = __float2bfloat16_rn(x);
+  }
+};
+
+// Joins `count` records (rec(i), in the order of the positions) into a
+// finished item or into `dst`, over the threads first, first + step, ...
+// Rows row0 .. row1 - 1 of the tile.  GLOBAL: another CTA wrote the records;
+// else this one did, in shared or global memory.
+template <bool GLOBAL>
+__device__ __forceinline__ float ld_part(const float* p) {
+  if (GLOBAL) return __ldcg(p);
+  return *static_cast<const volatile float*>(p);
+}
+template <int DT, int DH, int GT, bool GLOBAL, typename Rec>
+__device__ __forceinline__ void join_records(const DecodeArgs& a, int b, int hh, int count, Rec rec,
+                                             float* dst, int row0, int row1, int first, int step) {
+  using SH = DecodeShape<DT, DH, GT>;
+  const int hk = hh / a.tiles, h0 = hk * a.G + (hh % a.tiles) * SH::ROWS;
+  const int rows = min(SH::ROWS, a.G - (hh % a.tiles) * SH::ROWS);
+  for (int e = row0 * DH + first; e < row1 * DH; e += step) {
+    const int r = e / DH, d = e % DH;
+    float M = -INFINITY;
+    for (int i = 0; i < count; ++i) M = fmaxf(M, ld_part<GLOBAL>(rec(i) + r));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, O = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const float* p = rec(i);
+      const float c = fast_exp2(ld_part<GLOBAL>(p + r) - base);
+      L = fmaf(c, ld_part<GLOBAL>(p + SH::ROWS + r), L);
+      O = fmaf(c, ld_part<GLOBAL>(p + 2 * SH::ROWS + e), O);
+    }
+    if (dst) {
+      dst[2 * SH::ROWS + e] = O;
+      if (d == 0) {
+        dst[r] = M;
+        dst[SH::ROWS + r] = L;
+      }
+    } else if (r < rows) {
+      const bool none = M == -INFINITY && !(L != L);
+      ActOf::put(a.out, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(h0 + r) * DH + d,
+                 none ? 0.f : O * (a.v_scale / L), DT == PE_KV_F32);
+      if (d == 0) {
+        const float s = none ? -INFINITY : M + log2f(L);
+        a.lse_w[static_cast<size_t>(b) * a.Hq + h0 + r] = s;
+        if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h0 + r] = s * kLn2;
+      }
+    }
+  }
+}
+
+// A CTA's meta word pair: .x, .y the first partial's item (request, head
+// tile) when it began before the CTA, else -1; .z, .w the last partial's that
+// goes on after it (request and head tile).  An item that covers the whole
+// CTA is first and last: kWhole in .w.
+constexpr int kWhole = 1 << 30;
+
+template <int DT, int DH, int GT>
+__global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
+                                  DecodeShape<DT, DH, GT>::CTAS)
+    attn_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using SH = DecodeShape<DT, DH, GT>;
+  using Tile = typename TileOf<DT, DH, GT>::type;
+  constexpr int W = SH::WARPS, THREADS = W * 32;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ long long prefix[THREADS];
+  // a warp's partials: first (began before its piece), last (goes on after)
+  __shared__ int w_state[W], w_b[W][2], w_hh[W][2];
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int E = DH / 32;
-  const int b = blockIdx.x / a.Hkv, hk = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = request_len(a, b, false);
-  const int lo = a.window > 0 ? max(0, n - a.window) : 0;
-  for (int j = lo + w + 4 * blockIdx.y; j < n; j += 4 * gridDim.y) {
-    const int blk = a.block_table[static_cast<size_t>(b) * a.bt_stride + j / kPage];
-    if (blk < 0 || blk >= a.pool.num_blocks) continue;
-    const size_t row = (static_cast<size_t>(blk) * a.Hkv + hk) * kPage + j % kPage;
-    float kv[E], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) kv[e] = load_kv<S>(a.pool.k, row * DH + lane + 32 * e);
-    for (int g = 0; g < G; ++g) {
-      const A* q = static_cast<const A*>(a.q) + static_cast<size_t>(b) * a.q_stride +
-                   (hk * G + g) * DH;
-      float z = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) z += to_f(q[lane + 32 * e]) * (a.scale * a.k_scale) * kv[e];
-#pragma unroll
-      for (int x = 16; x; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-      const float lse = a.lse_w[b * a.Hq + hk * G + g];
-      if (lse != -INFINITY) sum += __expf(z - lse);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int heads = a.Hkv * a.tiles;
+  // rows that attend nothing
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Span s = span_of(a, b, tid == 0);
+    if (s.pe > s.pf) continue;
+    for (int e = tid; e < a.Hq * DH; e += THREADS)
+      ActOf::put(a.out, static_cast<size_t>(b) * a.out_stride + e, 0.f, DT == PE_KV_F32);
+    for (int h = tid; h < a.Hq; h += THREADS) {
+      a.lse_w[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
+      if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
     }
-    if (lane == 0) atomicAdd(a.pool.scores + row, sum);
+  }
+  const Line ln = line_setup<THREADS>(a, heads, prefix, false);
+  const long long want = (ln.total + W * kMinPages - 1) / (W * kMinPages);
+  const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1LL)));
+  const long long c0 = blockIdx.x < grid ? ln.total * blockIdx.x / grid : 0;
+  const long long c1 = blockIdx.x < grid ? ln.total * (blockIdx.x + 1) / grid : 0;
+  if (c0 >= c1) {
+    if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, -1, 0);
+    return;
+  }
+  // the first `rest` warps take a page more; with less than a page for each,
+  // the last ones have none
+  const long long per = (c1 - c0) / W;
+  const int rest = static_cast<int>((c1 - c0) % W);
+  const long long u0 = c0 + per * w + min(w, rest), u1 = u0 + per + (w < rest ? 1 : 0);
+  const int working = per > 0 ? W : rest;
+  char* ring_p = smem + w * SH::RING;
+  char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
+  const uint32_t ring = smem_u32(ring_p);
+  float* my_last = reinterpret_cast<float*>(ring_p);
+  float* my_head = a.head + (static_cast<size_t>(blockIdx.x) * W + w) * 2 * SH::REC;
+  float* my_done = my_head + SH::REC;  // a complete item on its way out
+  // bits of w_state: 1 a first partial in the head record, 2 it is in the
+  // ring instead, 4 its item ends here, 8 a last partial in the ring
+  int state = 0;
+  if (u0 < u1) {
+    Place pl = place_of<THREADS>(a, ln, heads, prefix, u0);
+    Feeder<SH, DT, DH, true> feed;
+    feed.pl = pl;
+    feed.left = u1 - u0;
+    feed.ids_at = -1;
+    feed.ids = -1;
+    feed.stage = 0;
+    feed.bad = 0;
+#pragma unroll
+    for (int i = 0; i < SH::STAGES - 1; ++i) feed.step(a, heads, ring, lane, true);
+    long long left = u1 - u0;
+    int stage = 0;
+    Tile tile;
+    while (true) {
+      const bool began = pl.p == pl.s.pf;
+      const int hk = pl.hh / a.tiles, r0 = (pl.hh % a.tiles) * SH::ROWS;
+      tile.start(a, pl.b, hk * a.G + r0, min(SH::ROWS, a.G - r0), scratch, lane);
+      const int stop = static_cast<int>(min(static_cast<long long>(pl.s.pe), pl.p + left));
+      left -= stop - pl.p;
+      for (; pl.p < stop; ++pl.p) {
+        cp_async_wait<SH::STAGES - 2>();
+        __syncwarp();
+        const bool none = (feed.bad >> stage) & 1;
+        feed.step(a, heads, ring, lane, true);
+        const int first = pl.p * kPage;
+        tile.page(ring + stage * 2 * SH::PAGEB, none ? kPage : pl.s.lo - first, pl.s.n - first,
+                  scratch, lane);
+        if (++stage == SH::STAGES) stage = 0;
+      }
+      const bool ended = pl.p == pl.s.pe;
+      if (left > 0) {  // more items follow in this piece
+        if (began) {   // and this one is complete
+          tile.store(my_done, scratch, lane);
+          __syncwarp();
+          join_records<DT, DH, GT, false>(
+              a, pl.b, pl.hh, 1, [&](int) -> const float* { return my_done; }, nullptr, 0,
+              SH::ROWS, lane, 32);
+          __syncwarp();
+        } else {
+          tile.store(my_head, scratch, lane);
+          state |= 1 | 4;
+          if (lane == 0) {
+            w_b[w][0] = pl.b;
+            w_hh[w][0] = pl.hh;
+          }
+        }
+        next_item(a, heads, pl);
+        continue;
+      }
+      cp_async_wait<0>();
+      __syncwarp();
+      tile.store(my_last, scratch, lane);
+      __syncwarp();
+      if (began && ended) {
+        join_records<DT, DH, GT, false>(
+            a, pl.b, pl.hh, 1, [&](int) -> const float* { return my_last; }, nullptr, 0, SH::ROWS,
+            lane, 32);
+      } else {
+        if (!began) {
+          state |= 1 | 2 | (ended ? 4 : 0);
+          if (lane == 0) {
+            w_b[w][0] = pl.b;
+            w_hh[w][0] = pl.hh;
+          }
+        }
+        if (!ended) {
+          state |= 8;
+          if (lane == 0) {
+            w_b[w][1] = pl.b;
+            w_hh[w][1] = pl.hh;
+          }
+        }
+      }
+      break;
+    }
+  }
+  if (lane == 0) w_state[w] = state;
+  __syncthreads();
+  // chains of partials of one item: warps from .. to
+  int4 meta = make_int4(-1, 0, -1, 0);
+  int from = -1;       // first warp of the open chain, its part there: last (or first)
+  bool before = false; // the chain began before this CTA
+  auto rec = [&](int i) -> const float* {
+    // the i-th part of the chain: warp `from`'s last part (its first, if the
+    // chain began before the CTA), then the later warps' first parts
+    const int x = from + i;
+    const bool in_ring = (i == 0 && !before) || (w_state[x] & 2);
+    return in_ring ? reinterpret_cast<const float*>(smem + x * SH::RING)
+                   : a.head + (static_cast<size_t>(blockIdx.x) * W + x) * 2 * SH::REC;
+  };
+  float* part = a.part + static_cast<size_t>(blockIdx.x) * 2 * SH::REC;
+  for (int x = 0; x < working; ++x) {
+    const int st = w_state[x];
+    if (st & 1) {
+      if (from < 0) {
+        from = x;
+        before = true;
+        meta.x = w_b[x][0];
+        meta.y = w_hh[x][0];
+      }
+      if (st & 4) {
+        join_records<DT, DH, GT, false>(a, w_b[x][0], w_hh[x][0], x - from + 1, rec,
+                                 before ? part : nullptr, 0, SH::ROWS, tid, THREADS);
+        if (!before) meta.z = -1;  // it ended in this CTA
+        from = -1;
+        before = false;
+      }
+    }
+    if ((st & 8) && from < 0) {
+      from = x;
+      meta.z = w_b[x][1];
+      meta.w = w_hh[x][1];
+    }
+  }
+  if (from >= 0) {
+    if (before) {
+      meta.z = meta.x;
+      meta.w = meta.y | kWhole;
+    }
+    join_records<DT, DH, GT, false>(a, 0, 0, working - from, rec,
+                                    before ? part : part + SH::REC, 0, SH::ROWS, tid, THREADS);
+  }
+  if (tid == 0) a.meta[blockIdx.x] = meta;
+}
+
+// Items that several CTAs share: block c joins the one whose first part is
+// CTA c's last; blocks of y split the rows.
+template <int DT, int DH, int GT>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ DecodeArgs a) {
+  using SH = DecodeShape<DT, DH, GT>;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int c = blockIdx.x;
+  const int4 m = __ldcg(a.meta + c);
+  if (m.z < 0 || (m.w & kWhole)) return;
+  int count = 2;  // the CTAs after c whose first part is this item's
+  while (true) {
+    const int4 x = __ldcg(a.meta + c + count - 1);
+    if (!(x.z >= 0 && (x.w & kWhole))) break;
+    ++count;
+  }
+  const int rows = SH::ROWS / gridDim.y;
+  join_records<DT, DH, GT, true>(
+      a, m.z, m.w, count,
+      [&](int i) -> const float* {
+        return a.part + (static_cast<size_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * SH::REC;
+      },
+      nullptr, blockIdx.y * rows, (blockIdx.y + 1) * rows, threadIdx.x, 128);
+}
+
+// Weights: the logits of the pages once more, now that lse is known; a page
+// of a kv head belongs to one warp, which sums its query heads in order.
+template <int DT, int DH, int GT>
+__global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
+                                  DecodeShape<DT, DH, GT>::CTAS)
+    attn_scores_kernel(const __grid_constant__ DecodeArgs a) {
+  using SH = DecodeShape<DT, DH, GT>;
+  constexpr int W = SH::WARPS, THREADS = W * 32;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ long long prefix[THREADS];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  // here a head tile is a whole kv head
+  DecodeArgs one = a;
+  one.tiles = 1;
+  const Line ln = line_setup<THREADS>(one, a.Hkv, prefix, false);
+  const long long warps = static_cast<long long>(gridDim.x) * W;
+  const long long u0 = ln.total * (blockIdx.x * W + w) / warps;
+  const long long u1 = ln.total * (blockIdx.x * W + w + 1) / warps;
+  if (u0 >= u1) return;
+  char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
+  const uint32_t ring = smem_u32(smem + w * SH::RING);
+  Place pl = place_of<THREADS>(one, ln, a.Hkv, prefix, u0);
+  Feeder<SH, DT, DH, false> feed;
+  feed.pl = pl;
+  feed.left = u1 - u0;
+  feed.ids_at = -1;
+  feed.ids = -1;
+  feed.stage = 0;
+  feed.bad = 0;
+#pragma unroll
+  for (int i = 0; i < SH::STAGES - 1; ++i) feed.step(one, a.Hkv, ring, lane, false);
+  int stage = 0;
+  long long left = u1 - u0;
+  constexpr int LH = DT == PE_KV_F32 ? SH::ROWS / 4 : GT;  // heads a lane
+  int have = -1;  // head tile whose query and lse are loaded
+  typename TileOf<DT, DH, GT>::type tile;
+  float lse[LH];
+  while (left > 0) {
+    if (pl.p == pl.s.pe) {
+      next_item(one, a.Hkv, pl);
+      have = -1;
+    }
+    cp_async_wait<SH::STAGES - 2>();
+    __syncwarp();
+    const bool none = (feed.bad >> stage) & 1;
+    feed.step(one, a.Hkv, ring, lane, false);
+    const uint32_t at = ring + stage * 2 * SH::PAGEB;
+    // positions of this lane's logits
+    float sum[2][2] = {};
+    for (int ht = 0; ht < a.tiles; ++ht) {
+      const int r0 = ht * SH::ROWS, rows = min(SH::ROWS, a.G - r0), h0 = pl.hh * a.G + r0;
+      if (have != ht) {
+        tile.start(a, pl.b, h0, rows, scratch, lane);
+#pragma unroll
+        for (int x = 0; x < LH; ++x) {
+          const int r = DT == PE_KV_F32 ? t * LH + x : g + 8 * x;
+          lse[x] = r < rows ? __ldcg(a.lse_w + static_cast<size_t>(pl.b) * a.Hq + h0 + r) : -INFINITY;
+        }
+        have = ht;
+      }
+      if constexpr (DT == PE_KV_F32) {
+        float z[LH][2];
+        F32Tile<DH>::logits(at, scratch, lane, z);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float s = 0.f;
+#pragma unroll
+          for (int x = 0; x < LH; ++x)
+            s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j] - lse[x]);
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          sum[j][0] += s;
+        }
+      } else {
+        float z[GT][2][2];
+        tile.q.template logits<SH>(at, lane, z);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < GT; ++x)
+              s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j][e] - lse[x]);
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+            sum[j][e] += s;
+          }
+      }
+    }
+    const int blk = none ? -1
+                         : a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p];
+    const int first = pl.p * kPage;
+    if (!none) {
+      float* sc = a.pool.scores + (static_cast<size_t>(blk) * a.Hkv + pl.hh) * kPage;
+      if constexpr (DT == PE_KV_F32) {
+        if (t < 2) {
+          const int r = key_of(t, g);
+          if (first + r >= pl.s.lo && first + r < pl.s.n) atomicAdd(sc + r, t ? sum[1][0] : sum[0][0]);
+        }
+      } else if (g < 4) {
+        const int r = key_of(g >> 1, 2 * t + (g & 1));
+        const float v = g == 0 ? sum[0][0] : g == 1 ? sum[0][1] : g == 2 ? sum[1][0] : sum[1][1];
+        if (first + r >= pl.s.lo && first + r < pl.s.n) atomicAdd(sc + r, v);
+      }
+    }
+    ++pl.p;
+    --left;
+    if (++stage == SH::STAGES) stage = 0;
   }
 }
 
-template <typename A, typename S, int DH>
-static cudaError_t launch_decode(const DecodeArgs& a, bool accumulate, cudaStream_t s) {
-  cudaError_t e = launch_pdl(attn_decode_kernel<A, S, DH>, dim3(a.B * a.Hq), dim3(128), 0, s, a);
+// --------------------------------------------------------------- launchers
+
+static int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+template <int DT, int DH, int GT>
+static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate, cudaStream_t s) {
+  using SH = DecodeShape<DT, DH, GT>;
+  const int grid = sms * SH::CTAS;
+  a.tiles = (a.G + SH::ROWS - 1) / SH::ROWS;
+  a.lse_w = reinterpret_cast<float*>(ws);
+  ws += (static_cast<size_t>(a.B) * a.Hq * 4 + 15) / 16 * 16;
+  a.meta = reinterpret_cast<int4*>(ws);
+  ws += static_cast<size_t>(grid) * sizeof(int4);
+  a.part = reinterpret_cast<float*>(ws);
+  ws += static_cast<size_t>(grid) * 2 * SH::REC * 4;
+  a.head = reinterpret_cast<float*>(ws);
+  // per device and kernel, so set on every call (a host-side table write)
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DT, DH, GT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
   if (e == cudaSuccess && accumulate)
-    e = launch_pdl(attn_scores_kernel<A, S, DH>, dim3(a.B * a.Hkv, 16), dim3(128), 0, s, a);
-  return e;
+    e = cudaFuncSetAttribute(attn_scores_kernel<DT, DH, GT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
+  if (e == cudaSuccess)
+    e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(attn_join_kernel<DT, DH, GT>, dim3(grid, 4), dim3(128), 0, s, a);
+  if (e == cudaSuccess && accumulate)
+    e = launch_pdl(attn_scores_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
+  return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+}
+
+template <int DT, int DH>
+static pe_status launch_decode_heads(DecodeArgs& a, char* ws, int sms, bool accumulate,
+                                     cudaStream_t s) {
+  if constexpr (DT != PE_KV_F32)
+    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, sms, accumulate, s);
+  return launch_decode<DT, DH, 1>(a, ws, sms, accumulate, s);
 }
 
 }  // namespace pe
@@ -174,7 +1208,12 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
   if (B < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return (static_cast<int64_t>(B) * n_heads * 4 + 15) / 16 * 16;
+  const int64_t sms = pe::sm_count();
+  if (sms < 1) return 0;
+  // the largest of the pool types: two CTAs an SM, 8 or 16 rows a tile
+  const int64_t grid = 2 * sms, rows = n_heads / n_kv_heads > 8 ? 16 : 8;
+  return (static_cast<int64_t>(B) * n_heads * 4 + 15) / 16 * 16 + grid * 16 +
+         grid * (2 + 2 * pe::kMaxWarps) * rows * (head_dim + 2) * 4;
 }
 
 pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, float scale,
@@ -189,17 +1228,22 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   if (B < 1 || n_heads < 1 || n_heads % pool->n_kv_heads || !std::isfinite(scale) ||
       !block_table || bt_stride < 1 || !seq_lens || window < 0 || !row_ok(q, q_stride, qw, eb) ||
       !row_ok(out, out_stride, qw, eb) || (accumulate && !pool->scores) || !workspace ||
-      !is_aligned16(workspace) ||
-      workspace_bytes < pe_attn_decode_workspace(B, n_heads, pool->n_kv_heads, dh))
+      !is_aligned16(workspace) || workspace_bytes <= 0)
     return PE_ERR_INVALID_ARGUMENT;
+  const int64_t need = pe_attn_decode_workspace(B, n_heads, pool->n_kv_heads, dh);
+  if (need == 0) return PE_ERR_CUDA;
+  if (workspace_bytes < need) return PE_ERR_INVALID_ARGUMENT;
   DecodeArgs a = {};
   a.pool = CachePool{pool->k, pool->v, pool->scores, pool->num_blocks};
   a.B = B;
   a.Hq = n_heads;
   a.Hkv = pool->n_kv_heads;
+  a.G = n_heads / pool->n_kv_heads;
   a.bt_stride = bt_stride;
   a.window = window;
-  a.scale = scale;
+  const bool codes = pool->dtype == PE_KV_E4M3;
+  a.scale = scale * kLog2e * (codes ? pool->k_scale : 1.f);
+  a.v_scale = codes ? pool->v_scale : 1.f;
   a.q = q;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
@@ -207,24 +1251,19 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   a.seq_lens = seq_lens;
   a.out = out;
   a.lse = lse;
-  a.lse_w = static_cast<float*>(workspace);
   a.err = err;
-  const bool codes = pool->dtype == PE_KV_E4M3;
-  a.k_scale = codes ? pool->k_scale : 1.f;
-  a.v_scale = codes ? pool->v_scale : 1.f;
+  char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = sm_count();
   const bool acc = accumulate != 0;
-  cudaError_t e;
   if (pool->dtype == PE_KV_F32)
-    e = dh == 64 ? launch_decode<float, float, 64>(a, acc, s)
-                 : launch_decode<float, float, 128>(a, acc, s);
-  else if (pool->dtype == PE_KV_BF16)
-    e = dh == 64 ? launch_decode<bf16, bf16, 64>(a, acc, s)
-                 : launch_decode<bf16, bf16, 128>(a, acc, s);
-  else
-    e = dh == 64 ? launch_decode<bf16, uint8_t, 64>(a, acc, s)
-                 : launch_decode<bf16, uint8_t, 128>(a, acc, s);
-  return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, sms, acc, s)
+                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, sms, acc, s);
+  if (pool->dtype == PE_KV_BF16)
+    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, sms, acc, s)
+                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, sms, acc, s);
+  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, sms, acc, s)
+                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, sms, acc, s);
 }
 
 }  // extern "C"
