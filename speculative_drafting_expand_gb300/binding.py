@@ -505,6 +505,8 @@ class KvPool:
         if any(t is not None and t.device != k.device for t in (v, scores)):
             raise ValueError("k, v and scores must be on one device")
         self.k, self.v, self.scores, self.device = k, v, scores, k.device
+        self.torch, self.i32 = torch, torch.int32
+        self._workspace = {}         # sizes by (requests, query heads)
         self.num_blocks, self.n_kv_heads, _, self.head_dim = k.shape
         self.dtype = kinds[k.dtype]
         self.act_dtype = torch.float32 if self.dtype == PE_KV_F32 else torch.bfloat16
@@ -516,29 +518,28 @@ class KvPool:
 def _cache_rows(pool: KvPool, name: str, t, rows: int, heads: int) -> int:
     """Row stride (elements) of a [rows, heads, head_dim] tensor whose heads
     are contiguous."""
-    if t.shape != (rows, heads, pool.head_dim) or t.dtype != pool.act_dtype:
-        raise ValueError(f"{name} must be {pool.act_dtype} [{rows}, {heads}, {pool.head_dim}]")
+    dh = pool.head_dim
+    if t.dtype != pool.act_dtype or t.shape != (rows, heads, dh):
+        raise ValueError(f"{name} must be {pool.act_dtype} [{rows}, {heads}, {dh}]")
     row, head, one = t.stride()
-    if one != 1 or (head != pool.head_dim and heads > 1):
+    if one != 1 or (head != dh and heads > 1):
         raise ValueError(f"{name} must have contiguous heads")
     if t.device != pool.device:
         raise ValueError(f"{name} must be on the pool's device")
-    return row if rows > 1 else heads * pool.head_dim
+    return row if rows > 1 else heads * dh
 
 
-def _cache_i32(device, name: str, t, shape) -> None:
-    torch = _torch()
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device}")
+def _cache_i32(pool: KvPool, name: str, t, shape) -> None:
+    if (t.dtype != pool.i32 or t.shape != shape or not t.is_contiguous()
+            or t.device != pool.device):
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {pool.device}")
 
 
-def _cache_table(device, name: str, t, B: int) -> int:
-    torch = _torch()
-    if (t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or t.device != device
-            or (t.shape[1] > 1 and t.stride(1) != 1)):
-        raise ValueError(f"{name} must be int32 [{B}, pages] with contiguous rows on {device}")
-    # a row's length is its stride: entries between rows belong to no request
-    if B > 1 and t.stride(0) != t.shape[1]:
+def _cache_table(pool: KvPool, name: str, t, B: int) -> int:
+    if t.dtype != pool.i32 or t.dim() != 2 or t.shape[0] != B or t.device != pool.device:
+        raise ValueError(f"{name} must be int32 [{B}, pages] on {pool.device}")
+    # the library takes a row's length as its stride
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.shape[1]
 
@@ -550,18 +551,31 @@ def _cache_ints(**values) -> None:
             raise ValueError(f"{name} must be a 32-bit integer")
 
 
-def _cache_call(device, stream, name, fn, *args) -> None:
-    """Call into the library with `device` current; `stream` None is that
-    device's current stream."""
-    torch = _torch()
+def _cache_empty(pool: KvPool, shape, dtype, stream):
+    """Memory for a call on `stream`, from that stream's share of the
+    allocator: what other streams still do with freed memory cannot meet it."""
+    torch = pool.torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=pool.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=pool.device)
+
+
+def _cache_call(pool: KvPool, stream, name, fn, *args) -> None:
+    """Call into the library with the pool's device current; `stream` None is
+    that device's current stream."""
+    torch = pool.torch
+    device = pool.device
     if device.type != "cuda":
         raise ValueError(f"{name} needs tensors on a GPU")
-    s = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     if torch.cuda.current_device() == device.index:
-        _check(name, fn(*args, s))
+        status = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(name, fn(*args, s))
+            status = fn(*args, s)
+    if status != PE_OK:
+        raise PeError(name, status)
 
 
 def pe_kv_append(pool: KvPool, q, k, v, pos, block_table, rope_theta: float = 0.0, req=None,
@@ -573,25 +587,22 @@ def pe_kv_append(pool: KvPool, q, k, v, pos, block_table, rope_theta: float = 0.
     T, B = k.shape[0], block_table.shape[0]
     ks = _cache_rows(pool, "k", k, T, pool.n_kv_heads)
     vs = _cache_rows(pool, "v", v, T, pool.n_kv_heads)
-    dev = pool.device
-    _cache_i32(dev, "pos", pos, (T,))
+    _cache_i32(pool, "pos", pos, (T,))
     if req is not None:
-        _cache_i32(dev, "req", req, (T,))
-    pages = _cache_table(dev, "block_table", block_table, B)
+        _cache_i32(pool, "req", req, (T,))
+    pages = _cache_table(pool, "block_table", block_table, B)
     n_heads = qs = qos = 0
     if q is not None:
         n_heads = q.shape[1]
         qs = _cache_rows(pool, "q", q, T, n_heads)
         if q_out is None:
-            q_out = _torch().empty((T, n_heads, pool.head_dim), dtype=q.dtype, device=dev)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = _cache_empty(pool, (T, n_heads, pool.head_dim), q.dtype, stream)
         qos = _cache_rows(pool, "q_out", q_out, T, n_heads)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if err is not None:
-        _cache_i32(dev, "err", err, (1,))
-    _cache_call(dev, stream, "pe_kv_append", lib().pe_kv_append, pool._ref, T, B, n_heads,
+        _cache_i32(pool, "err", err, (1,))
+    _cache_call(pool, stream, "pe_kv_append", lib().pe_kv_append, pool._ref, T, B, n_heads,
                 rope_theta, ptr(q), qs, ptr(k), ks, ptr(v), vs, ptr(pos), ptr(req),
                 ptr(block_table), pages, ptr(q_out), qos, ptr(err))
     return q_out
@@ -614,37 +625,33 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
     to pool.scores.  Returns out and lse [B, n_heads] float32 (made when
     None).  The workspace (uint8, pe_attn_decode_workspace bytes) is allocated
     for the call when None."""
-    torch = _torch()
+    torch = pool.torch
     _cache_ints(window=window)
     B, n_heads = q.shape[0], q.shape[1]
     dev, dh = pool.device, pool.head_dim
     qs = _cache_rows(pool, "q", q, B, n_heads)
-    pages = _cache_table(dev, "block_table", block_table, B)
-    _cache_i32(dev, "seq_lens", seq_lens, (B,))
-    made = []
+    pages = _cache_table(pool, "block_table", block_table, B)
+    _cache_i32(pool, "seq_lens", seq_lens, (B,))
     if out is None:
-        out = torch.empty((B, n_heads, dh), dtype=q.dtype, device=dev)
-        made.append(out)
+        out = _cache_empty(pool, (B, n_heads, dh), q.dtype, stream)
     if lse is None:
-        lse = torch.empty((B, n_heads), dtype=torch.float32, device=dev)
-        made.append(lse)
+        lse = _cache_empty(pool, (B, n_heads), torch.float32, stream)
     elif (lse.dtype != torch.float32 or lse.shape != (B, n_heads) or not lse.is_contiguous()
           or lse.device != dev):
         raise ValueError(f"lse must be contiguous float32 [{B}, {n_heads}]")
     os_ = _cache_rows(pool, "out", out, B, n_heads)
     if workspace is None:
-        with torch.cuda.device(dev):
-            n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        n = pool._workspace.get((B, n_heads))
+        if n is None:
+            with torch.cuda.device(dev):
+                n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh)
+            pool._workspace[B, n_heads] = n
+        workspace = _cache_empty(pool, n, torch.uint8, stream)
     elif not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError("workspace must be contiguous on the pool's device")
     if err is not None:
-        _cache_i32(dev, "err", err, (1,))
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
-    _cache_call(dev, stream, "pe_attn_decode", lib().pe_attn_decode, pool._ref, B, n_heads,
+        _cache_i32(pool, "err", err, (1,))
+    _cache_call(pool, stream, "pe_attn_decode", lib().pe_attn_decode, pool._ref, B, n_heads,
                 dh ** -0.5 if scale is None else scale, ptr(q), qs, ptr(block_table), pages,
                 ptr(seq_lens), window, ptr(out), os_, ptr(lse), int(accumulate), ptr(workspace),
                 workspace.numel() * workspace.element_size(), ptr(err))
@@ -659,35 +666,30 @@ def pe_kv_evict(pools: Sequence[KvPool], block_table, seq_lens, budget: int, sin
     pool.scores, per layer (one pool each) and kv head.  In place, or into
     the pages of dst_table.  Returns kept [layers, B, n_kv_heads, budget] and
     new_lens [B], int32 (made when None)."""
-    torch = _torch()
     pools = list(pools)
     if not pools:
         raise ValueError("no pools")
     _cache_ints(budget=budget, sinks=sinks, recent=recent)
     p0, B = pools[0], block_table.shape[0]
-    dev = p0.device
+    dev, torch = p0.device, p0.torch
     if any(p.device != dev for p in pools):
         raise ValueError("the pools must be on one device")
-    pages = _cache_table(dev, "block_table", block_table, B)
-    _cache_i32(dev, "seq_lens", seq_lens, (B,))
-    dst_pages = _cache_table(dev, "dst_table", dst_table, B) if dst_table is not None else 0
+    pages = _cache_table(p0, "block_table", block_table, B)
+    _cache_i32(p0, "seq_lens", seq_lens, (B,))
+    dst_pages = _cache_table(p0, "dst_table", dst_table, B) if dst_table is not None else 0
     shape = (len(pools), B, p0.n_kv_heads, budget)
     if budget < 1:
         raise ValueError("budget must be positive")
     if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
-        if stream is not None:
-            kept.record_stream(stream)
-    _cache_i32(dev, "kept", kept, shape)
+        kept = _cache_empty(p0, shape, torch.int32, stream)
+    _cache_i32(p0, "kept", kept, shape)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        if stream is not None:
-            new_lens.record_stream(stream)
-    _cache_i32(dev, "new_lens", new_lens, (B,))
+        new_lens = _cache_empty(p0, B, torch.int32, stream)
+    _cache_i32(p0, "new_lens", new_lens, (B,))
     if err is not None:
-        _cache_i32(dev, "err", err, (1,))
+        _cache_i32(p0, "err", err, (1,))
     arr = (pe_kv_pool * len(pools))(*[p.struct for p in pools])
-    _cache_call(dev, stream, "pe_kv_evict", lib().pe_kv_evict, len(pools), arr, B,
+    _cache_call(p0, stream, "pe_kv_evict", lib().pe_kv_evict, len(pools), arr, B,
                 ptr(block_table), pages, ptr(seq_lens), budget, sinks, recent, rope_theta,
                 ptr(dst_table), dst_pages, ptr(kept), ptr(new_lens), ptr(err))
     return kept, new_lens

@@ -44,6 +44,7 @@ namespace pe {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxWarps = 8;  // warps a CTA
+constexpr int kMostCtas = 512;  // so that the join of an item over all of them fits
 constexpr int kMinPages = 2;  // pages a warp, where there are fewer than the grid could take
 
 // ------------------------------------------------------------------ shapes
@@ -84,7 +85,7 @@ struct DecodeArgs {
   float* lse_w;    // [B, Hq], in units of ln 2
   int4* meta;      // [grid]: item and flags of the CTA's first and last partial
   float* part;     // [grid][2][REC]
-  float* head;     // [grid * WARPS][2][REC]
+  float* head;     // [grid * WARPS][REC]
 };
 
 // A request's positions and pages: lo..n-1 attended, pages pf..pe-1.
@@ -145,6 +146,24 @@ __device__ __forceinline__ Line line_setup(const DecodeArgs& a, int heads, long 
   return ln;
 }
 
+// Part i of `total` pages in n equal parts, the first ones a page longer
+// (i >= n: nothing).
+struct Share {
+  long long first, count;
+};
+__device__ __forceinline__ Share share_of(long long total, int n, int i) {
+  long long per, rest;
+  if (total >> 31) {
+    per = total / n;
+    rest = total % n;
+  } else {
+    per = static_cast<uint32_t>(total) / static_cast<uint32_t>(n);
+    rest = static_cast<uint32_t>(total) % static_cast<uint32_t>(n);
+  }
+  if (i >= n) return Share{0, 0};
+  return Share{per * i + min(static_cast<long long>(i), rest), per + (i < rest ? 1 : 0)};
+}
+
 // A place on the line: page p of head tile hh of request b.
 struct Place {
   int b, hh;
@@ -168,8 +187,14 @@ __device__ __forceinline__ Place place_of(const DecodeArgs& a, const Line& ln, i
     left -= static_cast<long long>(pl.s.pe - pl.s.pf) * heads;
     pl.s = span_of(a, ++pl.b, false);
   }
-  pl.hh = static_cast<int>(left / (pl.s.pe - pl.s.pf));
-  pl.p = pl.s.pf + static_cast<int>(left % (pl.s.pe - pl.s.pf));
+  const uint32_t np = pl.s.pe - pl.s.pf;
+  if (left >> 31) {
+    pl.hh = static_cast<int>(left / np);
+    pl.p = pl.s.pf + static_cast<int>(left % np);
+  } else {
+    pl.hh = static_cast<int>(static_cast<uint32_t>(left) / np);
+    pl.p = pl.s.pf + static_cast<int>(static_cast<uint32_t>(left) % np);
+  }
   return pl;
 }
 // The first page of the next item (there is one).
@@ -293,6 +318,28 @@ struct Feeder {
     if (++stage == SH::STAGES) stage = 0;
   }
 };
+
+// Writes a row's lse (units of ln 2 in, natural out) and returns what its sum
+// of p v is multiplied by; a row without weight gives 0 and -inf.
+__device__ __forceinline__ float put_lse(const DecodeArgs& a, int b, int h, float m, float l,
+                                         bool write) {
+  const bool none = m == -INFINITY && l == 0.f;
+  if (write) {
+    const float s = none ? -INFINITY : m + log2f(l);
+    const size_t at = static_cast<size_t>(b) * a.Hq + h;
+    a.lse_w[at] = s;
+    if (a.lse) a.lse[at] = s * kLn2;
+  }
+  return none ? 0.f : a.v_scale / l;
+}
+template <int DT>
+__device__ __forceinline__ void put4(void* out, size_t at, float4 v) {
+  if constexpr (DT == PE_KV_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<bf16*>(out) + at) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
 
 // ------------------------------------------------------------ 16 and 8 bits
 
@@ -554,20 +601,26 @@ struct MmaTile {
     }
   }
 
-  // Element of the rows that tile i, column n holds.
+  // Element of the rows that tile i, column n holds: eight tiles hold eight
+  // elements in a row.
   static __device__ __forceinline__ int elem(int i, int n) {
     if constexpr (DT == PE_KV_BF16) return (n + 8 * (i >> 3)) * 8 + (i & 7);
     else return n * NT + i;
   }
+  __device__ __forceinline__ float value(int x, int i, int e) const {
+    return GT == 1 ? o[i][e] + o[i][2 + e] : o[i][2 * x + e];
+  }
+  __device__ __forceinline__ float sum_l(int x) const {
+    float s = l[x] + __shfl_xor_sync(0xffffffffu, l[x], 1);
+    return s + __shfl_xor_sync(0xffffffffu, s, 2);
+  }
 
   // The partial result as a record: m[ROWS], l[ROWS], O[ROWS][DH].
-  __device__ __forceinline__ void store(float* rec, char*, int lane) {
+  __device__ __forceinline__ void store(float* rec, int lane) const {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int x = 0; x < GT; ++x) {
-      float s = l[x];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      const float s = sum_l(x);
       const int r = g + 8 * x;
       if (t == 0) {
         rec[r] = m[x];
@@ -577,8 +630,36 @@ struct MmaTile {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          row[elem(i, 2 * t + e)] = GT == 1 ? o[i][e] + o[i][2 + e] : o[i][2 * x + e];
+        for (int i = 0; i < NT; i += 4)
+          *reinterpret_cast<float4*>(row + elem(i, 2 * t + e)) =
+              make_float4(value(x, i, e), value(x, i + 1, e), value(x, i + 2, e),
+                          value(x, i + 3, e));
+    }
+  }
+
+  // A complete item's result.
+  __device__ __forceinline__ void finish(const DecodeArgs& A, int b, int h0, int rows,
+                                         int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < GT; ++x) {
+      const float s = sum_l(x);
+      const int r = g + 8 * x;
+      if (r >= rows) continue;
+      const float inv = put_lse(A, b, h0 + r, m[x], s, t == 0);
+      bf16* row = static_cast<bf16*>(A.out) + static_cast<size_t>(b) * A.out_stride +
+                  static_cast<size_t>(h0 + r) * DH;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < NT; i += 8) {
+          uint4 v;
+          v.x = pack_bf16x2(value(x, i, e) * inv, value(x, i + 1, e) * inv);
+          v.y = pack_bf16x2(value(x, i + 2, e) * inv, value(x, i + 3, e) * inv);
+          v.z = pack_bf16x2(value(x, i + 4, e) * inv, value(x, i + 5, e) * inv);
+          v.w = pack_bf16x2(value(x, i + 6, e) * inv, value(x, i + 7, e) * inv);
+          *reinterpret_cast<uint4*>(row + elem(i, 2 * t + e)) = v;
+        }
     }
   }
 };
@@ -737,13 +818,30 @@ struct F32Tile {
     __syncwarp();  // p is rewritten by the next page
   }
 
-  __device__ __forceinline__ void store(float* rec, char*, int lane) {
+  __device__ __forceinline__ float sum_l(int x) const {
+    float s = l[x];
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    return s;
+  }
+  // The four lanes of a chunk hold its positions' parts; lane c % 4 ends with
+  // the sum.
+  __device__ __forceinline__ float4 value(int h, int c) const {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = o[h][c][e];
+      v[e] += __shfl_xor_sync(0xffffffffu, v[e], 1);
+      v[e] += __shfl_xor_sync(0xffffffffu, v[e], 2);
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+
+  __device__ __forceinline__ void store(float* rec, int lane) const {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int x = 0; x < R / 4; ++x) {
-      float s = l[x];
-#pragma unroll
-      for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      const float s = sum_l(x);
       if (g == 0) {
         rec[t * (R / 4) + x] = m[x];
         rec[R + t * (R / 4) + x] = s;
@@ -753,17 +851,34 @@ struct F32Tile {
     for (int h = 0; h < R; ++h)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = o[h][c][e];
-          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 1);
-          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 2);
-        }
-        if (t == (c & 3))
-#pragma unroll
-          for (int e = 0; e < 4; ++e) rec[2 * R + h * DH + (g + 8 * c) * 4 + e] = v[e];
+        const float4 v = value(h, c);
+        if (t == (c & 3)) *reinterpret_cast<float4*>(rec + 2 * R + h * DH + (g + 8 * c) * 4) = v;
       }
+  }
+
+  __device__ __forceinline__ void finish(const DecodeArgs& A, int b, int h0, int rows,
+                                         int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+    float inv[R / 4];
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x) {
+      const float s = sum_l(x);
+      const int r = t * (R / 4) + x;
+      inv[x] = r < rows ? put_lse(A, b, h0 + r, m[x], s, g == 0) : 0.f;
+    }
+    float* out = static_cast<float*>(A.out) + static_cast<size_t>(b) * A.out_stride +
+                 static_cast<size_t>(h0) * DH;
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const float f = __shfl_sync(0xffffffffu, inv[h % (R / 4)], h / (R / 4));
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float4 v = value(h, c);
+        if (t == (c & 3) && h < rows)
+          *reinterpret_cast<float4*>(out + h * DH + (g + 8 * c) * 4) =
+              make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      }
+    }
   }
 };
 
@@ -778,65 +893,45 @@ struct TileOf<PE_KV_F32, DH, GT> {
 
 // ----------------------------------------------------------------- results
 
-struct ActOf {
-  static __device__ __forceinline__ void put(void* out, size_t at, float x, bool f32) {
-    if (f32) static_cast<float*>(out)[at] = x;
-    else static_cast<bf16*>(out)[at] = __float2bfloat16_rn(x);
-  }
-};
-
-// Joins `count` records (rec(i), in the order of the positions) into a
-// finished item or into `dst`, over the threads first, first + step, ...
-// Rows row0 .. row1 - 1 of the tile.  GLOBAL: another CTA wrote the records;
-// else this one did, in shared or global memory.
-template <bool GLOBAL>
-__device__ __forceinline__ float ld_part(const float* p) {
-  if (GLOBAL) return __ldcg(p);
-  return *static_cast<const volatile float*>(p);
-}
-template <int DT, int DH, int GT, bool GLOBAL, typename Rec>
-__device__ __forceinline__ void join_records(const DecodeArgs& a, int b, int hh, int count, Rec rec,
-                                             float* dst, int row0, int row1, int first, int step) {
+// Joins the parts of one item inside a CTA, rec(0) .. rec(count - 1) in the
+// order of the positions, into the result or into `dst`.
+template <int DT, int DH, int GT, typename Rec>
+__device__ __forceinline__ void join_in_cta(const DecodeArgs& a, int b, int hh, int count, Rec rec,
+                                            float* dst, int threads) {
   using SH = DecodeShape<DT, DH, GT>;
-  const int hk = hh / a.tiles, h0 = hk * a.G + (hh % a.tiles) * SH::ROWS;
+  const int h0 = hh / a.tiles * a.G + (hh % a.tiles) * SH::ROWS;
   const int rows = min(SH::ROWS, a.G - (hh % a.tiles) * SH::ROWS);
-  for (int e = row0 * DH + first; e < row1 * DH; e += step) {
+  for (int e = threadIdx.x * 4; e < SH::ROWS * DH; e += threads * 4) {
     const int r = e / DH, d = e % DH;
     float M = -INFINITY;
-    for (int i = 0; i < count; ++i) M = fmaxf(M, ld_part<GLOBAL>(rec(i) + r));
+    for (int i = 0; i < count; ++i) M = fmaxf(M, rec(i)[r]);
     const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, O = 0.f;
-#pragma unroll 4
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < count; ++i) {
       const float* p = rec(i);
-      const float c = fast_exp2(ld_part<GLOBAL>(p + r) - base);
-      L = fmaf(c, ld_part<GLOBAL>(p + SH::ROWS + r), L);
-      O = fmaf(c, ld_part<GLOBAL>(p + 2 * SH::ROWS + e), O);
+      const float c = fast_exp2(p[r] - base);
+      const float4 v = *reinterpret_cast<const float4*>(p + 2 * SH::ROWS + e);
+      L = fmaf(c, p[SH::ROWS + r], L);
+      O = make_float4(fmaf(c, v.x, O.x), fmaf(c, v.y, O.y), fmaf(c, v.z, O.z), fmaf(c, v.w, O.w));
     }
     if (dst) {
-      dst[2 * SH::ROWS + e] = O;
+      *reinterpret_cast<float4*>(dst + 2 * SH::ROWS + e) = O;
       if (d == 0) {
         dst[r] = M;
         dst[SH::ROWS + r] = L;
       }
     } else if (r < rows) {
-      const bool none = M == -INFINITY && !(L != L);
-      ActOf::put(a.out, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(h0 + r) * DH + d,
-                 none ? 0.f : O * (a.v_scale / L), DT == PE_KV_F32);
-      if (d == 0) {
-        const float s = none ? -INFINITY : M + log2f(L);
-        a.lse_w[static_cast<size_t>(b) * a.Hq + h0 + r] = s;
-        if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h0 + r] = s * kLn2;
-      }
+      const float f = put_lse(a, b, h0 + r, M, L, d == 0);
+      put4<DT>(a.out, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(h0 + r) * DH + d,
+               make_float4(O.x * f, O.y * f, O.z * f, O.w * f));
     }
   }
 }
 
-// A CTA's meta word pair: .x, .y the first partial's item (request, head
-// tile) when it began before the CTA, else -1; .z, .w the last partial's that
-// goes on after it (request and head tile).  An item that covers the whole
-// CTA is first and last: kWhole in .w.
-constexpr int kWhole = 1 << 30;
+// A CTA's meta: of its last part, if that item began in the CTA and goes on
+// after it, the request (.x, else -1), the head tile (.y) and the number of
+// CTAs that have parts of it (.z).
 
 template <int DT, int DH, int GT>
 __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
@@ -849,6 +944,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   __shared__ long long prefix[THREADS];
   // a warp's partials: first (began before its piece), last (goes on after)
   __shared__ int w_state[W], w_b[W][2], w_hh[W][2];
+  __shared__ int after;  // pages of the CTA's last item that lie after it
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -857,34 +953,31 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Span s = span_of(a, b, tid == 0);
     if (s.pe > s.pf) continue;
-    for (int e = tid; e < a.Hq * DH; e += THREADS)
-      ActOf::put(a.out, static_cast<size_t>(b) * a.out_stride + e, 0.f, DT == PE_KV_F32);
+    for (int e = tid * 4; e < a.Hq * DH; e += THREADS * 4)
+      put4<DT>(a.out, static_cast<size_t>(b) * a.out_stride + e, make_float4(0.f, 0.f, 0.f, 0.f));
     for (int h = tid; h < a.Hq; h += THREADS) {
       a.lse_w[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
       if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
     }
   }
   const Line ln = line_setup<THREADS>(a, heads, prefix, false);
+  // CTAs and warps take whole pages, the first ones one more; with few pages,
+  // kMinPages a warp on fewer CTAs
   const long long want = (ln.total + W * kMinPages - 1) / (W * kMinPages);
-  const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1LL)));
-  const long long c0 = blockIdx.x < grid ? ln.total * blockIdx.x / grid : 0;
-  const long long c1 = blockIdx.x < grid ? ln.total * (blockIdx.x + 1) / grid : 0;
-  if (c0 >= c1) {
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, -1, 0);
+  const int grid = want < gridDim.x ? max(static_cast<int>(want), 1) : gridDim.x;
+  const Share cta = share_of(ln.total, grid, blockIdx.x);
+  if (cta.count == 0) {
+    if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // the first `rest` warps take a page more; with less than a page for each,
-  // the last ones have none
-  const long long per = (c1 - c0) / W;
-  const int rest = static_cast<int>((c1 - c0) % W);
-  const long long u0 = c0 + per * w + min(w, rest), u1 = u0 + per + (w < rest ? 1 : 0);
-  const int working = per > 0 ? W : rest;
+  const Share mine = share_of(cta.count, W, w);
+  const long long u0 = cta.first + mine.first, u1 = u0 + mine.count;
+  const int working = cta.count < W ? static_cast<int>(cta.count) : W;
   char* ring_p = smem + w * SH::RING;
   char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
   const uint32_t ring = smem_u32(ring_p);
   float* my_last = reinterpret_cast<float*>(ring_p);
-  float* my_head = a.head + (static_cast<size_t>(blockIdx.x) * W + w) * 2 * SH::REC;
-  float* my_done = my_head + SH::REC;  // a complete item on its way out
+  float* my_head = a.head + (static_cast<size_t>(blockIdx.x) * W + w) * SH::REC;
   // bits of w_state: 1 a first partial in the head record, 2 it is in the
   // ring instead, 4 its item ends here, 8 a last partial in the ring
   int state = 0;
@@ -905,7 +998,8 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
     while (true) {
       const bool began = pl.p == pl.s.pf;
       const int hk = pl.hh / a.tiles, r0 = (pl.hh % a.tiles) * SH::ROWS;
-      tile.start(a, pl.b, hk * a.G + r0, min(SH::ROWS, a.G - r0), scratch, lane);
+      const int rows = min(SH::ROWS, a.G - r0);
+      tile.start(a, pl.b, hk * a.G + r0, rows, scratch, lane);
       const int stop = static_cast<int>(min(static_cast<long long>(pl.s.pe), pl.p + left));
       left -= stop - pl.p;
       for (; pl.p < stop; ++pl.p) {
@@ -921,14 +1015,9 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
       const bool ended = pl.p == pl.s.pe;
       if (left > 0) {  // more items follow in this piece
         if (began) {   // and this one is complete
-          tile.store(my_done, scratch, lane);
-          __syncwarp();
-          join_records<DT, DH, GT, false>(
-              a, pl.b, pl.hh, 1, [&](int) -> const float* { return my_done; }, nullptr, 0,
-              SH::ROWS, lane, 32);
-          __syncwarp();
+          tile.finish(a, pl.b, hk * a.G + r0, rows, lane);
         } else {
-          tile.store(my_head, scratch, lane);
+          tile.store(my_head, lane);
           state |= 1 | 4;
           if (lane == 0) {
             w_b[w][0] = pl.b;
@@ -940,13 +1029,11 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
       }
       cp_async_wait<0>();
       __syncwarp();
-      tile.store(my_last, scratch, lane);
-      __syncwarp();
       if (began && ended) {
-        join_records<DT, DH, GT, false>(
-            a, pl.b, pl.hh, 1, [&](int) -> const float* { return my_last; }, nullptr, 0, SH::ROWS,
-            lane, 32);
+        tile.finish(a, pl.b, hk * a.G + r0, rows, lane);
       } else {
+        tile.store(my_last, lane);
+        if (w == working - 1 && lane == 0) after = pl.s.pe - pl.p;
         if (!began) {
           state |= 1 | 2 | (ended ? 4 : 0);
           if (lane == 0) {
@@ -967,17 +1054,17 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   }
   if (lane == 0) w_state[w] = state;
   __syncthreads();
-  // chains of partials of one item: warps from .. to
-  int4 meta = make_int4(-1, 0, -1, 0);
-  int from = -1;       // first warp of the open chain, its part there: last (or first)
-  bool before = false; // the chain began before this CTA
+  // chains of parts of one item: the warps from `from` on
+  int4 meta = make_int4(-1, 0, 0, 0);
+  int from = -1;        // first warp of the open chain, its part there: last (or first)
+  bool before = false;  // the chain began before this CTA
   auto rec = [&](int i) -> const float* {
     // the i-th part of the chain: warp `from`'s last part (its first, if the
     // chain began before the CTA), then the later warps' first parts
     const int x = from + i;
     const bool in_ring = (i == 0 && !before) || (w_state[x] & 2);
     return in_ring ? reinterpret_cast<const float*>(smem + x * SH::RING)
-                   : a.head + (static_cast<size_t>(blockIdx.x) * W + x) * 2 * SH::REC;
+                   : a.head + (static_cast<size_t>(blockIdx.x) * W + x) * SH::REC;
   };
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 2 * SH::REC;
   for (int x = 0; x < working; ++x) {
@@ -986,57 +1073,116 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
       if (from < 0) {
         from = x;
         before = true;
-        meta.x = w_b[x][0];
-        meta.y = w_hh[x][0];
       }
       if (st & 4) {
-        join_records<DT, DH, GT, false>(a, w_b[x][0], w_hh[x][0], x - from + 1, rec,
-                                 before ? part : nullptr, 0, SH::ROWS, tid, THREADS);
-        if (!before) meta.z = -1;  // it ended in this CTA
+        join_in_cta<DT, DH, GT>(a, w_b[x][0], w_hh[x][0], x - from + 1, rec,
+                                before ? part : nullptr, THREADS);
         from = -1;
         before = false;
       }
     }
-    if ((st & 8) && from < 0) {
-      from = x;
-      meta.z = w_b[x][1];
-      meta.w = w_hh[x][1];
-    }
+    if ((st & 8) && from < 0) from = x;
   }
   if (from >= 0) {
-    if (before) {
-      meta.z = meta.x;
-      meta.w = meta.y | kWhole;
+    join_in_cta<DT, DH, GT>(a, 0, 0, working - from, rec, before ? part : part + SH::REC, THREADS);
+    if (!before) {
+      // how many of the next CTAs the rest of the item reaches
+      meta.x = w_b[from][1];
+      meta.y = w_hh[from][1];
+      const Share next = share_of(ln.total, grid, min(static_cast<int>(blockIdx.x) + 1, grid - 1));
+      const Share last = share_of(ln.total, grid, grid - 1);
+      meta.z = 2;
+      long long rest = after - next.count;
+      if (rest > 0) {
+        // parts of next.count pages up to the first shorter one
+        const long long wide = next.count > last.count
+                                   ? ln.total - last.count * grid - (blockIdx.x + 2)
+                                   : 0;  // further CTAs with next.count pages
+        const long long of_wide = min(wide, (rest + next.count - 1) / next.count);
+        rest -= of_wide * next.count;
+        meta.z += static_cast<int>(of_wide);
+        if (rest > 0) meta.z += static_cast<int>((rest + last.count - 1) / last.count);
+      }
     }
-    join_records<DT, DH, GT, false>(a, 0, 0, working - from, rec,
-                                    before ? part : part + SH::REC, 0, SH::ROWS, tid, THREADS);
   }
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }
 
 // Items that several CTAs share: block c joins the one whose first part is
-// CTA c's last; blocks of y split the rows.
+// CTA c's last; blocks of y take a share of the rows.  The parts' m and l come
+// in at once, then the products with every part's load in flight together.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 4;  // blocks of y
 template <int DT, int DH, int GT>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
+    const __grid_constant__ DecodeArgs a) {
   using SH = DecodeShape<DT, DH, GT>;
+  constexpr int R = SH::ROWS / kJoinRows;          // rows of this block
+  constexpr int LANES = R * DH / 4;                // threads that hold the row's elements
+  constexpr int WAYS = kJoinThreads / LANES;       // parts taken side by side
+  constexpr int MOST = kMostCtas;
+  __shared__ float wt[MOST][R], red[2][R];
+  __shared__ float4 side[WAYS > 1 ? WAYS : 1][LANES];
   grid_dep_wait();
   grid_dep_launch();
-  const int c = blockIdx.x;
-  const int4 m = __ldcg(a.meta + c);
-  if (m.z < 0 || (m.w & kWhole)) return;
-  int count = 2;  // the CTAs after c whose first part is this item's
-  while (true) {
-    const int4 x = __ldcg(a.meta + c + count - 1);
-    if (!(x.z >= 0 && (x.w & kWhole))) break;
-    ++count;
+  const int c = blockIdx.x, row0 = blockIdx.y * R;
+  const int4 meta = __ldcg(a.meta + c);
+  if (meta.x < 0) return;
+  const int b = meta.x, hh = meta.y, count = min(meta.z, MOST);
+  auto rec = [&](int i) -> const float* {
+    return a.part + (static_cast<size_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * SH::REC;
+  };
+  const int tid = threadIdx.x;
+  for (int k = tid; k < count * R; k += kJoinThreads)
+    wt[k / R][k % R] = __ldcg(rec(k / R) + row0 + k % R);
+  __syncthreads();
+  // a warp a row: the maximum, then the weights and the sum
+  for (int r = tid >> 5; r < R; r += kJoinThreads / 32) {
+    const int lane = tid & 31;
+    float M = -INFINITY;
+    for (int i = lane; i < count; i += 32) M = fmaxf(M, wt[i][r]);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int i = lane; i < count; i += 32) {
+      const float x = fast_exp2(wt[i][r] - base);
+      L = fmaf(x, __ldcg(rec(i) + SH::ROWS + row0 + r), L);
+      wt[i][r] = x;
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+    if (lane == 0) {
+      red[0][r] = M;
+      red[1][r] = L;
+    }
   }
-  const int rows = SH::ROWS / gridDim.y;
-  join_records<DT, DH, GT, true>(
-      a, m.z, m.w, count,
-      [&](int i) -> const float* {
-        return a.part + (static_cast<size_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * SH::REC;
-      },
-      nullptr, blockIdx.y * rows, (blockIdx.y + 1) * rows, threadIdx.x, 128);
+  __syncthreads();
+  const int way = tid / LANES, e = (tid % LANES) * 4, r = e / DH;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = way; i < count; i += WAYS) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(rec(i) + 2 * SH::ROWS + row0 * DH + e));
+    const float x = wt[i][r];
+    O = make_float4(fmaf(x, v.x, O.x), fmaf(x, v.y, O.y), fmaf(x, v.z, O.z), fmaf(x, v.w, O.w));
+  }
+  if (WAYS > 1) {
+    side[way][tid % LANES] = O;
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int k = 1; k < WAYS; ++k) {
+      const float4 v = side[k][tid];
+      O = make_float4(O.x + v.x, O.y + v.y, O.z + v.z, O.w + v.w);
+    }
+  }
+  const int h0 = hh / a.tiles * a.G + (hh % a.tiles) * SH::ROWS;
+  const int rows = min(SH::ROWS, a.G - (hh % a.tiles) * SH::ROWS);
+  if (row0 + r >= rows) return;
+  const float f = put_lse(a, b, h0 + row0 + r, red[0][r], red[1][r], e % DH == 0);
+  put4<DT>(a.out,
+           static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(h0 + row0 + r) * DH + e % DH,
+           make_float4(O.x * f, O.y * f, O.z * f, O.w * f));
 }
 
 // Weights: the logits of the pages once more, now that lse is known; a page
@@ -1167,7 +1313,7 @@ static int sm_count() {
 template <int DT, int DH, int GT>
 static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate, cudaStream_t s) {
   using SH = DecodeShape<DT, DH, GT>;
-  const int grid = sms * SH::CTAS;
+  const int grid = std::min(sms * SH::CTAS, kMostCtas);
   a.tiles = (a.G + SH::ROWS - 1) / SH::ROWS;
   a.lse_w = reinterpret_cast<float*>(ws);
   ws += (static_cast<size_t>(a.B) * a.Hq * 4 + 15) / 16 * 16;
@@ -1185,7 +1331,7 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate
   if (e == cudaSuccess)
     e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
   if (e == cudaSuccess)
-    e = launch_pdl(attn_join_kernel<DT, DH, GT>, dim3(grid, 4), dim3(128), 0, s, a);
+    e = launch_pdl(attn_join_kernel<DT, DH, GT>, dim3(grid, kJoinRows), dim3(kJoinThreads), 0, s, a);
   if (e == cudaSuccess && accumulate)
     e = launch_pdl(attn_scores_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
@@ -1213,7 +1359,7 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
   // the largest of the pool types: two CTAs an SM, 8 or 16 rows a tile
   const int64_t grid = 2 * sms, rows = n_heads / n_kv_heads > 8 ? 16 : 8;
   return (static_cast<int64_t>(B) * n_heads * 4 + 15) / 16 * 16 + grid * 16 +
-         grid * (2 + 2 * pe::kMaxWarps) * rows * (head_dim + 2) * 4;
+         grid * (2 + pe::kMaxWarps) * rows * (head_dim + 2) * 4;
 }
 
 pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, float scale,
