@@ -35,6 +35,7 @@
 // e4m3 pools go through fp16, which holds every code; q is scaled there by a
 // power of two to [1, 2) so that fp16's range does not matter.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache_common.cuh"
 #include "pe_kernels.h"
@@ -59,12 +60,19 @@ struct DecodeShape {
   // what the registers of the fp32 path hold
   static constexpr int ROWS = DT == PE_KV_F32 ? (DH == 64 ? 8 : 4) : 8 * GT;
   static constexpr int WARPS = DT == PE_KV_F32 && DH == 128 ? 4 : 8;
-  static constexpr int STAGES = DT == PE_KV_E4M3 ? 6 : 3;
+  static constexpr int TAKE = DT == PE_KV_F32 ? 1 : 2;  // pages at a time
+  static constexpr int STAGES =                          // pages in the ring
+      DT == PE_KV_F32 ? 3 : PAGEB == 4096 ? 3 : 6;
   static constexpr int RING = STAGES * 2 * PAGEB;  // a warp's ring
   static constexpr int REC = ROWS * (DH + 2);      // a partial result, floats: m, l, O
   static constexpr int SCRATCH = DT == PE_KV_F32 ? (ROWS * DH + kPage * ROWS + ROWS) * 4 : 0;
   static constexpr int SMEM = WARPS * (RING + SCRATCH);
-  static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;  // a SM
+  static constexpr int CTAS = DT == PE_KV_E4M3 && DH == 64 ? 2 : 1;  // a SM
+  // the scores' kernel: K alone, two CTAs an SM
+  static constexpr int S_TAKE = DT == PE_KV_F32 ? 1 : 2;
+  static constexpr int S_STAGES = PAGEB == 1024 ? 8 : PAGEB == 2048 ? 6 : 3;
+  static constexpr int S_RING = S_STAGES * PAGEB;
+  static constexpr int S_SMEM = WARPS * (S_RING + SCRATCH);
   static_assert(REC * 4 <= RING, "a warp leaves its last partial in its ring");
 };
 
@@ -233,56 +241,50 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-// Lane (g = lane / 4, t = lane % 4).  K: rows key_of(j, g), j = 0, 1, elements
-// of chunks t + 4 i.  V: rows t + 4 i, chunks g + 8 i.  key_of() is the order
-// of the positions along the logits' columns: column n of half j.
+// Lane (g = lane / 4, t = lane % 4) reads, of K, chunks t + 4 i of rows
+// key_of(j, g), j = 0, 1, and of V chunks g + 8 i of rows t + 4 i'.  key_of()
+// is the order of the positions along the logits' columns: column n of half
+// j.  A page lies in the ring in its own order, but for the 16-byte chunks of
+// a row, whose places are exchanged such that the eight lanes that read
+// together meet all banks.
 __device__ __forceinline__ int key_of(int j, int n) { return 8 * j + (n >> 1) + 4 * (n & 1); }
 
-template <class SH, int DT, int DH, bool WITH_V>
+template <class SH>
+__device__ __forceinline__ uint32_t k_place(int r, int c) {
+  // rows of 64 bytes: two to the 128 bytes of all banks
+  if constexpr (SH::ROWB == 64) return static_cast<uint32_t>(((r * 4 + c) ^ (r & 4)) * 16);
+  else return static_cast<uint32_t>(r * SH::ROWB + (c ^ (r & 4)) * 16);
+}
+template <class SH>
+__device__ __forceinline__ uint32_t v_place(int r, int c) {
+  if constexpr (SH::ROWB == 64) return static_cast<uint32_t>(r * 64 + (c ^ (r & 2)) * 16);
+  else return static_cast<uint32_t>(r * SH::ROWB + (c ^ ((r & 3) << 1)) * 16);
+}
+
+// 32 lanes copy 512 bytes in a row at a time.
+template <class SH, bool WITH_V>
 __device__ __forceinline__ void copy_page(uint32_t stage, const CachePool& pool, int blk, int Hkv,
                                           int hk, int v_lo, int v_hi, int lane) {
   // positions v_lo <= offset < v_hi of the page are attended; the others
   // read as zeros whatever lies there
-  const int g = lane >> 2, t = lane & 3;
-  const size_t base = (static_cast<size_t>(blk) * Hkv + hk) * SH::PAGEB;
+  constexpr int CPR = SH::ROWB / 16;  // chunks a row
+  const size_t base = (static_cast<size_t>(blk) * Hkv + hk) * SH::PAGEB + lane * 16;
   const char* kp = static_cast<const char*>(pool.k) + base;
-  constexpr int KI = SH::CH / 2;  // chunks a row and lane
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = key_of(j, g);
-    const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
-#pragma unroll
-    for (int i = 0; i < KI; ++i)
-      cp_async16(stage + ((j * KI + i) * 32 + lane) * 16, kp + r * SH::ROWB + (t + 4 * i) * 16, n);
-  }
-  if (!WITH_V) return;
   const char* vp = static_cast<const char*>(pool.v) + base;
-  stage += SH::PAGEB;
-  if constexpr (DT == PE_KV_E4M3 && DH == 64) {
-    // rows of 64 bytes, 8 a lane: the page as it lies, shared by the lanes
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      cp_async16(stage + (i * 32 + lane) * 16, vp + (i * 32 + lane) * 16,
-                 r >= v_lo && r < v_hi ? 16u : 0u);
-    }
-  } else {
-    constexpr int VI = SH::CH / 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = t + 4 * i;
-      const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
-#pragma unroll
-      for (int c = 0; c < VI; ++c)
-        cp_async16(stage + ((i * VI + c) * 32 + lane) * 16, vp + r * SH::ROWB + (g + 8 * c) * 16,
-                   n);
-    }
+  for (int i = 0; i < SH::CH; ++i) {
+    const int r = (i * 32 + lane) / CPR, c = lane % CPR;
+    const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
+    cp_async16(stage + k_place<SH>(r, c), kp + i * 512, n);
+    if (WITH_V) cp_async16(stage + SH::PAGEB + v_place<SH>(r, c), vp + i * 512, n);
   }
 }
 
 // The copying side of a warp: pages of the line in order, a commit each.
-template <class SH, int DT, int DH, bool WITH_V>
+template <class SH, bool WITH_V>
 struct Feeder {
+  static constexpr int STAGES = WITH_V ? SH::STAGES : SH::S_STAGES;
+  static constexpr int STRIDE = WITH_V ? 2 * SH::PAGEB : SH::PAGEB;
   Place pl;
   long long left;  // units still to copy
   int ids;         // this lane's page of the 32 from ids_at on
@@ -290,8 +292,9 @@ struct Feeder {
   int stage;
   uint32_t bad;    // stages whose page is none
 
-  __device__ __forceinline__ void step(const DecodeArgs& a, int heads, uint32_t ring, int lane,
-                                       bool record) {
+  // heads: items a request; tiles: items a kv head
+  __device__ __forceinline__ void step(const DecodeArgs& a, int heads, int tiles, uint32_t ring,
+                                       int lane, bool record) {
     if (left > 0) {
       if (pl.p == pl.s.pe) {
         next_item(a, heads, pl);
@@ -308,14 +311,14 @@ struct Feeder {
       if (!ok && record && lane == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
       bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
       const int first = pl.p * kPage;
-      copy_page<SH, DT, DH, WITH_V>(ring + stage * 2 * SH::PAGEB, a.pool, ok ? blk : 0, a.Hkv,
-                                    pl.hh / a.tiles, ok ? pl.s.lo - first : kPage,
+      copy_page<SH, WITH_V>(ring + stage * STRIDE, a.pool, ok ? blk : 0, a.Hkv,
+                                    pl.hh / tiles, ok ? pl.s.lo - first : kPage,
                                     ok ? pl.s.n - first : 0, lane);
       ++pl.p;
       --left;
     }
     cp_async_commit();
-    if (++stage == SH::STAGES) stage = 0;
+    if (++stage == STAGES) stage = 0;
   }
 };
 
@@ -347,14 +350,12 @@ template <int DT>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (DT == PE_KV_BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -441,7 +442,7 @@ struct QueryTile {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        const uint4 v = lds16(stage + ((j * KI + i) * 32 + lane) * 16);
+        const uint4 v = lds16(stage + k_place<SH>(key_of(j, lane >> 2), (lane & 3) + 4 * i));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if constexpr (DT == PE_KV_BF16) {
 #pragma unroll
@@ -488,26 +489,37 @@ struct MmaTile {
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   }
 
-  __device__ __forceinline__ void page(uint32_t stage, int v_lo, int v_hi, char*, int lane) {
+  // NP pages in a row, at `stage`; positions v_lo <= i < v_hi of them are
+  // attended, and bit n of `none` takes out page n.
+  template <int NP>
+  __device__ __forceinline__ void pages(const uint32_t (&stage)[NP], int v_lo, int v_hi,
+                                        uint32_t none, char*, int lane) {
     const int t = lane & 3;
-    float z[GT][2][2];
-    q.template logits<SH>(stage, lane, z);
-    if (v_lo > 0 || v_hi < kPage) {
+    float z[NP][GT][2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int n = 0; n < NP; ++n) q.template logits<SH>(stage[n], lane, z[n]);
+    if (v_lo > 0 || v_hi < NP * kPage || none) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = key_of(j, 2 * t + e);
-          if (r < v_lo || r >= v_hi)
+      for (int n = 0; n < NP; ++n)
 #pragma unroll
-            for (int x = 0; x < GT; ++x) z[x][j][e] = -INFINITY;
-        }
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = n * kPage + key_of(j, 2 * t + e);
+            if (r < v_lo || r >= v_hi || ((none >> n) & 1))
+#pragma unroll
+              for (int x = 0; x < GT; ++x) z[n][x][j][e] = -INFINITY;
+          }
     }
     float top[GT];
     bool grow = false;
 #pragma unroll
     for (int x = 0; x < GT; ++x) {
-      top[x] = fmaxf(fmaxf(z[x][0][0], z[x][0][1]), fmaxf(z[x][1][0], z[x][1][1]));
+      top[x] = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        top[x] = fmax3(top[x], fmaxf(z[n][x][0][0], z[n][x][0][1]),
+                       fmaxf(z[n][x][1][0], z[n][x][1][1]));
       top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
       top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
       grow |= top[x] > m[x];
@@ -529,17 +541,26 @@ struct MmaTile {
         o[i][3] *= c[GT - 1];
       }
     }
-    uint32_t hi[GT][2], lo[GT][2];
+    uint32_t hi[NP][GT][2], lo[NP][GT][2];
 #pragma unroll
     for (int x = 0; x < GT; ++x) {
       const float base = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float p0 = fast_exp2(z[x][j][0] - base), p1 = fast_exp2(z[x][j][1] - base);
-        l[x] += p0 + p1;
-        split2<DT>(p0, p1, hi[x][j], lo[x][j]);
-      }
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float p0 = fast_exp2(z[n][x][j][0] - base), p1 = fast_exp2(z[n][x][j][1] - base);
+          l[x] += p0 + p1;
+          split2<DT>(p0, p1, hi[n][x][j], lo[n][x][j]);
+        }
     }
+#pragma unroll
+    for (int n = 0; n < NP; ++n) add_values(stage[n] + SH::PAGEB, hi[n], lo[n], lane);
+  }
+
+  // O += P V of a page
+  __device__ __forceinline__ void add_values(uint32_t vs, const uint32_t (&hi)[GT][2],
+                                             const uint32_t (&lo)[GT][2], int lane) {
     auto pv = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
       if constexpr (GT == 1) {
         mma16816<DT>(c, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
@@ -548,39 +569,40 @@ struct MmaTile {
         mma16816<DT>(c, lo[0][0], lo[1][0], lo[0][1], lo[1][1], b0, b1);
       }
     };
-    const uint32_t vs = stage + SH::PAGEB;
     if constexpr (DT == PE_KV_BF16) {
 #pragma unroll
       for (int c = 0; c < DH / 64; ++c) {
-        constexpr int VI = SH::CH / 4;
-        uint4 r[4];
+        uint32_t w[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = lds16(vs + ((i * VI + c) * 32 + lane) * 16);
-        const uint32_t* w0 = &r[0].x;
-        const uint32_t* w1 = &r[1].x;
-        const uint32_t* w2 = &r[2].x;
-        const uint32_t* w3 = &r[3].x;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = lds16(vs + v_place<SH>((lane & 3) + 4 * i, (lane >> 2) + 8 * c));
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+          w[i][2] = u.z;
+          w[i][3] = u.w;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          pv(o[8 * c + 2 * k], __byte_perm(w0[k], w1[k], 0x5410), __byte_perm(w2[k], w3[k], 0x5410));
-          pv(o[8 * c + 2 * k + 1], __byte_perm(w0[k], w1[k], 0x7632),
-             __byte_perm(w2[k], w3[k], 0x7632));
+          pv(o[8 * c + 2 * k], __byte_perm(w[0][k], w[1][k], 0x5410),
+             __byte_perm(w[2][k], w[3][k], 0x5410));
+          pv(o[8 * c + 2 * k + 1], __byte_perm(w[0][k], w[1][k], 0x7632),
+             __byte_perm(w[2][k], w[3][k], 0x7632));
         }
       }
     } else {
       uint32_t w[4][DH / 32];
       if constexpr (DH == 64) {
-        const int g = lane >> 2;
+        const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint2 u = lds8(vs + (t + 4 * i) * 64 + g * 8);
+          const uint2 u = lds8(vs + v_place<SH>(t + 4 * i, g >> 1) + (g & 1) * 8);
           w[i][0] = u.x;
           w[i][1] = u.y;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 u = lds16(vs + (i * 32 + lane) * 16);
+          const uint4 u = lds16(vs + v_place<SH>((lane & 3) + 4 * i, lane >> 2));
           w[i][0] = u.x;
           w[i][1] = u.y;
           w[i][DH / 32 - 2] = u.z;
@@ -711,7 +733,7 @@ struct F32Tile {
       float4 k[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint4 v = lds16(stage + ((j * KI + i) * 32 + lane) * 16);
+        const uint4 v = lds16(stage + k_place<SH>(key_of(j, lane >> 2), t + 4 * i));
         k[j] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                            __uint_as_float(v.w));
       }
@@ -742,8 +764,12 @@ struct F32Tile {
       }
   }
 
-  __device__ __forceinline__ void page(uint32_t stage, int v_lo, int v_hi, char* scratch,
-                                       int lane) {
+  template <int NP>
+  __device__ __forceinline__ void pages(const uint32_t (&at)[NP], int v_lo, int v_hi,
+                                        uint32_t none, char* scratch, int lane) {
+    static_assert(NP == 1, "one page at a time");
+    const uint32_t stage = at[0];
+    if (none) v_lo = kPage;
     float* p = reinterpret_cast<float*>(scratch) + R * DH;
     float* cs = p + kPage * R;
     const int g = lane >> 2, t = lane & 3;
@@ -805,7 +831,7 @@ struct F32Tile {
             *reinterpret_cast<const float4*>(p + (t + 4 * i) * R + h);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint4 v = lds16(vs + ((i * C + c) * 32 + lane) * 16);
+        const uint4 v = lds16(vs + v_place<SH>(t + 4 * i, g + 8 * c));
 #pragma unroll
         for (int h = 0; h < R; ++h) {
           o[h][c][0] = fmaf(w[h], __uint_as_float(v.x), o[h][c][0]);
@@ -983,15 +1009,15 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   int state = 0;
   if (u0 < u1) {
     Place pl = place_of<THREADS>(a, ln, heads, prefix, u0);
-    Feeder<SH, DT, DH, true> feed;
+    Feeder<SH, true> feed;
     feed.pl = pl;
     feed.left = u1 - u0;
     feed.ids_at = -1;
     feed.ids = -1;
     feed.stage = 0;
     feed.bad = 0;
-#pragma unroll
-    for (int i = 0; i < SH::STAGES - 1; ++i) feed.step(a, heads, ring, lane, true);
+#pragma unroll 1
+    for (int i = 0; i < SH::STAGES; ++i) feed.step(a, heads, a.tiles, ring, lane, true);
     long long left = u1 - u0;
     int stage = 0;
     Tile tile;
@@ -1002,16 +1028,27 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
       tile.start(a, pl.b, hk * a.G + r0, rows, scratch, lane);
       const int stop = static_cast<int>(min(static_cast<long long>(pl.s.pe), pl.p + left));
       left -= stop - pl.p;
-      for (; pl.p < stop; ++pl.p) {
-        cp_async_wait<SH::STAGES - 2>();
-        __syncwarp();
-        const bool none = (feed.bad >> stage) & 1;
-        feed.step(a, heads, ring, lane, true);
+      auto take = [&](auto count) {
+        constexpr int NP = decltype(count)::value;
+        cp_async_wait<SH::STAGES - NP>();
+        __syncwarp();  // other lanes' copies, and their reads of the pages before
+        uint32_t at[NP], none = 0;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          at[n] = ring + stage * 2 * SH::PAGEB;
+          none |= ((feed.bad >> stage) & 1) << n;
+          if (++stage == SH::STAGES) stage = 0;
+        }
         const int first = pl.p * kPage;
-        tile.page(ring + stage * 2 * SH::PAGEB, none ? kPage : pl.s.lo - first, pl.s.n - first,
-                  scratch, lane);
-        if (++stage == SH::STAGES) stage = 0;
-      }
+        tile.template pages<NP>(at, pl.s.lo - first, pl.s.n - first, none, scratch, lane);
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < NP; ++n) feed.step(a, heads, a.tiles, ring, lane, true);
+        pl.p += NP;
+      };
+      if constexpr (SH::TAKE > 1)
+        while (pl.p + SH::TAKE <= stop) take(std::integral_constant<int, SH::TAKE>());
+      while (pl.p < stop) take(std::integral_constant<int, 1>());
       const bool ended = pl.p == pl.s.pe;
       if (left > 0) {  // more items follow in this piece
         if (began) {   // and this one is complete
@@ -1188,10 +1225,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
 // Weights: the logits of the pages once more, now that lse is known; a page
 // of a kv head belongs to one warp, which sums its query heads in order.
 template <int DT, int DH, int GT>
-__global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
-                                  DecodeShape<DT, DH, GT>::CTAS)
+__global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
     attn_scores_kernel(const __grid_constant__ DecodeArgs a) {
   using SH = DecodeShape<DT, DH, GT>;
+  using Feed = Feeder<SH, false>;
   constexpr int W = SH::WARPS, THREADS = W * 32;
   extern __shared__ __align__(128) char smem[];
   __shared__ long long prefix[THREADS];
@@ -1199,44 +1236,42 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  // here a head tile is a whole kv head
-  DecodeArgs one = a;
-  one.tiles = 1;
-  const Line ln = line_setup<THREADS>(one, a.Hkv, prefix, false);
-  const long long warps = static_cast<long long>(gridDim.x) * W;
-  const long long u0 = ln.total * (blockIdx.x * W + w) / warps;
-  const long long u1 = ln.total * (blockIdx.x * W + w + 1) / warps;
-  if (u0 >= u1) return;
-  char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
-  const uint32_t ring = smem_u32(smem + w * SH::RING);
-  Place pl = place_of<THREADS>(one, ln, a.Hkv, prefix, u0);
-  Feeder<SH, DT, DH, false> feed;
+  const Line ln = line_setup<THREADS>(a, a.Hkv, prefix, false);
+  const Share mine = share_of(ln.total, gridDim.x * W, blockIdx.x * W + w);
+  if (mine.count == 0) return;
+  char* scratch = smem + W * SH::S_RING + w * SH::SCRATCH;
+  const uint32_t ring = smem_u32(smem + w * SH::S_RING);
+  Place pl = place_of<THREADS>(a, ln, a.Hkv, prefix, mine.first);
+  Feed feed;
   feed.pl = pl;
-  feed.left = u1 - u0;
+  feed.left = mine.count;
   feed.ids_at = -1;
   feed.ids = -1;
   feed.stage = 0;
   feed.bad = 0;
-#pragma unroll
-  for (int i = 0; i < SH::STAGES - 1; ++i) feed.step(one, a.Hkv, ring, lane, false);
+#pragma unroll 1
+  for (int i = 0; i < Feed::STAGES; ++i) feed.step(a, a.Hkv, 1, ring, lane, false);
   int stage = 0;
-  long long left = u1 - u0;
+  long long left = mine.count;
   constexpr int LH = DT == PE_KV_F32 ? SH::ROWS / 4 : GT;  // heads a lane
   int have = -1;  // head tile whose query and lse are loaded
   typename TileOf<DT, DH, GT>::type tile;
   float lse[LH];
-  while (left > 0) {
-    if (pl.p == pl.s.pe) {
-      next_item(one, a.Hkv, pl);
-      have = -1;
-    }
-    cp_async_wait<SH::STAGES - 2>();
+  auto take = [&](auto count) {
+    constexpr int NP = decltype(count)::value;
+    cp_async_wait<Feed::STAGES - NP>();
     __syncwarp();
-    const bool none = (feed.bad >> stage) & 1;
-    feed.step(one, a.Hkv, ring, lane, false);
-    const uint32_t at = ring + stage * 2 * SH::PAGEB;
-    // positions of this lane's logits
-    float sum[2][2] = {};
+    uint32_t at[NP], none = 0;
+    int blk[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      at[n] = ring + stage * Feed::STRIDE;
+      const bool bad = (feed.bad >> stage) & 1;
+      none |= (bad ? 1u : 0u) << n;
+      blk[n] = bad ? 0 : a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + n];
+      if (++stage == Feed::STAGES) stage = 0;
+    }
+    float sum[NP][2][2] = {};
     for (int ht = 0; ht < a.tiles; ++ht) {
       const int r0 = ht * SH::ROWS, rows = min(SH::ROWS, a.G - r0), h0 = pl.hh * a.G + r0;
       if (have != ht) {
@@ -1244,13 +1279,15 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
 #pragma unroll
         for (int x = 0; x < LH; ++x) {
           const int r = DT == PE_KV_F32 ? t * LH + x : g + 8 * x;
-          lse[x] = r < rows ? __ldcg(a.lse_w + static_cast<size_t>(pl.b) * a.Hq + h0 + r) : -INFINITY;
+          // a row without weight, or no row
+          lse[x] = -INFINITY;
+          if (r < rows) lse[x] = __ldcg(a.lse_w + static_cast<size_t>(pl.b) * a.Hq + h0 + r);
         }
         have = ht;
       }
       if constexpr (DT == PE_KV_F32) {
         float z[LH][2];
-        F32Tile<DH>::logits(at, scratch, lane, z);
+        F32Tile<DH>::logits(at[0], scratch, lane, z);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float s = 0.f;
@@ -1259,44 +1296,55 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
             s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j] - lse[x]);
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
-          sum[j][0] += s;
+          sum[0][j][0] += s;
         }
       } else {
-        float z[GT][2][2];
-        tile.q.template logits<SH>(at, lane, z);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int n = 0; n < NP; ++n) {
+          float z[GT][2][2];
+          tile.q.template logits<SH>(at[n], lane, z);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float s = 0.f;
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int x = 0; x < GT; ++x)
-              s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j][e] - lse[x]);
+            for (int e = 0; e < 2; ++e) {
+              float s = 0.f;
 #pragma unroll
-            for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-            sum[j][e] += s;
-          }
-      }
-    }
-    const int blk = none ? -1
-                         : a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p];
-    const int first = pl.p * kPage;
-    if (!none) {
-      float* sc = a.pool.scores + (static_cast<size_t>(blk) * a.Hkv + pl.hh) * kPage;
-      if constexpr (DT == PE_KV_F32) {
-        if (t < 2) {
-          const int r = key_of(t, g);
-          if (first + r >= pl.s.lo && first + r < pl.s.n) atomicAdd(sc + r, t ? sum[1][0] : sum[0][0]);
+              for (int x = 0; x < GT; ++x)
+                s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j][e] - lse[x]);
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+              sum[n][j][e] += s;
+            }
         }
-      } else if (g < 4) {
-        const int r = key_of(g >> 1, 2 * t + (g & 1));
-        const float v = g == 0 ? sum[0][0] : g == 1 ? sum[0][1] : g == 2 ? sum[1][0] : sum[1][1];
-        if (first + r >= pl.s.lo && first + r < pl.s.n) atomicAdd(sc + r, v);
       }
     }
-    ++pl.p;
-    --left;
-    if (++stage == SH::STAGES) stage = 0;
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NP; ++n) feed.step(a, a.Hkv, 1, ring, lane, false);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int first = (pl.p + n) * kPage;
+      float* sc = a.pool.scores + (static_cast<size_t>(blk[n]) * a.Hkv + pl.hh) * kPage;
+      // four lanes hold a position's sum; one of them adds it
+      const int r = DT == PE_KV_F32 ? key_of(t & 1, g) : key_of((g >> 1) & 1, 2 * t + (g & 1));
+      const float v = DT == PE_KV_F32 ? (t & 1 ? sum[n][1][0] : sum[n][0][0])
+                      : g & 2         ? (g & 1 ? sum[n][1][1] : sum[n][1][0])
+                                      : (g & 1 ? sum[n][0][1] : sum[n][0][0]);
+      const bool mine_to_add = DT == PE_KV_F32 ? t < 2 : g < 4;
+      if (mine_to_add && !((none >> n) & 1) && first + r >= pl.s.lo && first + r < pl.s.n)
+        atomicAdd(sc + r, v);
+    }
+    pl.p += NP;
+    left -= NP;
+  };
+  while (left > 0) {
+    if (pl.p == pl.s.pe) {
+      next_item(a, a.Hkv, pl);
+      have = -1;
+    }
+    const int run = static_cast<int>(min(static_cast<long long>(pl.s.pe - pl.p), left));
+    if (SH::S_TAKE > 1 && run >= SH::S_TAKE) take(std::integral_constant<int, SH::S_TAKE>());
+    else take(std::integral_constant<int, 1>());
   }
 }
 
@@ -1327,13 +1375,14 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
   if (e == cudaSuccess && accumulate)
     e = cudaFuncSetAttribute(attn_scores_kernel<DT, DH, GT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::S_SMEM);
   if (e == cudaSuccess)
     e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
   if (e == cudaSuccess)
     e = launch_pdl(attn_join_kernel<DT, DH, GT>, dim3(grid, kJoinRows), dim3(kJoinThreads), 0, s, a);
   if (e == cudaSuccess && accumulate)
-    e = launch_pdl(attn_scores_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
+    e = launch_pdl(attn_scores_kernel<DT, DH, GT>, dim3(2 * sms), dim3(SH::WARPS * 32), SH::S_SMEM,
+                   s, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
 
