@@ -118,7 +118,9 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * PE_ERR_INVALID_ARGUMENT: B < 1, window < 0, scale not finite, n_heads not
  * a positive multiple of n_kv_heads, accumulate without pool->scores, a
  * stride shorter than a row, a null or misaligned pointer, a short
- * workspace.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128. */
+ * workspace.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128, or B *
+ * bt_stride * n_heads past 2^31 - 1.  An attended v of +-inf gives +-inf or
+ * NaN. */
 pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, float scale,
                          const void* q, int64_t q_stride, const int32_t* block_table,
                          int32_t bt_stride, const int32_t* seq_lens, int32_t window, void* out,

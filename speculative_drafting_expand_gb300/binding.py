@@ -505,7 +505,8 @@ class KvPool:
         if any(t is not None and t.device != k.device for t in (v, scores)):
             raise ValueError("k, v and scores must be on one device")
         self.k, self.v, self.scores, self.device = k, v, scores, k.device
-        self.torch, self.i32 = torch, torch.int32
+        self.torch, self.i32, self.lib = torch, torch.int32, lib()
+        self.index = k.get_device()  # -1: not on a GPU
         self._workspace = {}         # sizes by (requests, query heads)
         self.num_blocks, self.n_kv_heads, _, self.head_dim = k.shape
         self.dtype = kinds[k.dtype]
@@ -519,29 +520,29 @@ def _cache_rows(pool: KvPool, name: str, t, rows: int, heads: int) -> int:
     """Row stride (elements) of a [rows, heads, head_dim] tensor whose heads
     are contiguous."""
     dh = pool.head_dim
-    if t.dtype != pool.act_dtype or t.shape != (rows, heads, dh):
+    if t.dtype is not pool.act_dtype or t.shape != (rows, heads, dh):
         raise ValueError(f"{name} must be {pool.act_dtype} [{rows}, {heads}, {dh}]")
     row, head, one = t.stride()
     if one != 1 or (head != dh and heads > 1):
         raise ValueError(f"{name} must have contiguous heads")
-    if t.device != pool.device:
+    if t.get_device() != pool.index:
         raise ValueError(f"{name} must be on the pool's device")
     return row if rows > 1 else heads * dh
 
 
 def _cache_i32(pool: KvPool, name: str, t, shape) -> None:
-    if (t.dtype != pool.i32 or t.shape != shape or not t.is_contiguous()
-            or t.device != pool.device):
+    if (t.dtype is not pool.i32 or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != pool.index):
         raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {pool.device}")
 
 
 def _cache_table(pool: KvPool, name: str, t, B: int) -> int:
-    if t.dtype != pool.i32 or t.dim() != 2 or t.shape[0] != B or t.device != pool.device:
-        raise ValueError(f"{name} must be int32 [{B}, pages] on {pool.device}")
-    # the library takes a row's length as its stride
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.shape[1]
+    # contiguous: the library takes a row's length as its stride
+    shape = t.shape
+    if (t.dtype is not pool.i32 or len(shape) != 2 or shape[0] != B or not t.is_contiguous()
+            or t.get_device() != pool.index):
+        raise ValueError(f"{name} must be contiguous int32 [{B}, pages] on {pool.device}")
+    return shape[1]
 
 
 def _cache_ints(**values) -> None:
@@ -564,15 +565,16 @@ def _cache_empty(pool: KvPool, shape, dtype, stream):
 def _cache_call(pool: KvPool, stream, name, fn, *args) -> None:
     """Call into the library with the pool's device current; `stream` None is
     that device's current stream."""
-    torch = pool.torch
-    device = pool.device
-    if device.type != "cuda":
+    index = pool.index
+    if index < 0:
         raise ValueError(f"{name} needs tensors on a GPU")
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    # the raw handles behind torch.cuda.current_stream() and current_device()
+    C = pool.torch._C
+    s = C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if C._cuda_getDevice() == index:
         status = fn(*args, s)
     else:
-        with torch.cuda.device(device):
+        with pool.torch.cuda.device(index):
             status = fn(*args, s)
     if status != PE_OK:
         raise PeError(name, status)
@@ -602,7 +604,7 @@ def pe_kv_append(pool: KvPool, q, k, v, pos, block_table, rope_theta: float = 0.
         raise ValueError("q_out without q")
     if err is not None:
         _cache_i32(pool, "err", err, (1,))
-    _cache_call(pool, stream, "pe_kv_append", lib().pe_kv_append, pool._ref, T, B, n_heads,
+    _cache_call(pool, stream, "pe_kv_append", pool.lib.pe_kv_append, pool._ref, T, B, n_heads,
                 rope_theta, ptr(q), qs, ptr(k), ks, ptr(v), vs, ptr(pos), ptr(req),
                 ptr(block_table), pages, ptr(q_out), qos, ptr(err))
     return q_out
@@ -628,7 +630,7 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
     torch = pool.torch
     _cache_ints(window=window)
     B, n_heads = q.shape[0], q.shape[1]
-    dev, dh = pool.device, pool.head_dim
+    dh = pool.head_dim
     qs = _cache_rows(pool, "q", q, B, n_heads)
     pages = _cache_table(pool, "block_table", block_table, B)
     _cache_i32(pool, "seq_lens", seq_lens, (B,))
@@ -636,25 +638,26 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
         out = _cache_empty(pool, (B, n_heads, dh), q.dtype, stream)
     if lse is None:
         lse = _cache_empty(pool, (B, n_heads), torch.float32, stream)
-    elif (lse.dtype != torch.float32 or lse.shape != (B, n_heads) or not lse.is_contiguous()
-          or lse.device != dev):
+    elif (lse.dtype is not torch.float32 or lse.shape != (B, n_heads) or not lse.is_contiguous()
+          or lse.get_device() != pool.index):
         raise ValueError(f"lse must be contiguous float32 [{B}, {n_heads}]")
     os_ = _cache_rows(pool, "out", out, B, n_heads)
     if workspace is None:
         n = pool._workspace.get((B, n_heads))
         if n is None:
-            with torch.cuda.device(dev):
+            with torch.cuda.device(pool.index):
                 n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh)
             pool._workspace[B, n_heads] = n
         workspace = _cache_empty(pool, n, torch.uint8, stream)
-    elif not workspace.is_contiguous() or workspace.device != dev:
+    elif not workspace.is_contiguous() or workspace.get_device() != pool.index:
         raise ValueError("workspace must be contiguous on the pool's device")
+    else:
+        n = workspace.numel() * workspace.element_size()
     if err is not None:
         _cache_i32(pool, "err", err, (1,))
-    _cache_call(pool, stream, "pe_attn_decode", lib().pe_attn_decode, pool._ref, B, n_heads,
+    _cache_call(pool, stream, "pe_attn_decode", pool.lib.pe_attn_decode, pool._ref, B, n_heads,
                 dh ** -0.5 if scale is None else scale, ptr(q), qs, ptr(block_table), pages,
-                ptr(seq_lens), window, ptr(out), os_, ptr(lse), int(accumulate), ptr(workspace),
-                workspace.numel() * workspace.element_size(), ptr(err))
+                ptr(seq_lens), window, ptr(out), os_, ptr(lse), int(accumulate), ptr(workspace), n, ptr(err))
     return out, lse
 
 
@@ -671,8 +674,8 @@ def pe_kv_evict(pools: Sequence[KvPool], block_table, seq_lens, budget: int, sin
         raise ValueError("no pools")
     _cache_ints(budget=budget, sinks=sinks, recent=recent)
     p0, B = pools[0], block_table.shape[0]
-    dev, torch = p0.device, p0.torch
-    if any(p.device != dev for p in pools):
+    torch = p0.torch
+    if any(p.index != p0.index for p in pools):
         raise ValueError("the pools must be on one device")
     pages = _cache_table(p0, "block_table", block_table, B)
     _cache_i32(p0, "seq_lens", seq_lens, (B,))
@@ -689,7 +692,7 @@ def pe_kv_evict(pools: Sequence[KvPool], block_table, seq_lens, budget: int, sin
     if err is not None:
         _cache_i32(p0, "err", err, (1,))
     arr = (pe_kv_pool * len(pools))(*[p.struct for p in pools])
-    _cache_call(p0, stream, "pe_kv_evict", lib().pe_kv_evict, len(pools), arr, B,
+    _cache_call(p0, stream, "pe_kv_evict", p0.lib.pe_kv_evict, len(pools), arr, B,
                 ptr(block_table), pages, ptr(seq_lens), budget, sinks, recent, rope_theta,
                 ptr(dst_table), dst_pages, ptr(kept), ptr(new_lens), ptr(err))
     return kept, new_lens

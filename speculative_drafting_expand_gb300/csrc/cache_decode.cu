@@ -35,6 +35,7 @@
 // e4m3 pools go through fp16, which holds every code; q is scaled there by a
 // power of two to [1, 2) so that fp16's range does not matter.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "cache_common.cuh"
@@ -116,40 +117,44 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, bool record)
 
 // The line of pages: where unit u lies.  Every thread sums the pages of an
 // equal share of the requests; the shares' prefix sums stay in shared memory
-// and a warp searches them, then its share.
+// and a warp searches them, then its share.  (The host refuses calls whose
+// tables could hold 2^31 pages.)
 struct Line {
-  long long total;  // units
-  int per;          // requests a share
+  int total;  // units
+  int per;    // requests a share
 };
 template <int THREADS>
-__device__ __forceinline__ Line line_setup(const DecodeArgs& a, int heads, long long* prefix,
-                                           bool record) {
-  __shared__ long long warp_sum[THREADS / 32];
+__device__ __forceinline__ Line line_setup(const DecodeArgs& a, int heads, int* prefix) {
+  __shared__ int warp_sum[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   Line ln;
   ln.per = (a.B + THREADS - 1) / THREADS;
-  long long mine = 0;
+  int mine = 0;
   for (int i = 0; i < ln.per; ++i) {
     const int b = tid * ln.per + i;
     if (b < a.B) {
-      const Span s = span_of(a, b, record);
+      const Span s = span_of(a, b, false);
       mine += s.pe - s.pf;
     }
   }
   mine *= heads;
-  long long x = mine;
+  int x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sum[tid >> 5] = x;
   __syncthreads();
-  long long base = 0;
-  for (int w = 0; w < (tid >> 5); ++w) base += warp_sum[w];
-  prefix[tid] = base + x - mine;
+  int base = 0;
   ln.total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) ln.total += warp_sum[w];
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int c = warp_sum[w];
+    base += w < (tid >> 5) ? c : 0;
+    ln.total += c;
+  }
+  prefix[tid] = base + x - mine;
   __syncthreads();
   return ln;
 }
@@ -157,19 +162,12 @@ __device__ __forceinline__ Line line_setup(const DecodeArgs& a, int heads, long 
 // Part i of `total` pages in n equal parts, the first ones a page longer
 // (i >= n: nothing).
 struct Share {
-  long long first, count;
+  int first, count;
 };
-__device__ __forceinline__ Share share_of(long long total, int n, int i) {
-  long long per, rest;
-  if (total >> 31) {
-    per = total / n;
-    rest = total % n;
-  } else {
-    per = static_cast<uint32_t>(total) / static_cast<uint32_t>(n);
-    rest = static_cast<uint32_t>(total) % static_cast<uint32_t>(n);
-  }
+__device__ __forceinline__ Share share_of(int total, int n, int i) {
+  const int per = static_cast<uint32_t>(total) / static_cast<uint32_t>(n), rest = total - per * n;
   if (i >= n) return Share{0, 0};
-  return Share{per * i + min(static_cast<long long>(i), rest), per + (i < rest ? 1 : 0)};
+  return Share{per * i + min(i, rest), per + (i < rest ? 1 : 0)};
 }
 
 // A place on the line: page p of head tile hh of request b.
@@ -180,29 +178,24 @@ struct Place {
 };
 template <int THREADS>
 __device__ __forceinline__ Place place_of(const DecodeArgs& a, const Line& ln, int heads,
-                                          const long long* prefix, long long u) {
-  int lo = 0, hi = THREADS - 1;  // last share with prefix <= u
+                                          const int* prefix, int u) {
+  int lo = 0, hi = min(a.B, THREADS) - 1;  // last share with prefix <= u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   Place pl;
-  long long left = u - prefix[lo];
+  int left = u - prefix[lo];
   pl.b = lo * ln.per;
   pl.s = span_of(a, pl.b, false);
-  while (left >= static_cast<long long>(pl.s.pe - pl.s.pf) * heads) {
-    left -= static_cast<long long>(pl.s.pe - pl.s.pf) * heads;
+  while (left >= (pl.s.pe - pl.s.pf) * heads) {
+    left -= (pl.s.pe - pl.s.pf) * heads;
     pl.s = span_of(a, ++pl.b, false);
   }
   const uint32_t np = pl.s.pe - pl.s.pf;
-  if (left >> 31) {
-    pl.hh = static_cast<int>(left / np);
-    pl.p = pl.s.pf + static_cast<int>(left % np);
-  } else {
-    pl.hh = static_cast<int>(static_cast<uint32_t>(left) / np);
-    pl.p = pl.s.pf + static_cast<int>(static_cast<uint32_t>(left) % np);
-  }
+  pl.hh = static_cast<uint32_t>(left) / np;
+  pl.p = pl.s.pf + (left - pl.hh * static_cast<int>(np));
   return pl;
 }
 // The first page of the next item (there is one).
@@ -286,7 +279,7 @@ struct Feeder {
   static constexpr int STAGES = WITH_V ? SH::STAGES : SH::S_STAGES;
   static constexpr int STRIDE = WITH_V ? 2 * SH::PAGEB : SH::PAGEB;
   Place pl;
-  long long left;  // units still to copy
+  int left;        // units still to copy
   int ids;         // this lane's page of the 32 from ids_at on
   int ids_at;      // -1: none
   int stage;
@@ -706,7 +699,14 @@ struct F32Tile {
     const float* src = static_cast<const float*>(A.q) + static_cast<size_t>(b) * A.q_stride +
                        static_cast<size_t>(h0) * DH;
     __syncwarp();
-    for (int i = lane; i < R * DH; i += 32) q[i] = i < rows * DH ? src[i] * A.scale : 0.f;
+#pragma unroll
+    for (int i = 0; i < R * DH / 128; ++i) {
+      const int e = (i * 32 + lane) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < rows * DH) v = *reinterpret_cast<const float4*>(src + e);
+      *reinterpret_cast<float4*>(q + e) =
+          make_float4(v.x * A.scale, v.y * A.scale, v.z * A.scale, v.w * A.scale);
+    }
     __syncwarp();
 #pragma unroll
     for (int x = 0; x < R / 4; ++x) {
@@ -919,27 +919,38 @@ struct TileOf<PE_KV_F32, DH, GT> {
 
 // ----------------------------------------------------------------- results
 
-// Joins the parts of one item inside a CTA, rec(0) .. rec(count - 1) in the
-// order of the positions, into the result or into `dst`.
-template <int DT, int DH, int GT, typename Rec>
-__device__ __forceinline__ void join_in_cta(const DecodeArgs& a, int b, int hh, int count, Rec rec,
-                                            float* dst, int threads) {
+// Joins the parts of one item inside a CTA: part[0] .. part[count - 1] in the
+// order of the positions, into the result (dst NULL) or a record.
+template <int DT, int DH, int GT, int W>
+__device__ __forceinline__ void join_in_cta(const DecodeArgs& a, int b, int hh, int count,
+                                            const float* const (&part)[W], float* dst) {
   using SH = DecodeShape<DT, DH, GT>;
   const int h0 = hh / a.tiles * a.G + (hh % a.tiles) * SH::ROWS;
   const int rows = min(SH::ROWS, a.G - (hh % a.tiles) * SH::ROWS);
-  for (int e = threadIdx.x * 4; e < SH::ROWS * DH; e += threads * 4) {
+#pragma unroll 1
+  for (int e = threadIdx.x * 4; e < SH::ROWS * DH; e += W * 32 * 4) {
     const int r = e / DH, d = e % DH;
+    float m[W], l[W];
+    float4 v[W];
     float M = -INFINITY;
-    for (int i = 0; i < count; ++i) M = fmaxf(M, rec(i)[r]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {  // every load before any use; past count: the first again
+      m[i] = part[i][r];
+      l[i] = part[i][SH::ROWS + r];
+      v[i] = *reinterpret_cast<const float4*>(part[i] + 2 * SH::ROWS + e);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) M = fmaxf(M, i < count ? m[i] : -INFINITY);
     const float base = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < count; ++i) {
-      const float* p = rec(i);
-      const float c = fast_exp2(p[r] - base);
-      const float4 v = *reinterpret_cast<const float4*>(p + 2 * SH::ROWS + e);
-      L = fmaf(c, p[SH::ROWS + r], L);
-      O = make_float4(fmaf(c, v.x, O.x), fmaf(c, v.y, O.y), fmaf(c, v.z, O.z), fmaf(c, v.w, O.w));
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i >= count) break;
+      const float c = fast_exp2(m[i] - base);
+      L = fmaf(c, l[i], L);
+      O = make_float4(fmaf(c, v[i].x, O.x), fmaf(c, v[i].y, O.y), fmaf(c, v[i].z, O.z),
+                      fmaf(c, v[i].w, O.w));
     }
     if (dst) {
       *reinterpret_cast<float4*>(dst + 2 * SH::ROWS + e) = O;
@@ -967,38 +978,28 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   using Tile = typename TileOf<DT, DH, GT>::type;
   constexpr int W = SH::WARPS, THREADS = W * 32;
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long prefix[THREADS];
-  // a warp's partials: first (began before its piece), last (goes on after)
+  __shared__ int prefix[THREADS];
+  // a warp's parts: first (its item began before the piece), last (it goes on
+  // after it)
   __shared__ int w_state[W], w_b[W][2], w_hh[W][2];
   __shared__ int after;  // pages of the CTA's last item that lie after it
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int heads = a.Hkv * a.tiles;
-  // rows that attend nothing
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Span s = span_of(a, b, tid == 0);
-    if (s.pe > s.pf) continue;
-    for (int e = tid * 4; e < a.Hq * DH; e += THREADS * 4)
-      put4<DT>(a.out, static_cast<size_t>(b) * a.out_stride + e, make_float4(0.f, 0.f, 0.f, 0.f));
-    for (int h = tid; h < a.Hq; h += THREADS) {
-      a.lse_w[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
-      if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
-    }
-  }
-  const Line ln = line_setup<THREADS>(a, heads, prefix, false);
+  const Line ln = line_setup<THREADS>(a, heads, prefix);
   // CTAs and warps take whole pages, the first ones one more; with few pages,
   // kMinPages a warp on fewer CTAs
-  const long long want = (ln.total + W * kMinPages - 1) / (W * kMinPages);
-  const int grid = want < gridDim.x ? max(static_cast<int>(want), 1) : gridDim.x;
+  const int grid = min(static_cast<int>(gridDim.x),
+                       max(1, static_cast<int>((static_cast<uint32_t>(ln.total) + W * kMinPages - 1) /
+                                               (W * kMinPages))));
   const Share cta = share_of(ln.total, grid, blockIdx.x);
   if (cta.count == 0) {
     if (tid == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
   const Share mine = share_of(cta.count, W, w);
-  const long long u0 = cta.first + mine.first, u1 = u0 + mine.count;
-  const int working = cta.count < W ? static_cast<int>(cta.count) : W;
+  const int working = min(cta.count, W);
   char* ring_p = smem + w * SH::RING;
   char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
   const uint32_t ring = smem_u32(ring_p);
@@ -1007,26 +1008,25 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   // bits of w_state: 1 a first partial in the head record, 2 it is in the
   // ring instead, 4 its item ends here, 8 a last partial in the ring
   int state = 0;
-  if (u0 < u1) {
-    Place pl = place_of<THREADS>(a, ln, heads, prefix, u0);
+  if (mine.count > 0) {
+    Place pl = place_of<THREADS>(a, ln, heads, prefix, cta.first + mine.first);
     Feeder<SH, true> feed;
     feed.pl = pl;
-    feed.left = u1 - u0;
+    feed.left = mine.count;
     feed.ids_at = -1;
     feed.ids = -1;
     feed.stage = 0;
     feed.bad = 0;
 #pragma unroll 1
     for (int i = 0; i < SH::STAGES; ++i) feed.step(a, heads, a.tiles, ring, lane, true);
-    long long left = u1 - u0;
-    int stage = 0;
+    int left = mine.count, stage = 0;
     Tile tile;
     while (true) {
       const bool began = pl.p == pl.s.pf;
       const int hk = pl.hh / a.tiles, r0 = (pl.hh % a.tiles) * SH::ROWS;
       const int rows = min(SH::ROWS, a.G - r0);
       tile.start(a, pl.b, hk * a.G + r0, rows, scratch, lane);
-      const int stop = static_cast<int>(min(static_cast<long long>(pl.s.pe), pl.p + left));
+      const int stop = min(pl.s.pe, pl.p + left);
       left -= stop - pl.p;
       auto take = [&](auto count) {
         constexpr int NP = decltype(count)::value;
@@ -1091,56 +1091,64 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   }
   if (lane == 0) w_state[w] = state;
   __syncthreads();
-  // chains of parts of one item: the warps from `from` on
+  // Chains of parts of one item: the warps from `from` on.  A warp's first
+  // part lies in its ring (bit of in_ring) or its head record, its last part
+  // in its ring.
+  uint32_t in_ring = 0;
+#pragma unroll
+  for (int x = 0; x < W; ++x) in_ring |= ((w_state[x] >> 1) & 1) << x;
   int4 meta = make_int4(-1, 0, 0, 0);
   int from = -1;        // first warp of the open chain, its part there: last (or first)
   bool before = false;  // the chain began before this CTA
-  auto rec = [&](int i) -> const float* {
-    // the i-th part of the chain: warp `from`'s last part (its first, if the
-    // chain began before the CTA), then the later warps' first parts
-    const int x = from + i;
-    const bool in_ring = (i == 0 && !before) || (w_state[x] & 2);
-    return in_ring ? reinterpret_cast<const float*>(smem + x * SH::RING)
-                   : a.head + (static_cast<size_t>(blockIdx.x) * W + x) * SH::REC;
-  };
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 2 * SH::REC;
-  for (int x = 0; x < working; ++x) {
-    const int st = w_state[x];
-    if (st & 1) {
-      if (from < 0) {
-        from = x;
-        before = true;
+#pragma unroll 1
+  for (int x = 0; x <= working; ++x) {
+    const int st = x < working ? w_state[x] : 0;
+    if ((st & 1) && from < 0) {
+      from = x;
+      before = true;
+    }
+    const bool over = x == working;  // what is open goes on after the CTA
+    if (from >= 0 && ((st & 4) || over)) {
+      const int count = over ? x - from : x - from + 1;
+      const float* parts[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (i > 0 && i >= count) {
+          parts[i] = parts[0];
+          continue;
+        }
+        const int y = from + i;
+        parts[i] = (i == 0 && !before) || ((in_ring >> y) & 1)
+                       ? reinterpret_cast<const float*>(smem + y * SH::RING)
+                       : a.head + (static_cast<size_t>(blockIdx.x) * W + y) * SH::REC;
       }
-      if (st & 4) {
-        join_in_cta<DT, DH, GT>(a, w_b[x][0], w_hh[x][0], x - from + 1, rec,
-                                before ? part : nullptr, THREADS);
-        from = -1;
-        before = false;
+      const int y = over ? from : x, k = over && !before ? 1 : 0;
+      join_in_cta<DT, DH, GT, W>(a, w_b[y][k], w_hh[y][k], count, parts,
+                                 before ? part : over ? part + SH::REC : nullptr);
+      if (over && !before) {
+        // how many of the next CTAs the rest of the item reaches
+        meta.x = w_b[from][1];
+        meta.y = w_hh[from][1];
+        const Share next = share_of(ln.total, grid, min(static_cast<int>(blockIdx.x) + 1, grid - 1));
+        const Share last = share_of(ln.total, grid, grid - 1);
+        meta.z = 2;
+        int rest = after - next.count;
+        if (rest > 0) {
+          // further CTAs of next.count pages, then shorter ones
+          const int wide = next.count > last.count
+                               ? ln.total - last.count * grid - static_cast<int>(blockIdx.x + 2)
+                               : 0;
+          const int of_wide = min(wide, (rest + next.count - 1) / next.count);
+          rest -= of_wide * next.count;
+          meta.z += of_wide;
+          if (rest > 0) meta.z += (rest + last.count - 1) / last.count;
+        }
       }
+      from = -1;
+      before = false;
     }
     if ((st & 8) && from < 0) from = x;
-  }
-  if (from >= 0) {
-    join_in_cta<DT, DH, GT>(a, 0, 0, working - from, rec, before ? part : part + SH::REC, THREADS);
-    if (!before) {
-      // how many of the next CTAs the rest of the item reaches
-      meta.x = w_b[from][1];
-      meta.y = w_hh[from][1];
-      const Share next = share_of(ln.total, grid, min(static_cast<int>(blockIdx.x) + 1, grid - 1));
-      const Share last = share_of(ln.total, grid, grid - 1);
-      meta.z = 2;
-      long long rest = after - next.count;
-      if (rest > 0) {
-        // parts of next.count pages up to the first shorter one
-        const long long wide = next.count > last.count
-                                   ? ln.total - last.count * grid - (blockIdx.x + 2)
-                                   : 0;  // further CTAs with next.count pages
-        const long long of_wide = min(wide, (rest + next.count - 1) / next.count);
-        rest -= of_wide * next.count;
-        meta.z += static_cast<int>(of_wide);
-        if (rest > 0) meta.z += static_cast<int>((rest + last.count - 1) / last.count);
-      }
-    }
   }
   if (tid == 0) a.meta[blockIdx.x] = meta;
 }
@@ -1158,20 +1166,32 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
   constexpr int LANES = R * DH / 4;                // threads that hold the row's elements
   constexpr int WAYS = kJoinThreads / LANES;       // parts taken side by side
   constexpr int MOST = kMostCtas;
-  __shared__ float wt[MOST][R], red[2][R];
+  __shared__ float wt[MOST][R], ls[MOST][R], red[2][R];
   __shared__ float4 side[WAYS > 1 ? WAYS : 1][LANES];
   grid_dep_wait();
   grid_dep_launch();
-  const int c = blockIdx.x, row0 = blockIdx.y * R;
+  const int c = blockIdx.x, row0 = blockIdx.y * R, tid = threadIdx.x;
   const int4 meta = __ldcg(a.meta + c);
+  // rows that attend nothing
+  for (int b = blockIdx.x * kJoinRows + blockIdx.y; b < a.B; b += gridDim.x * kJoinRows) {
+    const Span s = span_of(a, b, tid == 0);
+    if (s.pe > s.pf) continue;
+    for (int e = tid * 4; e < a.Hq * DH; e += kJoinThreads * 4)
+      put4<DT>(a.out, static_cast<size_t>(b) * a.out_stride + e, make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int h = tid; h < a.Hq; h += kJoinThreads) {
+      a.lse_w[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
+      if (a.lse) a.lse[static_cast<size_t>(b) * a.Hq + h] = -INFINITY;
+    }
+  }
   if (meta.x < 0) return;
   const int b = meta.x, hh = meta.y, count = min(meta.z, MOST);
   auto rec = [&](int i) -> const float* {
     return a.part + (static_cast<size_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * SH::REC;
   };
-  const int tid = threadIdx.x;
-  for (int k = tid; k < count * R; k += kJoinThreads)
+  for (int k = tid; k < count * R; k += kJoinThreads) {
     wt[k / R][k % R] = __ldcg(rec(k / R) + row0 + k % R);
+    ls[k / R][k % R] = __ldcg(rec(k / R) + SH::ROWS + row0 + k % R);
+  }
   __syncthreads();
   // a warp a row: the maximum, then the weights and the sum
   for (int r = tid >> 5; r < R; r += kJoinThreads / 32) {
@@ -1184,7 +1204,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
     float L = 0.f;
     for (int i = lane; i < count; i += 32) {
       const float x = fast_exp2(wt[i][r] - base);
-      L = fmaf(x, __ldcg(rec(i) + SH::ROWS + row0 + r), L);
+      L = fmaf(x, ls[i][r], L);
       wt[i][r] = x;
     }
 #pragma unroll
@@ -1231,12 +1251,12 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
   using Feed = Feeder<SH, false>;
   constexpr int W = SH::WARPS, THREADS = W * 32;
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long prefix[THREADS];
+  __shared__ int prefix[THREADS];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const Line ln = line_setup<THREADS>(a, a.Hkv, prefix, false);
+  const Line ln = line_setup<THREADS>(a, a.Hkv, prefix);
   const Share mine = share_of(ln.total, gridDim.x * W, blockIdx.x * W + w);
   if (mine.count == 0) return;
   char* scratch = smem + W * SH::S_RING + w * SH::SCRATCH;
@@ -1251,8 +1271,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
   feed.bad = 0;
 #pragma unroll 1
   for (int i = 0; i < Feed::STAGES; ++i) feed.step(a, a.Hkv, 1, ring, lane, false);
-  int stage = 0;
-  long long left = mine.count;
+  int stage = 0, left = mine.count;
   constexpr int LH = DT == PE_KV_F32 ? SH::ROWS / 4 : GT;  // heads a lane
   int have = -1;  // head tile whose query and lse are loaded
   typename TileOf<DT, DH, GT>::type tile;
@@ -1342,7 +1361,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
       next_item(a, a.Hkv, pl);
       have = -1;
     }
-    const int run = static_cast<int>(min(static_cast<long long>(pl.s.pe - pl.p), left));
+    const int run = min(pl.s.pe - pl.p, left);
     if (SH::S_TAKE > 1 && run >= SH::S_TAKE) take(std::integral_constant<int, SH::S_TAKE>());
     else take(std::integral_constant<int, 1>());
   }
@@ -1350,16 +1369,33 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
 
 // --------------------------------------------------------------- launchers
 
-static int sm_count() {
-  int dev = 0, sms = 0;
+static int sm_count(int& dev) {
+  int sms = 0;
+  dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return sms;
 }
 
+// The kernels' shared memory, asked for once per device.
 template <int DT, int DH, int GT>
-static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate, cudaStream_t s) {
+static cudaError_t allow_smem(int dev) {
+  using SH = DecodeShape<DT, DH, GT>;
+  static std::atomic<uint64_t> done{0};
+  if (dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DT, DH, GT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_scores_kernel<DT, DH, GT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::S_SMEM);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
+
+template <int DT, int DH, int GT>
+static pe_status launch_decode(DecodeArgs& a, char* ws, int dev, int sms, bool accumulate,
+                               cudaStream_t s) {
   using SH = DecodeShape<DT, DH, GT>;
   const int grid = std::min(sms * SH::CTAS, kMostCtas);
   a.tiles = (a.G + SH::ROWS - 1) / SH::ROWS;
@@ -1370,12 +1406,7 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate
   a.part = reinterpret_cast<float*>(ws);
   ws += static_cast<size_t>(grid) * 2 * SH::REC * 4;
   a.head = reinterpret_cast<float*>(ws);
-  // per device and kernel, so set on every call (a host-side table write)
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DT, DH, GT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
-  if (e == cudaSuccess && accumulate)
-    e = cudaFuncSetAttribute(attn_scores_kernel<DT, DH, GT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SH::S_SMEM);
+  cudaError_t e = allow_smem<DT, DH, GT>(dev);
   if (e == cudaSuccess)
     e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
   if (e == cudaSuccess)
@@ -1387,11 +1418,18 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int sms, bool accumulate
 }
 
 template <int DT, int DH>
-static pe_status launch_decode_heads(DecodeArgs& a, char* ws, int sms, bool accumulate,
+static pe_status launch_decode_heads(DecodeArgs& a, char* ws, int dev, int sms, bool accumulate,
                                      cudaStream_t s) {
   if constexpr (DT != PE_KV_F32)
-    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, sms, accumulate, s);
-  return launch_decode<DT, DH, 1>(a, ws, sms, accumulate, s);
+    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, dev, sms, accumulate, s);
+  return launch_decode<DT, DH, 1>(a, ws, dev, sms, accumulate, s);
+}
+
+// The largest of the pool types: two CTAs an SM, 8 or 16 rows a tile.
+static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int head_dim, int sms) {
+  const int64_t grid = 2 * sms, rows = n_heads / n_kv_heads > 8 ? 16 : 8;
+  return (B * n_heads * 4 + 15) / 16 * 16 + grid * 16 +
+         grid * (2 + kMaxWarps) * rows * (head_dim + 2) * 4;
 }
 
 }  // namespace pe
@@ -1403,12 +1441,9 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
   if (B < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  const int64_t sms = pe::sm_count();
-  if (sms < 1) return 0;
-  // the largest of the pool types: two CTAs an SM, 8 or 16 rows a tile
-  const int64_t grid = 2 * sms, rows = n_heads / n_kv_heads > 8 ? 16 : 8;
-  return (static_cast<int64_t>(B) * n_heads * 4 + 15) / 16 * 16 + grid * 16 +
-         grid * (2 + pe::kMaxWarps) * rows * (head_dim + 2) * 4;
+  int dev;
+  const int sms = pe::sm_count(dev);
+  return sms < 1 ? 0 : pe::workspace_bytes_for(B, n_heads, n_kv_heads, head_dim, sms);
 }
 
 pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, float scale,
@@ -1425,9 +1460,13 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
       !row_ok(out, out_stride, qw, eb) || (accumulate && !pool->scores) || !workspace ||
       !is_aligned16(workspace) || workspace_bytes <= 0)
     return PE_ERR_INVALID_ARGUMENT;
-  const int64_t need = pe_attn_decode_workspace(B, n_heads, pool->n_kv_heads, dh);
-  if (need == 0) return PE_ERR_CUDA;
-  if (workspace_bytes < need) return PE_ERR_INVALID_ARGUMENT;
+  // the pages are counted in 32 bits (a table of that size is 8 GB)
+  if (static_cast<int64_t>(B) * bt_stride > 2147483647LL / n_heads) return PE_ERR_UNSUPPORTED;
+  int dev;
+  const int sms = sm_count(dev);
+  if (sms < 1) return PE_ERR_CUDA;
+  if (workspace_bytes < workspace_bytes_for(B, n_heads, pool->n_kv_heads, dh, sms))
+    return PE_ERR_INVALID_ARGUMENT;
   DecodeArgs a = {};
   a.pool = CachePool{pool->k, pool->v, pool->scores, pool->num_blocks};
   a.B = B;
@@ -1449,16 +1488,15 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   a.err = err;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = sm_count();
   const bool acc = accumulate != 0;
   if (pool->dtype == PE_KV_F32)
-    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, sms, acc, s)
-                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, dev, sms, acc, s);
   if (pool->dtype == PE_KV_BF16)
-    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, sms, acc, s)
-                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, sms, acc, s);
-  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, sms, acc, s)
-                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, dev, sms, acc, s);
+  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, dev, sms, acc, s)
+                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, dev, sms, acc, s);
 }
 
 }  // extern "C"

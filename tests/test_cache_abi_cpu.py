@@ -102,7 +102,7 @@ def _decode(B, pool=None, change=()):
     (dict(q=0), 1), (dict(q=BASE + 8), 1), (dict(qs=128), 1), (dict(qs=257), 1),
     (dict(table=0), 1), (dict(stride=0), 1), (dict(lens=0), 1), (dict(window=-1), 1),
     (dict(out=0), 1), (dict(os=128), 1), (dict(ws=0), 1), (dict(ws=BASE + 8), 1),
-    (dict(bytes=0), 1)])
+    (dict(bytes=0), 1), (dict(stride=1 << 28), 2)])
 def test_decode_refusals(B, change, status):
     assert _decode(B, change=change) == status
 
