@@ -67,7 +67,7 @@ typedef struct {
  * rope_theta 0 rotates nothing.  Angles are exact to 2^-32 of a turn;
  * results are rounded once to their type (e4m3: x / scale, nearest even,
  * saturated at +-448).  A row with pos[t] < 0 is padding: nothing of it is
- * read or written.
+ * written.
  *
  * q [T, n_heads, head_dim] (NULL: no q, then q_out is NULL too), k, v [T,
  * n_kv_heads, head_dim], q_out like q: rows `*_stride` elements apart, heads

@@ -1,6 +1,8 @@
 // cache_append.cu -- new rows of q, k and v into a paged KV cache: rotate-half
 // rotary embedding of q and k at the row's position, k and v stored in the
 // position's page slot (include/peagle_cache.h).
+#include <algorithm>
+
 #include "cache_common.cuh"
 #include "pe_kernels.h"
 
@@ -22,89 +24,165 @@ struct AppendArgs {
   RopeSteps rope;
 };
 
-template <typename T>
-__device__ __forceinline__ void store_kv(void* base, size_t at, float x, float scale);
-template <>
-__device__ __forceinline__ void store_kv<float>(void* base, size_t at, float x, float) {
-  static_cast<float*>(base)[at] = x;
-}
-template <>
-__device__ __forceinline__ void store_kv<bf16>(void* base, size_t at, float x, float) {
-  static_cast<bf16*>(base)[at] = __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ void store_kv<uint8_t>(void* base, size_t at, float x, float scale) {
-  const uint16_t c = f32x2_to_e4m3x2(__fdiv_rn(x, scale), 0.f);
-  static_cast<uint8_t*>(base)[at] = static_cast<uint8_t>(c & 0xff);
+// A chunk of activations into a pool, as the pool holds it.
+template <typename S, int N>
+__device__ __forceinline__ void store_kv(void* base, size_t at, const float (&x)[N], float scale) {
+  if constexpr (sizeof(S) == 1) {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      w[i] = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
+             (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale),
+                                                    __fdiv_rn(x[4 * i + 3], scale)))
+              << 16);
+    static_assert(N == 8, "bf16 activations beside e4m3 pools");
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<S*>(base) + at) = Chunk<S>::put(x);
+  }
 }
 
-// One CTA a row, a thread per (head, pair).
+// A CTA a row.  The lanes of a group take 16 bytes each of two heads (q heads,
+// then k heads); to turn a pair (i, i + DH / 2) a lane needs the chunk that
+// its partner half a head further holds, so the low half of the lanes turns
+// the first head and the other half the second, with one exchange before and
+// one after.  More threads copy v.  Bound by bytes for many rows and by
+// latency for few: every load is on its way before the first use, and the
+// row's sines and cosines (one pair a thread, shared by all heads) are worked
+// out meanwhile.
+constexpr int kAppendMost = 512;
+
 template <typename A, typename S, int DH>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendMost) kv_append_kernel(
+    const __grid_constant__ AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int HALF = DH / 2;
-  __shared__ float cs[HALF], sn[HALF];
-  const int t = blockIdx.x;
+  using C = Chunk<A>;
+  constexpr int N = C::N;         // elements of a chunk
+  constexpr int LANES = DH / N;   // lanes of a head
+  constexpr int HALF = LANES / 2;
+  __shared__ float cs[DH / 2], sn[DH / 2];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int hq = a.q ? a.Hq : 0, heads = hq + a.Hkv;
+  const int turned = (heads + 1) / 2 * LANES, all = turned + a.Hkv * LANES;
+  const int threads = blockDim.x;
+  const A* q = static_cast<const A*>(a.q) + static_cast<size_t>(t) * a.q_stride;
+  const A* k = static_cast<const A*>(a.k) + static_cast<size_t>(t) * a.k_stride;
+  const A* v = static_cast<const A*>(a.v) + static_cast<size_t>(t) * a.v_stride;
+  const int c = tid % LANES;
+  const bool high = c >= HALF;
+  // this thread's chunks of item w: two heads', or one of v
+  auto load = [&](int w, uint4 (&x)[2]) {
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    if (w < turned) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int h = w / LANES * 2 + y;
+        if (h < heads)
+          x[y] = *reinterpret_cast<const uint4*>((h < hq ? q + h * DH : k + (h - hq) * DH) + c * N);
+      }
+    } else if (w < all) {
+      x[0] = *reinterpret_cast<const uint4*>(v + static_cast<size_t>(w - turned) * N);
+    }
+  };
+  uint4 x[2];
+  load(tid, x);
   const int p = a.pos[t];
   if (p < 0) return;  // padding
   const int r = a.req ? a.req[t] : t;
   int blk = -1;
   if (r < 0 || r >= a.B) {
-    if (threadIdx.x == 0) record_error(a.err, PE_DEV_BAD_ROW);
+    if (tid == 0) record_error(a.err, PE_DEV_BAD_ROW);
   } else if (p >= static_cast<long long>(a.bt_stride) * kPage) {
-    if (threadIdx.x == 0) record_error(a.err, PE_DEV_BAD_POSITION);
+    if (tid == 0) record_error(a.err, PE_DEV_BAD_POSITION);
   } else {
     blk = a.block_table[static_cast<size_t>(r) * a.bt_stride + p / kPage];
     if (blk < 0 || blk >= a.pool.num_blocks) {
-      if (threadIdx.x == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
+      if (tid == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
       blk = -1;
     }
   }
-  const int off = p % kPage;
-  if (threadIdx.x < HALF) {
-    float c = 1.f, s = 0.f;
-    if (a.rope.on) rope_cos_sin(a.rope.step[threadIdx.x], p, c, s);
-    cs[threadIdx.x] = c;
-    sn[threadIdx.x] = s;
+  for (int i = tid; a.rope.on && i < DH / 2; i += threads) {
+    float cc, ss;
+    rope_cos_sin(a.rope.step[i], p, cc, ss);
+    cs[i] = cc;
+    sn[i] = ss;
   }
   __syncthreads();
-  const A* q = static_cast<const A*>(a.q) + static_cast<size_t>(t) * a.q_stride;
-  const A* k = static_cast<const A*>(a.k) + static_cast<size_t>(t) * a.k_stride;
-  const A* v = static_cast<const A*>(a.v) + static_cast<size_t>(t) * a.v_stride;
-  A* qo = static_cast<A*>(a.q_out) + static_cast<size_t>(t) * a.qo_stride;
-  const int hq = a.q ? a.Hq : 0;
-  for (int w = threadIdx.x; w < (hq + a.Hkv) * HALF; w += blockDim.x) {
-    const int h = w / HALF, i = w % HALF;
-    const A* x = h < hq ? q + h * DH : k + (h - hq) * DH;
-    const float x1 = to_f(x[i]), x2 = to_f(x[i + HALF]);
-    const float y1 = x1 * cs[i] - x2 * sn[i];
-    const float y2 = x2 * cs[i] + x1 * sn[i];
-    if (h < hq) {
-      qo[h * DH + i] = from_f<A>(y1);
-      qo[h * DH + i + HALF] = from_f<A>(y2);
-    } else if (blk >= 0) {
-      const size_t at = ((static_cast<size_t>(blk) * a.Hkv + (h - hq)) * kPage + off) * DH;
-      store_kv<S>(a.pool.k, at + i, y1, a.k_scale);
-      store_kv<S>(a.pool.k, at + i + HALF, y2, a.k_scale);
+  const int off = p % kPage;
+  // element (head, 0) of the row's slot
+  auto slot = [&](int h) {
+    return ((static_cast<size_t>(blk) * a.Hkv + h) * kPage + off) * DH;
+  };
+  for (int w0 = tid / 32 * 32; w0 < all; w0 += threads) {  // whole warps: they exchange
+    const int w = w0 + tid % 32;
+    if (w0 >= threads) load(w, x);
+    if (a.rope.on && w0 < turned) {
+      const uint4 got = shfl_xor16(high ? x[0] : x[1], HALF);
+      uint4 lo = high ? got : x[0], hi = high ? x[1] : got;
+      float u[N], y[N];
+      C::get(lo, u);
+      C::get(hi, y);
+      if (w < turned) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int i = c % HALF * N + e;
+          const float z = u[e] * cs[i] - y[e] * sn[i];
+          y[e] = y[e] * cs[i] + u[e] * sn[i];
+          u[e] = z;
+        }
+        // q leaves rounded to its type, k as it is rounded by its pool: the
+        // exchange is done on what is stored
+        const int h = w / LANES * 2 + (high ? 1 : 0);
+        if (h >= hq && h < heads && blk >= 0) {
+          store_kv<S>(a.pool.k, slot(h - hq) + c % HALF * N, u, a.k_scale);
+          store_kv<S>(a.pool.k, slot(h - hq) + c % HALF * N + DH / 2, y, a.k_scale);
+        }
+      }
+      lo = C::put(u);
+      hi = C::put(y);
+      const uint4 back = shfl_xor16(high ? lo : hi, HALF);
+      if (w < turned) {
+        x[0] = high ? back : lo;
+        x[1] = high ? hi : back;
+      }
+    }
+    if (w < turned) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int h = w / LANES * 2 + y;
+        if (h < hq) {
+          *reinterpret_cast<uint4*>(static_cast<A*>(a.q_out) +
+                                    static_cast<size_t>(t) * a.qo_stride + h * DH + c * N) = x[y];
+        } else if (h < heads && blk >= 0 && !a.rope.on) {
+          float z[N];
+          C::get(x[y], z);
+          store_kv<S>(a.pool.k, slot(h - hq) + c * N, z, a.k_scale);
+        }
+      }
+    } else if (w < all && blk >= 0) {
+      float z[N];
+      C::get(x[0], z);
+      const int e = (w - turned) * N;
+      store_kv<S>(a.pool.v, slot(e / DH) + e % DH, z, a.v_scale);
     }
   }
-  if (blk < 0) return;
-  for (int w = threadIdx.x; w < a.Hkv * DH; w += blockDim.x) {
-    const size_t at =
-        ((static_cast<size_t>(blk) * a.Hkv + w / DH) * kPage + off) * DH + w % DH;
-    store_kv<S>(a.pool.v, at, to_f(v[w]), a.v_scale);
-  }
-  if (a.pool.scores)
-    for (int h = threadIdx.x; h < a.Hkv; h += blockDim.x)
+  if (a.pool.scores && blk >= 0)
+    for (int h = tid; h < a.Hkv; h += threads)
       a.pool.scores[(static_cast<size_t>(blk) * a.Hkv + h) * kPage + off] = 0.f;
 }
 
+template <typename A, typename S, int DH>
+static cudaError_t launch_append_dim(const AppendArgs& a, cudaStream_t s) {
+  constexpr int LANES = DH / Chunk<A>::N;
+  const long long items =
+      ((static_cast<long long>(a.q ? a.Hq : 0) + a.Hkv + 1) / 2 + a.Hkv) * LANES;
+  const int threads = static_cast<int>(std::min<long long>(kAppendMost, (items + 31) / 32 * 32));
+  return launch_pdl(kv_append_kernel<A, S, DH>, dim3(a.T), dim3(threads), 0, s, a);
+}
 template <typename A, typename S>
 static cudaError_t launch_append(const AppendArgs& a, int dh, cudaStream_t s) {
-  if (dh == 64)
-    return launch_pdl(kv_append_kernel<A, S, 64>, dim3(a.T), dim3(256), 0, s, a);
-  return launch_pdl(kv_append_kernel<A, S, 128>, dim3(a.T), dim3(256), 0, s, a);
+  return dh == 64 ? launch_append_dim<A, S, 64>(a, s) : launch_append_dim<A, S, 128>(a, s);
 }
 
 }  // namespace pe

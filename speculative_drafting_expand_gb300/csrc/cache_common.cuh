@@ -81,4 +81,84 @@ __device__ __forceinline__ void rope_cos_sin(uint64_t step, long long pos, float
   sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
 }
 
+// The same for results that are rounded to 16 bits or fewer (FAST): the
+// hardware's sine and cosine, whose error on half a turn either way is 2^-21,
+// next to half a step of 2^-9 of the result.
+template <bool FAST>
+__device__ __forceinline__ void rope_turn(uint64_t step, long long pos, float& c, float& s) {
+  if constexpr (FAST) {
+    const uint64_t turn = step * static_cast<uint64_t>(pos);
+    const int32_t top = static_cast<int32_t>(static_cast<uint32_t>(turn >> 32));
+    __sincosf(static_cast<float>(top) * 1.4629180792671596e-9f, &s, &c);  // 2 pi 2^-32
+  } else {
+    rope_cos_sin(step, pos, c, s);
+  }
+}
+
+// The element type's chunk of 16 bytes as floats and back.
+template <typename S>
+struct Chunk;
+template <>
+struct Chunk<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+};
+template <>
+struct Chunk<bf16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+  }
+};
+template <>
+struct Chunk<uint8_t> {
+  static constexpr int N = 16;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[16]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t h = e4m3x2_to_f16x2(w[i] >> (16 * k));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x[4 * i + 2 * k] = f.x;
+        x[4 * i + 2 * k + 1] = f.y;
+      }
+  }
+  static __device__ __forceinline__ uint4 put(const float (&x)[16]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = f32x2_to_e4m3x2(x[4 * i], x[4 * i + 1]) |
+             (static_cast<uint32_t>(f32x2_to_e4m3x2(x[4 * i + 2], x[4 * i + 3])) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ uint4 shfl_xor16(uint4 v, int m) {
+  v.x = __shfl_xor_sync(0xffffffffu, v.x, m);
+  v.y = __shfl_xor_sync(0xffffffffu, v.y, m);
+  v.z = __shfl_xor_sync(0xffffffffu, v.z, m);
+  v.w = __shfl_xor_sync(0xffffffffu, v.w, m);
+  return v;
+}
+
 }  // namespace pe

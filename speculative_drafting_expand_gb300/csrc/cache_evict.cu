@@ -5,7 +5,26 @@
 // R(j - p) R(p) = R(j), so a key that moves from p to j is turned by j - p
 // and is then the key of position j: the kept positions form an ordinary
 // cache of positions 0 .. budget - 1.
+//
+// Bound by the bytes of the kept rows, read and written once; the scores are
+// a few percent of them.  One launch: a cluster of CTAs for each (layer,
+// request, kv head) finds the weight of the last position that stays, makes
+// the ordered list, and moves the rows.  The choosing of one row's CTAs runs
+// beside the moving of another's.
+//
+// The weight is found by bisection of its 32 bits, two bits a step: the
+// scores lie in shared memory as integers of the same order, and each step
+// counts those at or above three candidates.  Its time does not depend on the
+// values (a histogram's does: equal scores, such as the zeros of positions
+// that were never attended, meet in one counter), and it ends as soon as a
+// count is right.  Every CTA of a cluster chooses for itself: the scores are
+// read again from L2, and nothing is exchanged.
+//
+// In place, row j is written where an earlier-listed row may still lie, never
+// a later one (kept[j] >= j, ascending): a round of rows is read by the whole
+// cluster before the first of it is written.
 #include <algorithm>
+#include <atomic>
 
 #include "cache_common.cuh"
 #include "pe_kernels.h"
@@ -56,167 +75,285 @@ __device__ __forceinline__ int page_of(const int32_t* table, int stride, int b, 
   return -1;
 }
 
-__device__ __forceinline__ int block_count(bool x, int* red) {
-  const int c = __popc(__ballot_sync(0xffffffffu, x));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
-  __syncthreads();
-  int t = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) t += red[i];
-  return t;
-}
 
-// A CTA per (layer, request, kv head): the threshold by bisection of the 32
-// key bits, the list by counting, then the rows in order.
-template <typename S, int DH>
-__global__ void __launch_bounds__(256) kv_evict_kernel(const __grid_constant__ EvictArgs a) {
+constexpr int kEvictThreads = 512;
+constexpr int kMostKeys = 24576;  // scores that are held in shared memory
+
+// A row on its way: where from (-1: nowhere) and to, by how much the key
+// turns.
+struct Move {
+  long long src, dst;  // row numbers in the pool, -1: none
+  int turn;            // old position - new position
+};
+
+template <typename S, int DH, bool IN_PLACE>
+__global__ void __launch_bounds__(kEvictThreads, 2)
+    kv_evict_kernel(const __grid_constant__ EvictArgs a, int cluster, int key_room) {
+  constexpr int T = kEvictThreads, WARPS = T / 32;
+  constexpr int ROWB = DH * static_cast<int>(sizeof(S));
+  constexpr int LANES = ROWB / 16;       // lanes that hold a row, 16 bytes each
+  constexpr int ROUND = 2 * T / LANES;   // rows a CTA moves at a time: two a group of lanes
+  constexpr int HALF = LANES / 2;
+  extern __shared__ uint32_t keys[];     // [key_room]
+  __shared__ uint64_t step[DH / 2];
+  __shared__ int count[3][4];            // three steps' counters
+  __shared__ int scan[2][WARPS];
   grid_dep_wait();
   grid_dep_launch();
-  __shared__ int red[8], warp_base[8];
-  const int h = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv, layer = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cluster, row = blockIdx.x / cluster;
+  const int h = row % a.Hkv, b = row / a.Hkv, layer = blockIdx.y;
   const CachePool pool = a.pool[layer];
-  const int tid = threadIdx.x;
   const int n = evict_len(a, b, tid == 0);
   const int m = min(n, a.budget);
   int32_t* kept =
       a.kept + ((static_cast<size_t>(layer) * a.B + b) * a.Hkv + h) * static_cast<size_t>(a.budget);
-  if (layer == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
-  const int lo = a.sinks, hi = n - a.recent, need = a.budget - a.sinks - a.recent;
-  const bool all = n <= a.budget;
-  auto key_of = [&](int p) -> uint32_t {
-    const int blk = page_of(a.block_table, a.bt_stride, b, p, pool.num_blocks, a.err);
-    if (blk < 0) return score_key(-INFINITY);
-    return score_key(pool.scores[(static_cast<size_t>(blk) * a.Hkv + h) * kPage + p % kPage]);
-  };
-  // largest T with count(key >= T) >= need
-  uint32_t T = 0;
-  int above = 0;  // count(key > T)
-  if (!all && need > 0) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = T | (1u << bit);
-      int c = 0;
-      for (int p = lo + tid; p - tid < hi; p += 256) c += block_count(p < hi && key_of(p) >= t, red);
-      if (c >= need) T = t;
-    }
-    for (int p = lo + tid; p - tid < hi; p += 256)
-      above += block_count(p < hi && key_of(p) > T, red);
-  }
-  int ties = need - above;  // of the positions at T, the first so many
-  int base = 0, seen = 0;
-  for (int p0 = 0; p0 < n; p0 += 256) {
-    const int p = p0 + tid;
-    bool keep = p < n, tie = false;
-    if (!all && p >= lo && p < hi) {
-      const uint32_t key = need > 0 ? key_of(p) : 0u;
-      tie = need > 0 && key == T;
-      keep = need > 0 && key > T;
-    }
-    // ties before this position
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    __syncthreads();
-    if ((tid & 31) == 0) warp_base[tid >> 5] = __popc(tb);
-    __syncthreads();
-    int before = seen + __popc(tb & ((1u << (tid & 31)) - 1)), round = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < (tid >> 5)) before += warp_base[w];
-      round += warp_base[w];
-    }
-    seen += round;
-    if (tie && before < ties) keep = true;
-    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
-    __syncthreads();
-    if ((tid & 31) == 0) warp_base[tid >> 5] = __popc(kb);
-    __syncthreads();
-    int at = base + __popc(kb & ((1u << (tid & 31)) - 1));
-    round = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < (tid >> 5)) at += warp_base[w];
-      round += warp_base[w];
-    }
-    if (keep && at < m) kept[at] = p;
-    base += round;
-  }
-  for (int j = m + tid; j < a.budget; j += 256) kept[j] = -1;
-  __syncthreads();
-  // the rows, a warp each, eight at a time: kept[j] >= j and the list
-  // ascends, so in place a round's stores never touch a later round's rows
-  const bool in_place = a.dst_table == nullptr;
-  const int32_t* dtab = in_place ? a.block_table : a.dst_table;
-  const int dstride = in_place ? a.bt_stride : a.dst_stride;
-  constexpr int HALF = DH / 2, E = HALF / 32;
-  const int lane = tid & 31, w = tid >> 5;
-  for (int j0 = 0; j0 < m; j0 += 8) {
-    const int j = j0 + w;
-    S klo[E], khi[E], vlo[E], vhi[E];
-    float sc = 0.f;
-    int sb = -1, db = -1, p = 0;
-    if (j < m) {
-      p = __ldcg(kept + j);
-      sb = page_of(a.block_table, a.bt_stride, b, p, pool.num_blocks, a.err);
-      db = page_of(dtab, dstride, b, j, pool.num_blocks, a.err);
-    }
-    if (sb >= 0) {
-      const size_t r = (static_cast<size_t>(sb) * a.Hkv + h) * kPage + p % kPage;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = lane + 32 * e;
-        klo[e] = static_cast<const S*>(pool.k)[r * DH + i];
-        khi[e] = static_cast<const S*>(pool.k)[r * DH + HALF + i];
-        vlo[e] = static_cast<const S*>(pool.v)[r * DH + i];
-        vhi[e] = static_cast<const S*>(pool.v)[r * DH + HALF + i];
+  if (layer == 0 && h == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
+  if (tid < DH / 2) step[tid] = a.rope.step[tid];
+  if (tid < 12) count[tid / 4][tid % 4] = 0;
+  const int32_t* table = a.block_table + static_cast<size_t>(b) * a.bt_stride;
+  auto owns = [&](int j) { return j / ROUND % cluster == rank; };
+  int same = m;  // positions below stay where they are
+  if (n <= a.budget) {
+    for (int j = tid; j < a.budget; j += T)
+      if (owns(j)) kept[j] = j < m ? j : -1;
+  } else {
+    // ---- the weight of the last position that stays
+    const int lo = a.sinks, mid = n - a.recent - lo, need = a.budget - a.sinks - a.recent;
+    auto load_key = [&](int i) -> uint32_t {
+      const int p = lo + i;
+      const int blk = table[p / kPage];
+      if (blk < 0 || blk >= pool.num_blocks) {
+        record_error(a.err, PE_DEV_BAD_BLOCK);
+        return score_key(-INFINITY);
       }
-      sc = pool.scores[r];
+      return score_key(pool.scores[(static_cast<size_t>(blk) * a.Hkv + h) * kPage + p % kPage]);
+    };
+    const int held = min(mid, key_room);
+    if (need > 0)
+#pragma unroll 4
+      for (int i = tid; i < held; i += T) keys[i] = load_key(i);
+    auto key = [&](int i) { return i < held ? keys[i] : load_key(i); };
+    __syncthreads();
+    uint32_t floor = 0;   // count(key >= floor) >= need
+    bool exact = false;   // it is need
+    if (need > 0) {
+      for (int shift = 30, turn = 0; shift >= 0 && !exact; shift -= 2, turn = turn == 2 ? 0 : turn + 1) {
+        const uint32_t t1 = floor + (1u << shift), t2 = floor + (2u << shift),
+                       t3 = floor + (3u << shift);
+        int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll 4
+        for (int i = tid; i < held; i += T) {
+          const uint32_t k = keys[i];
+          c1 += k >= t1;
+          c2 += k >= t2;
+          c3 += k >= t3;
+        }
+        for (int i = held + tid; i < mid; i += T) {
+          const uint32_t k = load_key(i);
+          c1 += k >= t1;
+          c2 += k >= t2;
+          c3 += k >= t3;
+        }
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        if (lane == 0) {
+          atomicAdd(&count[turn][0], c1);
+          atomicAdd(&count[turn][1], c2);
+          atomicAdd(&count[turn][2], c3);
+        }
+        __syncthreads();
+        c1 = count[turn][0];
+        c2 = count[turn][1];
+        c3 = count[turn][2];
+        // the counters that the step after next adds to
+        if (tid < 3) count[turn == 0 ? 2 : turn - 1][tid] = 0;
+        const int c = c3 >= need ? c3 : c2 >= need ? c2 : c1 >= need ? c1 : -1;
+        floor = c3 >= need ? t3 : c2 >= need ? t2 : c1 >= need ? t1 : floor;
+        exact = c == need;
+      }
+    }
+    // stay: key > T, and the first `ties` of key == T
+    const uint32_t cut = exact ? floor - 1 : floor;
+    // ---- the list, in order: each thread an odd number of positions in a row
+    const int seg = ((mid + T - 1) / T) | 1;
+    const int i0 = min(tid * seg, mid), i1 = min(i0 + seg, mid);
+    int gt = 0, eq = 0;
+    if (need > 0)
+      for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key(i);
+        gt += k > cut;
+        eq += k == cut;
+      }
+    int g = gt, q = eq;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, g, o), y = __shfl_up_sync(0xffffffffu, q, o);
+      if (lane >= o) {
+        g += x;
+        q += y;
+      }
+    }
+    if (lane == 31) {
+      scan[0][warp] = g;
+      scan[1][warp] = q;
     }
     __syncthreads();
-    if (sb >= 0 && db >= 0) {
-      const size_t r = (static_cast<size_t>(db) * a.Hkv + h) * kPage + j % kPage;
+    int all_gt = 0;
+    g -= gt;
+    q -= eq;
+    for (int w = 0; w < WARPS; ++w) {
+      const int x = scan[0][w], y = scan[1][w];
+      all_gt += x;
+      g += w < warp ? x : 0;
+      q += w < warp ? y : 0;
+    }
+    const int ties = need - all_gt;
+    int at = lo + g + min(q, ties);
+    if (need > 0)
+      for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key(i);
+        const bool tie = k == cut;
+        if (k > cut || (tie && q < ties)) {
+          if (owns(at)) kept[at] = lo + i;
+          ++at;
+        }
+        q += tie;
+      }
+    for (int j = tid; j < lo; j += T)
+      if (owns(j)) kept[j] = j;
+    for (int j = m - a.recent + tid; j < m; j += T)
+      if (owns(j)) kept[j] = n - m + j;
+    if (IN_PLACE) same = lo;
+  }
+  // the list is this CTA's own for the rows that it moves
+  __syncthreads();
+  if (IN_PLACE) {
+    // no CTA of the cluster reads scores to choose by any more
+    if (cluster > 1) cluster_sync_all();
+  }
+  const int32_t* dtab =
+      IN_PLACE ? table : a.dst_table + static_cast<size_t>(b) * a.dst_stride;
+  const int dstride = IN_PLACE ? a.bt_stride : a.dst_stride;
+  const int group = tid / LANES, c = tid % LANES;
+  const bool high = c >= HALF;
+  // rows round + 2 group and + 1; in place from the first that may move
+  for (int round = (IN_PLACE ? same / ROUND / cluster * cluster + rank : rank) * ROUND;
+       round - rank * ROUND < m; round += ROUND * cluster) {
+    Move mv[2];
+    uint4 kv[2], vv[2];
+    float sc[2];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = lane + 32 * e;
-        if (a.rope.on && p != j) {
-          float c, s;
-          rope_cos_sin(a.rope.step[i], static_cast<long long>(j) - p, c, s);
-          float x1, x2;
-          if constexpr (sizeof(S) == 1) {
-            const uint32_t u = e4m3x2_to_f16x2(klo[e] | (static_cast<uint32_t>(khi[e]) << 8));
-            x1 = __half2float(__ushort_as_half(static_cast<unsigned short>(u & 0xffff)));
-            x2 = __half2float(__ushort_as_half(static_cast<unsigned short>(u >> 16)));
-          } else {
-            x1 = to_f(klo[e]);
-            x2 = to_f(khi[e]);
-          }
-          const float y1 = x1 * c - x2 * s, y2 = x2 * c + x1 * s;
-          if constexpr (sizeof(S) == 1) {
-            const uint16_t y = f32x2_to_e4m3x2(y1, y2);
-            klo[e] = static_cast<uint8_t>(y & 0xff);
-            khi[e] = static_cast<uint8_t>(y >> 8);
-          } else {
-            klo[e] = from_f<S>(y1);
-            khi[e] = from_f<S>(y2);
+    for (int x = 0; x < 2; ++x) {
+      const int j = round + 2 * group + x;
+      mv[x].src = mv[x].dst = -1;
+      mv[x].turn = 0;
+      if (j < m) {
+        const int p = __ldcg(kept + j);
+        if (!(IN_PLACE && p == j)) {
+          const int sb = table[p / kPage];
+          const int db = j / kPage < dstride ? dtab[j / kPage] : -2;
+          const bool s_ok = sb >= 0 && sb < pool.num_blocks, d_ok = db >= 0 && db < pool.num_blocks;
+          if (c == 0 && !(s_ok && d_ok))
+            record_error(a.err, db == -2 && j / kPage >= dstride ? PE_DEV_BAD_POSITION
+                                                                 : PE_DEV_BAD_BLOCK);
+          if (s_ok && d_ok) {
+            mv[x].src = (static_cast<long long>(sb) * a.Hkv + h) * kPage + p % kPage;
+            mv[x].dst = (static_cast<long long>(db) * a.Hkv + h) * kPage + j % kPage;
+            mv[x].turn = p - j;
           }
         }
-        static_cast<S*>(pool.k)[r * DH + i] = klo[e];
-        static_cast<S*>(pool.k)[r * DH + HALF + i] = khi[e];
-        static_cast<S*>(pool.v)[r * DH + i] = vlo[e];
-        static_cast<S*>(pool.v)[r * DH + HALF + i] = vhi[e];
       }
-      if (lane == 0) pool.scores[r] = sc;
+      kv[x] = vv[x] = make_uint4(0, 0, 0, 0);
+      sc[x] = 0.f;
+      if (mv[x].src >= 0) {
+        const size_t at = static_cast<size_t>(mv[x].src) * ROWB + c * 16;
+        kv[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(pool.k) + at));
+        vv[x] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(pool.v) + at));
+        if (c == 0) sc[x] = pool.scores[mv[x].src];
+      }
     }
+    if (IN_PLACE) {
+      if (cluster > 1) cluster_sync_all();
+      else __syncthreads();
+    }
+    if (a.rope.on) {
+      // lanes of the low half take the pairs of the first row, the others
+      // the second's: a lane's other row's chunk is its partner's missing one
+      const uint4 got = shfl_xor16(high ? kv[0] : kv[1], HALF);
+      uint4 x1 = high ? got : kv[0], x2 = high ? kv[1] : got;
+      const int turn = high ? mv[1].turn : mv[0].turn;
+      if (turn != 0) {
+        constexpr int N = Chunk<S>::N;
+        float u[N], v[N];
+        Chunk<S>::get(x1, u);
+        Chunk<S>::get(x2, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          float cs, sn;
+          rope_turn<sizeof(S) != 4>(step[(c % HALF) * N + e], -static_cast<long long>(turn), cs, sn);
+          const float y = u[e] * cs - v[e] * sn;
+          v[e] = v[e] * cs + u[e] * sn;
+          u[e] = y;
+        }
+        x1 = Chunk<S>::put(u);
+        x2 = Chunk<S>::put(v);
+      }
+      const uint4 back = shfl_xor16(high ? x1 : x2, HALF);
+      kv[0] = high ? back : x1;
+      kv[1] = high ? x2 : back;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (mv[x].dst >= 0) {
+        const size_t at = static_cast<size_t>(mv[x].dst) * ROWB + c * 16;
+        *reinterpret_cast<uint4*>(static_cast<char*>(pool.k) + at) = kv[x];
+        *reinterpret_cast<uint4*>(static_cast<char*>(pool.v) + at) = vv[x];
+        if (c == 0) pool.scores[mv[x].dst] = sc[x];
+      }
   }
-  __syncthreads();
+  // positions that hold nothing any more
+  if (rank != 0) return;
   const int page_end = (m + kPage - 1) / kPage * kPage;
-  const int end = in_place ? max(n, page_end) : page_end;
-  for (int j = m + tid; j < end; j += 256) {
-    const int db = page_of(dtab, dstride, b, j, pool.num_blocks, a.err);
+  const int end = IN_PLACE ? max(n, page_end) : page_end;
+  for (int j = m + tid; j < end; j += T) {
+    const int db = page_of(dtab - static_cast<size_t>(b) * dstride, dstride, b, j, pool.num_blocks,
+                           a.err);
     if (db >= 0) pool.scores[(static_cast<size_t>(db) * a.Hkv + h) * kPage + j % kPage] = 0.f;
   }
 }
 
+template <typename S, int DH, bool IN_PLACE>
+static cudaError_t launch_evict_one(const EvictArgs& a, int n_layers, int dev, int sms,
+                                    cudaStream_t s) {
+  // Clusters while the rows alone leave SMs idle (two CTAs an SM).
+  const long long rows = static_cast<long long>(a.B) * a.Hkv * n_layers;
+  int cluster = 1;
+  while (cluster < 8 && rows * cluster * 2 <= 2LL * sms) cluster *= 2;
+  const long long room = std::min<long long>(static_cast<long long>(a.bt_stride) * kPage, kMostKeys);
+  static std::atomic<uint64_t> done{0};
+  if (dev >= 64 || !((done.load(std::memory_order_relaxed) >> dev) & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<S, DH, IN_PLACE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMostKeys * 4);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done.fetch_or(1ull << dev);
+  }
+  return launch_pdl_cluster(kv_evict_kernel<S, DH, IN_PLACE>,
+                            dim3(static_cast<unsigned>(a.B) * a.Hkv * cluster, n_layers),
+                            dim3(kEvictThreads), static_cast<size_t>(room) * 4, s, cluster, a,
+                            cluster, static_cast<int>(room));
+}
+
 template <typename S>
-static cudaError_t launch_evict(const EvictArgs& a, int n_layers, int dh, cudaStream_t s) {
-  const dim3 grid(a.B * a.Hkv, n_layers);
-  if (dh == 64) return launch_pdl(kv_evict_kernel<S, 64>, grid, dim3(256), 0, s, a);
-  return launch_pdl(kv_evict_kernel<S, 128>, grid, dim3(256), 0, s, a);
+static cudaError_t launch_evict(const EvictArgs& a, int n_layers, int dh, int dev, int sms,
+                                cudaStream_t s) {
+  if (dh == 64)
+    return a.dst_table ? launch_evict_one<S, 64, false>(a, n_layers, dev, sms, s)
+                       : launch_evict_one<S, 64, true>(a, n_layers, dev, sms, s);
+  return a.dst_table ? launch_evict_one<S, 128, false>(a, n_layers, dev, sms, s)
+                     : launch_evict_one<S, 128, true>(a, n_layers, dev, sms, s);
 }
 
 }  // namespace pe
@@ -261,9 +398,12 @@ extern "C" pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int3
     a.pool[l] = CachePool{pools[l].k, pools[l].v, pools[l].scores, pools[l].num_blocks};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int dh = pools[0].head_dim;
-  cudaError_t e;
-  if (pools[0].dtype == PE_KV_F32) e = launch_evict<float>(a, n_layers, dh, s);
-  else if (pools[0].dtype == PE_KV_BF16) e = launch_evict<bf16>(a, n_layers, dh, s);
-  else e = launch_evict<uint8_t>(a, n_layers, dh, s);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return PE_ERR_CUDA;
+  if (pools[0].dtype == PE_KV_F32) e = launch_evict<float>(a, n_layers, dh, dev, sms, s);
+  else if (pools[0].dtype == PE_KV_BF16) e = launch_evict<bf16>(a, n_layers, dh, dev, sms, s);
+  else e = launch_evict<uint8_t>(a, n_layers, dh, dev, sms, s);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
