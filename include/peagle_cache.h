@@ -161,7 +161,8 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  * sinks or recent < 0 or together above budget, rope_theta negative or not
  * finite, pools that differ or have no scores, a null or misaligned pointer,
  * new_lens == seq_lens.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128,
- * more than 2^31 - 1 entries of kept. */
+ * more than 2^31 - 1 entries of kept, budget past 2^30 or bt_stride past
+ * 2^26. */
 pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                       int32_t budget, int32_t sinks, int32_t recent, float rope_theta,
