@@ -14,10 +14,11 @@
 //
 // The weight is found by bisection of its 32 bits, two bits a step: the
 // scores lie in shared memory as integers of the same order, and each step
-// counts those at or above three candidates.  Its time does not depend on the
+// counts those at or above three candidates.  No step's time depends on the
 // values (a histogram's does: equal scores, such as the zeros of positions
-// that were never attended, meet in one counter), and it ends as soon as a
-// count is right.  Every CTA of a cluster chooses for itself: the scores are
+// that were never attended, meet in one counter).  It ends as soon as a count
+// is right, or when so few scores are left between two candidates that each
+// of them can be ranked among the others.  Every CTA of a cluster chooses for itself: the scores are
 // read again from L2, and nothing is exchanged.
 //
 // In place, row j is written where an earlier-listed row may still lie, never
@@ -78,6 +79,7 @@ __device__ __forceinline__ int page_of(const int32_t* table, int stride, int b, 
 
 constexpr int kEvictThreads = 512;
 constexpr int kMostKeys = 24576;  // scores that are held in shared memory
+constexpr int kRanked = 128;      // keys that are ranked at once
 
 // A row on its way: its number in the pool where it goes (-1: nowhere) and by
 // how much its key turns.
@@ -117,6 +119,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   __shared__ uint64_t step[DH / 2];
   __shared__ int4 found[2][WARPS];  // counts of a bisection step, by warp
   __shared__ int scan[2][WARPS];
+  __shared__ uint32_t ranked[kRanked], cut_key;
+  __shared__ int n_ranked;
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,6 +133,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
       a.kept + ((static_cast<size_t>(layer) * a.B + b) * a.Hkv + h) * static_cast<size_t>(a.budget);
   if (layer == 0 && h == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
   if (tid < DH / 2) step[tid] = a.rope.step[tid];
+  if (tid == 0) n_ranked = 0;
   const int32_t* table = a.block_table + static_cast<size_t>(b) * a.bt_stride;
   auto owns = [&](int j) { return (j / ROUND & (cluster - 1)) == rank; };
   int same = m;  // positions below stay where they are
@@ -159,10 +164,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
       for (int p = tid * 4; p < held; p += T * 4)
         *reinterpret_cast<uint4*>(keys + p) = load_keys(p);
     __syncthreads();
-    uint32_t floor = 0;  // count(key >= floor) >= need
-    bool exact = false;  // it is need
+    // Bisection: count(key >= floor) = at_floor >= need > above = count(key
+    // >= floor + 2^shift).  Once few keys lie between, they are ranked.
+    uint32_t floor = 0;
+    int at_floor = hi - lo, above = 0, shift = 32;
     if (need > 0) {
-      for (int shift = 30, odd = 0; shift >= 0 && !exact; shift -= 2, odd ^= 1) {
+      for (int odd = 0; shift > 0 && at_floor != need && at_floor - above > kRanked; odd ^= 1) {
+        shift -= 2;
         const uint32_t t1 = floor + (1u << shift), t2 = floor + (2u << shift),
                        t3 = floor + (3u << shift);
         int c1 = 0, c2 = 0, c3 = 0;
@@ -183,13 +191,54 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
         c1 = __reduce_add_sync(0xffffffffu, f.x);
         c2 = __reduce_add_sync(0xffffffffu, f.y);
         c3 = __reduce_add_sync(0xffffffffu, f.z);
-        const int c = c3 >= need ? c3 : c2 >= need ? c2 : c1 >= need ? c1 : -1;
-        floor = c3 >= need ? t3 : c2 >= need ? t2 : c1 >= need ? t1 : floor;
-        exact = c == need;
+        if (c3 >= need) {
+          floor = t3;
+          at_floor = c3;
+        } else if (c2 >= need) {
+          floor = t2;
+          at_floor = c2;
+          above = c3;
+        } else if (c1 >= need) {
+          floor = t1;
+          at_floor = c1;
+          above = c2;
+        } else {
+          above = c1;
+        }
       }
     }
     // stay: key > cut, and the first `ties` of key == cut
-    const uint32_t cut = exact ? floor - 1 : floor;
+    uint32_t cut = at_floor == need ? floor - 1 : floor;
+    if (need > 0 && at_floor != need && shift > 0) {
+      auto add = [&](uint32_t k) {
+        if (k != 0 && (shift == 32 || k - floor < 1u << shift)) {
+          const int i = atomicAdd(&n_ranked, 1);
+          if (i < kRanked) ranked[i] = k;
+        }
+      };
+      auto add4 = [&](const uint4& k) {
+        add(k.x);
+        add(k.y);
+        add(k.z);
+        add(k.w);
+      };
+      for (int p = tid * 4; p < held; p += T * 4) add4(*reinterpret_cast<const uint4*>(keys + p));
+      for (int p = held + tid * 4; p < hi; p += T * 4) add4(load_keys(p));
+      __syncthreads();
+      const int count = at_floor - above;
+      if (tid < count) {
+        const uint32_t k = ranked[tid];
+        int more = 0, same_key = 0;
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+          more += ranked[i] > k;
+          same_key += ranked[i] == k;
+        }
+        if (above + more < need && need <= above + more + same_key) cut_key = k;
+      }
+      __syncthreads();
+      cut = cut_key;
+    }
     // ---- the list, in order: each thread an odd number of positions in a row
     auto key = [&](int p) -> uint32_t {
       if (p < held) return keys[p];
@@ -298,15 +347,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   // in place from the first round that may move anything
   const int stride = ROUND * cluster;
   const int first = (IN_PLACE ? same / stride * stride : 0) + rank * ROUND;
-  int from[2];
+  int from[AHEAD + 1][2];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    from[0] = entry(first + i * stride, 0);
-    from[1] = entry(first + i * stride, 1);
-    issue(first + i * stride, from, i);
-  }
-  from[0] = entry(first + AHEAD * stride, 0);
-  from[1] = entry(first + AHEAD * stride, 1);
+  for (int i = 0; i <= AHEAD; ++i)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) from[i][x] = entry(first + i * stride, x);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) issue(first + i * stride, from[i], i);
   int slot = 0;
   for (int round = first; round - rank * ROUND < m; round += stride) {
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
@@ -360,9 +407,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
         if (c == 0) pool.scores[mv[x].dst] = weights[slot * ROUND + 2 * group + x];
       }
     __syncwarp();  // the slot is free
-    issue(round + AHEAD * stride, from, slot);
-    from[0] = entry(round + (AHEAD + 1) * stride, 0);
-    from[1] = entry(round + (AHEAD + 1) * stride, 1);
+    issue(round + AHEAD * stride, from[AHEAD], slot);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) from[AHEAD][x] = entry(round + (AHEAD + 1) * stride, x);
     if (++slot == AHEAD) slot = 0;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
