@@ -87,9 +87,12 @@ pe_status pe_kv_append(const pe_kv_pool* pool, int32_t T, int32_t B, int32_t n_h
                        void* q_out, int64_t q_out_stride, int32_t* err, void* stream);
 
 /* Bytes of workspace of a pe_attn_decode call of B requests on the current
- * device (the lengths do not matter); 0 on a bad argument. */
+ * device; 0 on a bad argument.  bt_stride 0: what every call needs (the
+ * lengths do not matter).  bt_stride > 0: with room for the logits of a table
+ * of that width, at most 1 GiB of them, which a call with accumulate keeps
+ * there instead of working them out twice. */
 int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
-                                 int32_t head_dim);
+                                 int32_t head_dim, int32_t bt_stride);
 
 /* Attention of one new token per request over its cached positions.
  *
@@ -110,8 +113,8 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * `*_stride` elements apart, heads contiguous, rows 16-byte aligned.  lse:
  * NULL, or fp32 [B, n_heads].  block_table [B, bt_stride], seq_lens [B].
  * Sums, maxima and weights are held in fp32.  workspace: 16-byte aligned,
- * workspace_bytes at least pe_attn_decode_workspace(); contents need not be
- * set and do not carry over; calls that may overlap need one each.
+ * workspace_bytes at least pe_attn_decode_workspace(.., 0); contents need not
+ * be set and do not carry over; calls that may overlap need one each.
  * Device errors: PE_DEV_BAD_POSITION (seq_lens[b] < 0 or past the table:
  * read as 0 or the table's end), PE_DEV_BAD_BLOCK (the page's positions are
  * left out).

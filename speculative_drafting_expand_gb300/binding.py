@@ -132,7 +132,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pe_status_string.restype = ctypes.c_char_p
     lib.pe_kv_append.argtypes = [P(pe_kv_pool), _i32, _i32, _i32, ctypes.c_float, _vp, _i64, _vp,
                                  _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
-    lib.pe_attn_decode_workspace.argtypes = [_i32, _i32, _i32, _i32]
+    lib.pe_attn_decode_workspace.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.pe_attn_decode.argtypes = [P(pe_kv_pool), _i32, _i32, ctypes.c_float, _vp, _i64, _vp,
                                    _i32, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp]
     lib.pe_kv_evict.argtypes = [_i32, P(pe_kv_pool), _i32, _vp, _i32, _vp, _i32, _i32, _i32,
@@ -507,7 +507,7 @@ class KvPool:
         self.k, self.v, self.scores, self.device = k, v, scores, k.device
         self.torch, self.i32, self.lib = torch, torch.int32, lib()
         self.index = k.get_device()  # -1: not on a GPU
-        self._workspace = {}         # sizes by (requests, query heads)
+        self._workspace = {}         # sizes by (requests, query heads, table width)
         self.num_blocks, self.n_kv_heads, _, self.head_dim = k.shape
         self.dtype = kinds[k.dtype]
         self.act_dtype = torch.float32 if self.dtype == PE_KV_F32 else torch.bfloat16
@@ -610,9 +610,13 @@ def pe_kv_append(pool: KvPool, q, k, v, pos, block_table, rope_theta: float = 0.
     return q_out
 
 
-def pe_attn_decode_workspace(B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
-    """Bytes of workspace of a pe_attn_decode call on the current device."""
-    n = lib().pe_attn_decode_workspace(B, n_heads, n_kv_heads, head_dim)
+def pe_attn_decode_workspace(B: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                             pages: int = 0) -> int:
+    """Bytes of workspace of a pe_attn_decode call on the current device; with
+    `pages`, the block table's width, room for the logits of a call that
+    accumulates (it then works them out once instead of twice)."""
+    _cache_ints(B=B, n_heads=n_heads, pages=pages)
+    n = lib().pe_attn_decode_workspace(B, n_heads, n_kv_heads, head_dim, pages)
     if n <= 0:
         raise ValueError("pe_attn_decode_workspace: bad sizes")
     return n
@@ -643,11 +647,12 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
         raise ValueError(f"lse must be contiguous float32 [{B}, {n_heads}]")
     os_ = _cache_rows(pool, "out", out, B, n_heads)
     if workspace is None:
-        n = pool._workspace.get((B, n_heads))
+        room = pages if accumulate else 0
+        n = pool._workspace.get((B, n_heads, room))
         if n is None:
             with torch.cuda.device(pool.index):
-                n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh)
-            pool._workspace[B, n_heads] = n
+                n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh, room)
+            pool._workspace[B, n_heads, room] = n
         workspace = _cache_empty(pool, n, torch.uint8, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != pool.index:
         raise ValueError("workspace must be contiguous on the pool's device")

@@ -91,6 +91,9 @@ struct DecodeArgs {
   float* lse;      // caller's, or NULL
   int* err;
   // workspace
+  float* stash;    // logits of the line's first stash_pages pages, as the
+                   // lanes hold them
+  int stash_pages;
   float* lse_w;    // [B, Hq], in units of ln 2
   int4* meta;      // [grid]: item and flags of the CTA's first and last partial
   float* part;     // [grid][2][REC]
@@ -214,6 +217,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -254,22 +260,29 @@ __device__ __forceinline__ uint32_t v_place(int r, int c) {
   else return static_cast<uint32_t>(r * SH::ROWB + (c ^ ((r & 3) << 1)) * 16);
 }
 
-// 32 lanes copy 512 bytes in a row at a time.
+// 32 lanes copy 512 bytes in a row at a time.  Positions v_lo <= offset < v_hi
+// of the page are attended; the others read as zeros whatever lies there.
 template <class SH, bool WITH_V>
-__device__ __forceinline__ void copy_page(uint32_t stage, const CachePool& pool, int blk, int Hkv,
-                                          int hk, int v_lo, int v_hi, int lane) {
-  // positions v_lo <= offset < v_hi of the page are attended; the others
-  // read as zeros whatever lies there
+__device__ __forceinline__ void copy_page(uint32_t stage, const CachePool& pool, size_t page,
+                                          int v_lo, int v_hi, int lane) {
   constexpr int CPR = SH::ROWB / 16;  // chunks a row
-  const size_t base = (static_cast<size_t>(blk) * Hkv + hk) * SH::PAGEB + lane * 16;
+  const size_t base = page * SH::PAGEB + lane * 16;
   const char* kp = static_cast<const char*>(pool.k) + base;
   const char* vp = static_cast<const char*>(pool.v) + base;
+  const bool whole = v_lo <= 0 && v_hi >= kPage;
 #pragma unroll
   for (int i = 0; i < SH::CH; ++i) {
     const int r = (i * 32 + lane) / CPR, c = lane % CPR;
-    const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
-    cp_async16(stage + k_place<SH>(r, c), kp + i * 512, n);
-    if (WITH_V) cp_async16(stage + SH::PAGEB + v_place<SH>(r, c), vp + i * 512, n);
+    const uint32_t k_at = stage + k_place<SH>(r, c);
+    const uint32_t v_at = stage + SH::PAGEB + v_place<SH>(r, c);
+    if (whole) {
+      cp_async16(k_at, kp + i * 512);
+      if (WITH_V) cp_async16(v_at, vp + i * 512);
+    } else {
+      const uint32_t n = r >= v_lo && r < v_hi ? 16u : 0u;
+      cp_async16(k_at, kp + i * 512, n);
+      if (WITH_V) cp_async16(v_at, vp + i * 512, n);
+    }
   }
 }
 
@@ -279,34 +292,51 @@ struct Feeder {
   static constexpr int STAGES = WITH_V ? SH::STAGES : SH::S_STAGES;
   static constexpr int STRIDE = WITH_V ? 2 * SH::PAGEB : SH::PAGEB;
   Place pl;
-  int left;        // units still to copy
-  int ids;         // this lane's page of the 32 from ids_at on
-  int ids_at;      // -1: none
+  int hk;        // kv head of the place
+  int left;      // units still to copy
+  int ids;       // this lane's page of the 32 from ids_at on
+  int ids_at;
   int stage;
-  uint32_t bad;    // stages whose page is none
+  uint32_t bad;  // stages whose page is none
 
+  __device__ __forceinline__ void start(const DecodeArgs& a, const Place& at, int tiles, int count,
+                                        int lane) {
+    pl = at;
+    hk = pl.hh / tiles;
+    left = count;
+    stage = 0;
+    bad = 0;
+    fetch(a, lane);
+  }
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, int lane) {
+    ids_at = pl.p;
+    ids = -1;
+    if (pl.p + lane < pl.s.pe)
+      ids = a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + lane];
+  }
   // heads: items a request; tiles: items a kv head
   __device__ __forceinline__ void step(const DecodeArgs& a, int heads, int tiles, uint32_t ring,
                                        int lane, bool record) {
     if (left > 0) {
       if (pl.p == pl.s.pe) {
         next_item(a, heads, pl);
-        ids_at = -1;
-      }
-      if (ids_at < 0 || pl.p >= ids_at + 32) {
-        ids_at = pl.p;
-        ids = -1;
-        if (pl.p + lane < pl.s.pe)
-          ids = a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + lane];
+        hk = pl.hh / tiles;
+        fetch(a, lane);
+      } else if (pl.p - ids_at == 32) {
+        fetch(a, lane);
       }
       const int blk = __shfl_sync(0xffffffffu, ids, pl.p - ids_at);
-      const bool ok = blk >= 0 && blk < a.pool.num_blocks;
-      if (!ok && record && lane == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
-      bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
       const int first = pl.p * kPage;
-      copy_page<SH, WITH_V>(ring + stage * STRIDE, a.pool, ok ? blk : 0, a.Hkv,
-                                    pl.hh / tiles, ok ? pl.s.lo - first : kPage,
-                                    ok ? pl.s.n - first : 0, lane);
+      const uint32_t at = ring + stage * STRIDE;
+      if (static_cast<uint32_t>(blk) < static_cast<uint32_t>(a.pool.num_blocks)) {
+        bad &= ~(1u << stage);
+        copy_page<SH, WITH_V>(at, a.pool, static_cast<size_t>(blk) * a.Hkv + hk, pl.s.lo - first,
+                              pl.s.n - first, lane);
+      } else {
+        if (record && lane == 0) record_error(a.err, PE_DEV_BAD_BLOCK);
+        bad |= 1u << stage;
+        copy_page<SH, WITH_V>(at, a.pool, 0, kPage, 0, lane);  // zeros
+      }
       ++pl.p;
       --left;
     }
@@ -373,26 +403,30 @@ template <int DT, int DH, int GT>
 struct QueryTile {
   static constexpr int STEPS = DH / 16;  // k steps of 16 elements
   uint32_t a[GT][STEPS][2];
-  float factor[GT];  // logit = sum * factor (units of ln 2)
+  float factor[GT];  // logit = sum * factor (units of ln 2); positive
 
   __device__ __forceinline__ void load(const DecodeArgs& A, int b, int h0, int rows, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    // the scale's sign goes to q (and all of it if it is 0), so that the
+    // largest sum is the largest logit
+    const uint32_t sign = A.scale < 0.f ? 0x80008000u : 0u;
+    const float scale = A.scale == 0.f ? 1.f : fabsf(A.scale);
 #pragma unroll
     for (int x = 0; x < GT; ++x) {
       const int r = g + 8 * x;
-      const bool on = r < rows;
+      const bool on = r < rows && A.scale != 0.f;
       const bf16* q = static_cast<const bf16*>(A.q) + static_cast<size_t>(b) * A.q_stride +
                       static_cast<size_t>(h0 + (on ? r : 0)) * DH;
-      factor[x] = A.scale;
+      factor[x] = scale;
       if constexpr (DT == PE_KV_BF16) {
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
           uint4 v = *reinterpret_cast<const uint4*>(q + (t + 4 * i) * 8);
-          if (!on) v = make_uint4(0, 0, 0, 0);
-          a[x][2 * i][0] = v.x;
-          a[x][2 * i][1] = v.y;
-          a[x][2 * i + 1][0] = v.z;
-          a[x][2 * i + 1][1] = v.w;
+          if (!on) v = make_uint4(sign, sign, sign, sign);
+          a[x][2 * i][0] = v.x ^ sign;
+          a[x][2 * i][1] = v.y ^ sign;
+          a[x][2 * i + 1][0] = v.z ^ sign;
+          a[x][2 * i + 1][1] = v.w ^ sign;
         }
       } else {
         uint32_t w[STEPS][2];
@@ -404,7 +438,7 @@ struct QueryTile {
           const uint32_t z[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            w[4 * i + e / 2][e & 1] = on ? z[e] : 0u;
+            w[4 * i + e / 2][e & 1] = on ? z[e] ^ sign : 0u;
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(z[e] << 16)),
                                    fabsf(__uint_as_float(z[e] & 0xffff0000u))));
           }
@@ -425,10 +459,9 @@ struct QueryTile {
     }
   }
 
-  // Logits of a page (units of ln 2): z[x][j][e], head g + 8 x, position
-  // key_of(j, 2 t + e).
+  // Sums q.k of a page: z[x][j][e], head g + 8 x, position key_of(j, 2 t + e).
   template <class SH>
-  __device__ __forceinline__ void logits(uint32_t stage, int lane, float (&z)[GT][2][2]) const {
+  __device__ __forceinline__ void sums(uint32_t stage, int lane, float (&z)[GT][2][2]) const {
     float c[2][4] = {};
     constexpr int KI = SH::CH / 2;
 #pragma unroll
@@ -456,7 +489,7 @@ struct QueryTile {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) z[x][j][e] = c[j][2 * x + e] * factor[x];
+        for (int e = 0; e < 2; ++e) z[x][j][e] = c[j][2 * x + e];
   }
 };
 
@@ -484,13 +517,16 @@ struct MmaTile {
 
   // NP pages in a row, at `stage`; positions v_lo <= i < v_hi of them are
   // attended, and bit n of `none` takes out page n.
+  // stash: where the logits of the first stash_n pages go, LOGITS floats a
+  // lane and page.
+  static constexpr int LOGITS = 4 * GT;
   template <int NP>
   __device__ __forceinline__ void pages(const uint32_t (&stage)[NP], int v_lo, int v_hi,
-                                        uint32_t none, char*, int lane) {
+                                        uint32_t none, char*, float* stash, int stash_n, int lane) {
     const int t = lane & 3;
     float z[NP][GT][2][2];
 #pragma unroll
-    for (int n = 0; n < NP; ++n) q.template logits<SH>(stage[n], lane, z[n]);
+    for (int n = 0; n < NP; ++n) q.template sums<SH>(stage[n], lane, z[n]);
     if (v_lo > 0 || v_hi < NP * kPage || none) {
 #pragma unroll
       for (int n = 0; n < NP; ++n)
@@ -504,6 +540,14 @@ struct MmaTile {
               for (int x = 0; x < GT; ++x) z[n][x][j][e] = -INFINITY;
           }
     }
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      if (n < stash_n)
+#pragma unroll
+        for (int x = 0; x < GT; ++x)
+          *reinterpret_cast<float4*>(stash + ((n * GT + x) * 32 + lane) * 4) =
+              make_float4(z[n][x][0][0] * q.factor[x], z[n][x][0][1] * q.factor[x],
+                          z[n][x][1][0] * q.factor[x], z[n][x][1][1] * q.factor[x]);
     float top[GT];
     bool grow = false;
 #pragma unroll
@@ -514,7 +558,7 @@ struct MmaTile {
         top[x] = fmax3(top[x], fmaxf(z[n][x][0][0], z[n][x][0][1]),
                        fmaxf(z[n][x][1][0], z[n][x][1][1]));
       top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * q.factor[x];
       grow |= top[x] > m[x];
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -542,7 +586,8 @@ struct MmaTile {
       for (int n = 0; n < NP; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float p0 = fast_exp2(z[n][x][j][0] - base), p1 = fast_exp2(z[n][x][j][1] - base);
+          const float p0 = fast_exp2(fmaf(z[n][x][j][0], q.factor[x], -base));
+          const float p1 = fast_exp2(fmaf(z[n][x][j][1], q.factor[x], -base));
           l[x] += p0 + p1;
           split2<DT>(p0, p1, hi[n][x][j], lo[n][x][j]);
         }
@@ -764,9 +809,11 @@ struct F32Tile {
       }
   }
 
+  static constexpr int LOGITS = R / 2;
   template <int NP>
   __device__ __forceinline__ void pages(const uint32_t (&at)[NP], int v_lo, int v_hi,
-                                        uint32_t none, char* scratch, int lane) {
+                                        uint32_t none, char* scratch, float* stash, int stash_n,
+                                        int lane) {
     static_assert(NP == 1, "one page at a time");
     const uint32_t stage = at[0];
     if (none) v_lo = kPage;
@@ -790,6 +837,10 @@ struct F32Tile {
         top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], s));
       grow |= top[x] > m[x];
     }
+    if (stash_n > 0)
+#pragma unroll
+      for (int x = 0; x < R / 4; ++x)
+        *reinterpret_cast<float2*>(stash + (x * 32 + lane) * 2) = make_float2(z[x][0], z[x][1]);
     const bool scale = __any_sync(0xffffffffu, grow);
     if (scale) {
 #pragma unroll
@@ -1011,12 +1062,8 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   if (mine.count > 0) {
     Place pl = place_of<THREADS>(a, ln, heads, prefix, cta.first + mine.first);
     Feeder<SH, true> feed;
-    feed.pl = pl;
-    feed.left = mine.count;
-    feed.ids_at = -1;
-    feed.ids = -1;
-    feed.stage = 0;
-    feed.bad = 0;
+    feed.start(a, pl, a.tiles, mine.count, lane);
+    int unit = cta.first + mine.first;  // of the page that is taken next
 #pragma unroll 1
     for (int i = 0; i < SH::STAGES; ++i) feed.step(a, heads, a.tiles, ring, lane, true);
     int left = mine.count, stage = 0;
@@ -1040,7 +1087,10 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
           if (++stage == SH::STAGES) stage = 0;
         }
         const int first = pl.p * kPage;
-        tile.template pages<NP>(at, pl.s.lo - first, pl.s.n - first, none, scratch, lane);
+        tile.template pages<NP>(at, pl.s.lo - first, pl.s.n - first, none, scratch,
+                                a.stash + static_cast<size_t>(unit) * Tile::LOGITS * 32,
+                                a.stash_pages - unit, lane);
+        unit += NP;
         __syncwarp();
 #pragma unroll
         for (int n = 0; n < NP; ++n) feed.step(a, heads, a.tiles, ring, lane, true);
@@ -1242,14 +1292,38 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
            make_float4(O.x * f, O.y * f, O.z * f, O.w * f));
 }
 
-// Weights: the logits of the pages once more, now that lse is known; a page
-// of a kv head belongs to one warp, which sums its query heads in order.
+// Adds the weights of a page's positions to the pool's scores.  v[i]: this
+// lane's part of the sum at position pos[i] of four, joined over the eight
+// lanes of equal t; each lane ends with one position's sum.
+__device__ __forceinline__ float join_heads(const float (&v)[4], int g) {
+  // three exchanges halve the four values, then the two, then add the last
+  const float a0 = g & 4 ? v[2] : v[0], a1 = g & 4 ? v[3] : v[1];
+  const float b0 = g & 4 ? v[0] : v[2], b1 = g & 4 ? v[1] : v[3];
+  const float c0 = a0 + __shfl_xor_sync(0xffffffffu, b0, 16);
+  const float c1 = a1 + __shfl_xor_sync(0xffffffffu, b1, 16);
+  const float d = (g & 2 ? c1 : c0) + __shfl_xor_sync(0xffffffffu, g & 2 ? c0 : c1, 8);
+  return d + __shfl_xor_sync(0xffffffffu, d, 4);  // value (g >> 1): j = g / 4, e = g / 2 % 2
+}
+__device__ __forceinline__ void add_scores(const DecodeArgs& a, const Span& s, int hk, int blk,
+                                           int p, int r, bool mine, float v) {
+  const int at = p * kPage + r;
+  if (mine && blk >= 0 && blk < a.pool.num_blocks && at >= s.lo && at < s.n)
+    atomicAdd(a.pool.scores + (static_cast<size_t>(blk) * a.Hkv + hk) * kPage + r, v);
+}
+
+// Weights, now that lse is known: of the pages whose logits the first kernel
+// left in the workspace from those, of the others from the logits once more.
+// A page of a kv head belongs to one warp, which sums its query heads in
+// order; the additions are reductions in L2 because requests may share pages.
 template <int DT, int DH, int GT>
 __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
     attn_scores_kernel(const __grid_constant__ DecodeArgs a) {
   using SH = DecodeShape<DT, DH, GT>;
   using Feed = Feeder<SH, false>;
+  using Tile = typename TileOf<DT, DH, GT>::type;
+  constexpr bool F32 = DT == PE_KV_F32;
   constexpr int W = SH::WARPS, THREADS = W * 32;
+  constexpr int LH = F32 ? SH::ROWS / 4 : GT;  // heads a lane
   extern __shared__ __align__(128) char smem[];
   __shared__ int prefix[THREADS];
   grid_dep_wait();
@@ -1262,78 +1336,147 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
   char* scratch = smem + W * SH::S_RING + w * SH::SCRATCH;
   const uint32_t ring = smem_u32(smem + w * SH::S_RING);
   Place pl = place_of<THREADS>(a, ln, a.Hkv, prefix, mine.first);
+  // a lane's row of the tile and, of the lanes that hold a sum, its position
+  auto head_of = [&](int x) { return F32 ? t * LH + x : g + 8 * x; };
+  const int r = F32 ? key_of(t & 1, g) : key_of(g >> 2, 2 * t + ((g >> 1) & 1));
+  const bool adds = F32 ? t < 2 : (g & 1) == 0;
+  float lse[LH];
+  auto load_lse = [&](int r0) {
+#pragma unroll
+    for (int x = 0; x < LH; ++x) {
+      // a row without weight, or no row
+      lse[x] = -INFINITY;
+      if (head_of(x) < min(SH::ROWS, a.G - r0))
+        lse[x] = __ldcg(a.lse_w + static_cast<size_t>(pl.b) * a.Hq + pl.hh * a.G + r0 + head_of(x));
+    }
+  };
+  auto weight = [&](float z, int x) {
+    return lse[x] == -INFINITY ? 0.f : fast_exp2(z - lse[x]);
+  };
+  // ---- logits that are there
+  int left = min(mine.count, max(0, a.stash_pages - mine.first));
+  const int over = mine.count - left;
+  if (left > 0) {
+    const float* stash = a.stash + static_cast<size_t>(mine.first) * Tile::LOGITS * 32;
+    load_lse(0);
+    while (left > 0) {
+      if (pl.p == pl.s.pe) {
+        next_item(a, a.Hkv, pl);
+        load_lse(0);
+      }
+      const int run = min(min(pl.s.pe - pl.p, left), 32);
+      const int ids =
+          lane < run ? a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + lane] : -1;
+      constexpr int U = 4;  // pages in flight
+#pragma unroll 1
+      for (int i = 0; i < run; i += U) {
+        float z[U][Tile::LOGITS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* from = stash + static_cast<size_t>(min(i + u, run - 1)) * Tile::LOGITS * 32;
+          if constexpr (F32) {
+#pragma unroll
+            for (int x = 0; x < LH; ++x) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(from + (x * 32 + lane) * 2));
+              z[u][2 * x] = v.x;
+              z[u][2 * x + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < GT; ++x) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + (x * 32 + lane) * 4));
+              z[u][4 * x] = v.x;
+              z[u][4 * x + 1] = v.y;
+              z[u][4 * x + 2] = v.z;
+              z[u][4 * x + 3] = v.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float sum;
+          if constexpr (F32) {
+            float v[2] = {0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < LH; ++x)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) v[j] += weight(z[u][2 * x + j], x);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              v[j] += __shfl_xor_sync(0xffffffffu, v[j], 1);
+              v[j] += __shfl_xor_sync(0xffffffffu, v[j], 2);
+            }
+            sum = t & 1 ? v[1] : v[0];
+          } else {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < GT; ++x)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] += weight(z[u][4 * x + k], x);
+            sum = join_heads(v, g);
+          }
+          const int blk = __shfl_sync(0xffffffffu, ids, min(i + u, 31));
+          add_scores(a, pl.s, pl.hh, blk, pl.p + i + u, r, adds && i + u < run, sum);
+        }
+      }
+      stash += static_cast<size_t>(run) * Tile::LOGITS * 32;
+      pl.p += run;
+      left -= run;
+    }
+  }
+  // ---- logits once more
+  if (over == 0) return;
+  if (pl.p == pl.s.pe) next_item(a, a.Hkv, pl);
+  left = over;
   Feed feed;
-  feed.pl = pl;
-  feed.left = mine.count;
-  feed.ids_at = -1;
-  feed.ids = -1;
-  feed.stage = 0;
-  feed.bad = 0;
+  feed.start(a, pl, 1, left, lane);
 #pragma unroll 1
   for (int i = 0; i < Feed::STAGES; ++i) feed.step(a, a.Hkv, 1, ring, lane, false);
-  int stage = 0, left = mine.count;
-  constexpr int LH = DT == PE_KV_F32 ? SH::ROWS / 4 : GT;  // heads a lane
+  int stage = 0;
   int have = -1;  // head tile whose query and lse are loaded
-  typename TileOf<DT, DH, GT>::type tile;
-  float lse[LH];
+  Tile tile;
   auto take = [&](auto count) {
     constexpr int NP = decltype(count)::value;
     cp_async_wait<Feed::STAGES - NP>();
     __syncwarp();
-    uint32_t at[NP], none = 0;
+    uint32_t at[NP];
     int blk[NP];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       at[n] = ring + stage * Feed::STRIDE;
-      const bool bad = (feed.bad >> stage) & 1;
-      none |= (bad ? 1u : 0u) << n;
-      blk[n] = bad ? 0 : a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + n];
+      blk[n] = a.block_table[static_cast<size_t>(pl.b) * a.bt_stride + pl.p + n];
       if (++stage == Feed::STAGES) stage = 0;
     }
-    float sum[NP][2][2] = {};
+    float sum[NP] = {};
     for (int ht = 0; ht < a.tiles; ++ht) {
-      const int r0 = ht * SH::ROWS, rows = min(SH::ROWS, a.G - r0), h0 = pl.hh * a.G + r0;
       if (have != ht) {
-        tile.start(a, pl.b, h0, rows, scratch, lane);
-#pragma unroll
-        for (int x = 0; x < LH; ++x) {
-          const int r = DT == PE_KV_F32 ? t * LH + x : g + 8 * x;
-          // a row without weight, or no row
-          lse[x] = -INFINITY;
-          if (r < rows) lse[x] = __ldcg(a.lse_w + static_cast<size_t>(pl.b) * a.Hq + h0 + r);
-        }
+        const int r0 = ht * SH::ROWS;
+        tile.start(a, pl.b, pl.hh * a.G + r0, min(SH::ROWS, a.G - r0), scratch, lane);
+        load_lse(r0);
         have = ht;
       }
-      if constexpr (DT == PE_KV_F32) {
-        float z[LH][2];
+      if constexpr (F32) {
+        float z[LH][2], v[2] = {0.f, 0.f};
         F32Tile<DH>::logits(at[0], scratch, lane, z);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float s = 0.f;
 #pragma unroll
-          for (int x = 0; x < LH; ++x)
-            s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j] - lse[x]);
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          sum[0][j][0] += s;
+          for (int x = 0; x < LH; ++x) v[j] += weight(z[x][j], x);
+          v[j] += __shfl_xor_sync(0xffffffffu, v[j], 1);
+          v[j] += __shfl_xor_sync(0xffffffffu, v[j], 2);
         }
+        sum[0] += t & 1 ? v[1] : v[0];
       } else {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-          float z[GT][2][2];
-          tile.q.template logits<SH>(at[n], lane, z);
+          float z[GT][2][2], v[4] = {0.f, 0.f, 0.f, 0.f};
+          tile.q.template sums<SH>(at[n], lane, z);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int x = 0; x < GT; ++x)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float s = 0.f;
-#pragma unroll
-              for (int x = 0; x < GT; ++x)
-                s += lse[x] == -INFINITY ? 0.f : fast_exp2(z[x][j][e] - lse[x]);
-#pragma unroll
-              for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-              sum[n][j][e] += s;
-            }
+            for (int k = 0; k < 4; ++k)
+              v[k] += weight(z[x][k >> 1][k & 1] * tile.q.factor[x], x);
+          sum[n] += join_heads(v, g);
         }
       }
     }
@@ -1341,18 +1484,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32, 2)
 #pragma unroll
     for (int n = 0; n < NP; ++n) feed.step(a, a.Hkv, 1, ring, lane, false);
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int first = (pl.p + n) * kPage;
-      float* sc = a.pool.scores + (static_cast<size_t>(blk[n]) * a.Hkv + pl.hh) * kPage;
-      // four lanes hold a position's sum; one of them adds it
-      const int r = DT == PE_KV_F32 ? key_of(t & 1, g) : key_of((g >> 1) & 1, 2 * t + (g & 1));
-      const float v = DT == PE_KV_F32 ? (t & 1 ? sum[n][1][0] : sum[n][0][0])
-                      : g & 2         ? (g & 1 ? sum[n][1][1] : sum[n][1][0])
-                                      : (g & 1 ? sum[n][0][1] : sum[n][0][0]);
-      const bool mine_to_add = DT == PE_KV_F32 ? t < 2 : g < 4;
-      if (mine_to_add && !((none >> n) & 1) && first + r >= pl.s.lo && first + r < pl.s.n)
-        atomicAdd(sc + r, v);
-    }
+    for (int n = 0; n < NP; ++n) add_scores(a, pl.s, pl.hh, blk[n], pl.p + n, r, adds, sum[n]);
     pl.p += NP;
     left -= NP;
   };
@@ -1394,8 +1526,8 @@ static cudaError_t allow_smem(int dev) {
 }
 
 template <int DT, int DH, int GT>
-static pe_status launch_decode(DecodeArgs& a, char* ws, int dev, int sms, bool accumulate,
-                               cudaStream_t s) {
+static pe_status launch_decode(DecodeArgs& a, char* ws, char* ws_end, int dev, int sms,
+                               bool accumulate, cudaStream_t s) {
   using SH = DecodeShape<DT, DH, GT>;
   const int grid = std::min(sms * SH::CTAS, kMostCtas);
   a.tiles = (a.G + SH::ROWS - 1) / SH::ROWS;
@@ -1406,6 +1538,13 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int dev, int sms, bool a
   a.part = reinterpret_cast<float*>(ws);
   ws += static_cast<size_t>(grid) * 2 * SH::REC * 4;
   a.head = reinterpret_cast<float*>(ws);
+  ws += static_cast<size_t>(grid) * SH::WARPS * SH::REC * 4;
+  // the rest of the workspace holds logits, where one tile has all heads
+  a.stash = reinterpret_cast<float*>(ws);
+  constexpr int page = TileOf<DT, DH, GT>::type::LOGITS * 32 * 4;
+  a.stash_pages = accumulate && a.tiles == 1 && ws_end > ws
+                      ? static_cast<int>(std::min<int64_t>((ws_end - ws) / page, 1 << 30))
+                      : 0;
   cudaError_t e = allow_smem<DT, DH, GT>(dev);
   if (e == cudaSuccess)
     e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
@@ -1418,12 +1557,15 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, int dev, int sms, bool a
 }
 
 template <int DT, int DH>
-static pe_status launch_decode_heads(DecodeArgs& a, char* ws, int dev, int sms, bool accumulate,
-                                     cudaStream_t s) {
+static pe_status launch_decode_heads(DecodeArgs& a, char* ws, char* ws_end, int dev, int sms,
+                                     bool accumulate, cudaStream_t s) {
   if constexpr (DT != PE_KV_F32)
-    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, dev, sms, accumulate, s);
-  return launch_decode<DT, DH, 1>(a, ws, dev, sms, accumulate, s);
+    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, ws_end, dev, sms, accumulate, s);
+  return launch_decode<DT, DH, 1>(a, ws, ws_end, dev, sms, accumulate, s);
 }
+
+// Logits that a call with accumulate may keep: more are worked out again.
+constexpr int64_t kMostLogits = int64_t{1} << 30;  // bytes
 
 // The largest of the pool types: two CTAs an SM, 8 or 16 rows a tile.
 static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int head_dim, int sms) {
@@ -1437,13 +1579,17 @@ static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int h
 extern "C" {
 
 int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
-                                 int32_t head_dim) {
-  if (B < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads ||
+                                 int32_t head_dim, int32_t bt_stride) {
+  if (B < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || bt_stride < 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
   int dev;
   const int sms = pe::sm_count(dev);
-  return sms < 1 ? 0 : pe::workspace_bytes_for(B, n_heads, n_kv_heads, head_dim, sms);
+  if (sms < 1) return 0;
+  const int64_t rows = n_heads / n_kv_heads > 8 ? 16 : 8;
+  const double logits = 1.0 * B * bt_stride * n_kv_heads * pe::kPage * rows * 4;
+  return pe::workspace_bytes_for(B, n_heads, n_kv_heads, head_dim, sms) +
+         (logits < pe::kMostLogits ? static_cast<int64_t>(logits) : pe::kMostLogits);
 }
 
 pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, float scale,
@@ -1490,13 +1636,13 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool acc = accumulate != 0;
   if (pool->dtype == PE_KV_F32)
-    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, dev, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
   if (pool->dtype == PE_KV_BF16)
-    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, dev, sms, acc, s);
-  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, dev, sms, acc, s)
-                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, dev, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
+  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
+                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
 }
 
 }  // extern "C"

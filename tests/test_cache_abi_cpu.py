@@ -113,8 +113,8 @@ def test_decode_accumulate_needs_scores(B):
 
 def test_workspace_sizes(B):
     f = B.lib().pe_attn_decode_workspace
-    assert f(0, 4, 2, 64) == 0 and f(1, 3, 2, 64) == 0 and f(1, 4, 2, 80) == 0
-    assert f(1, 4, 0, 64) == 0
+    assert f(0, 4, 2, 64, 0) == 0 and f(1, 3, 2, 64, 0) == 0 and f(1, 4, 2, 80, 0) == 0
+    assert f(1, 4, 0, 64, 0) == 0 and f(1, 4, 2, 64, -1) == 0
 
 
 def _evict(B, pools=None, change=()):

@@ -194,6 +194,29 @@ def test_decode_long_lengths(dt, D, H, G, lens):
     _check_decode(ref, lens, dt, D, out, lse, before, c.scores, c.table)
 
 
+@pytest.mark.parametrize("dt,D,G", [("bf16", 64, 8), ("e4m3", 64, 3), ("f32", 64, 8), ("f32", 128, 3),
+                                    ("bf16", 128, 12), ("e4m3", 128, 16)])
+def test_decode_scores_from_kept_and_repeated_logits(dt, D, G):
+    """A workspace with room for the logits of none, some (odd numbers of
+    pages, inside an item) or all pages gives the same scores."""
+    torch, B = _lib()
+    rng = np.random.default_rng(14)
+    lens, H = [333, 0, 16, 70], 2
+    c = Cache(rng, lens, H, D, dt)
+    q = _make(rng, (4, H * G, D), "f32" if dt == "f32" else "bf16", 2.0)
+    least = B.pe_attn_decode_workspace(4, H * G, H, D)
+    most = B.pe_attn_decode_workspace(4, H * G, H, D, c.t.shape[1])
+    assert most - least == 4 * c.t.shape[1] * H * 16 * (16 if G > 8 else 8) * 4
+    before = c.scores.clone()
+    kv = c.values()
+    ref = C.decode(np.nan_to_num(kv[0]), np.nan_to_num(kv[1]), _host(q), c.table, lens)
+    for size in (least, least + 512, least + 7 * 1024, least + 40 * 1024 + 16, most):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")   # NaN, if it were read
+        c.scores.copy_(before)
+        out, lse = B.pe_attn_decode(c.pool, q, c.t, _i32(lens), accumulate=True, workspace=ws)
+        _check_decode(ref, lens, dt, D, out, lse, before, c.scores, c.table)
+
+
 def test_decode_many_short_requests():
     torch, B = _lib()
     rng = np.random.default_rng(9)
@@ -208,7 +231,8 @@ def test_decode_many_short_requests():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "e4m3", "f32"])
-def test_decode_strided_rows_scale_and_sharp_logits(dt):
+@pytest.mark.parametrize("scale", [0.7, -0.7, 0.0])
+def test_decode_strided_rows_scale_and_sharp_logits(dt, scale):
     """q as a slice of a fused projection's output, out as a slice of a wider
     buffer (whose other elements stay), a scale of its own, logits in the
     hundreds."""
@@ -220,9 +244,10 @@ def test_decode_strided_rows_scale_and_sharp_logits(dt):
     qkv = _make(rng, (2, H * G + 2 * H, D), act, 3.0)
     q = qkv[:, :H * G]
     wide = torch.full((2, H * G + 4, D), 7.0, dtype=_act(dt), device="cuda")
-    out, lse = B.pe_attn_decode(c.pool, q, c.t, _i32(lens), scale=0.7, out=wide[:, 2:2 + H * G])
+    out, lse = B.pe_attn_decode(c.pool, q, c.t, _i32(lens), scale=scale, out=wide[:, 2:2 + H * G])
     kv = c.values()
-    ref = C.decode(np.nan_to_num(kv[0]), np.nan_to_num(kv[1]), _host(q), c.table, lens, scale=float(np.float32(0.7)))
+    ref = C.decode(np.nan_to_num(kv[0]), np.nan_to_num(kv[1]), _host(q), c.table, lens, 
+                   scale=float(np.float32(scale)))
     _check_decode(ref, lens, dt, D, out, lse)
     assert bool((wide[:, :2] == 7).all()) and bool((wide[:, -2:] == 7).all())
 
