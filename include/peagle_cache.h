@@ -172,6 +172,24 @@ pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
                       const int32_t* dst_table, int32_t dst_stride, int32_t* kept,
                       int32_t* new_lens, int32_t* err, void* stream);
 
+/* Collect scores in the drafting step.  After this call every layer l of
+ * pe_draft_forward adds, besides what it does anyway, the attention weights
+ * of each request's next-token row (the first of its K sampled rows; query
+ * heads of a kv head summed) over positions 0 .. the row's own to scores[l]
+ * [num_blocks, Hkv, 16] fp32, 16-byte aligned, of the pools that the step is
+ * given.  No other result changes.  The step's attention computes rows in
+ * tiles and keeps no weights, so they come from a pass of their own over each
+ * layer's K and V (three launches a layer): collect on the steps where they
+ * are worth it.
+ * scores: HOST array of n_layers device pointers, copied; NULL turns the
+ * collecting off.  The first call allocates the pass's workspace on the
+ * handle: make it outside a graph capture.  A step with a larger batch or
+ * table than before allocates room for its logits (at most 1 GiB), or works
+ * them out twice if it is being captured.  Calls on one handle must not
+ * overlap.  PE_ERR_INVALID_ARGUMENT: a null or misaligned entry;
+ * PE_ERR_OUT_OF_MEMORY. */
+pe_status pe_set_kv_scores(pe_handle* h, float* const* scores);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,7 +51,8 @@ EXPORTED = ("pe_create", "pe_destroy", "pe_expand_batch", "pe_draft_forward",
             "pe_train_mask_view", "pe_train_partition", "pe_status_string")
 
 # include/peagle_cache.h
-CACHE_EXPORTED = ("pe_kv_append", "pe_attn_decode_workspace", "pe_attn_decode", "pe_kv_evict")
+CACHE_EXPORTED = ("pe_kv_append", "pe_attn_decode_workspace", "pe_attn_decode", "pe_kv_evict",
+                  "pe_set_kv_scores")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -135,6 +136,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pe_attn_decode_workspace.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.pe_attn_decode.argtypes = [P(pe_kv_pool), _i32, _i32, ctypes.c_float, _vp, _i64, _vp,
                                    _i32, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp]
+    lib.pe_set_kv_scores.argtypes = [_vp, P(_vp)]
     lib.pe_kv_evict.argtypes = [_i32, P(pe_kv_pool), _i32, _vp, _i32, _vp, _i32, _i32, _i32,
                                 ctypes.c_float, _vp, _i32, _vp, _vp, _vp, _vp]
     for name in EXPORTED[:-1] + CACHE_EXPORTED:
@@ -292,6 +294,8 @@ def pe_expand_batch(dr: Drafter, K: int, target_ids, target_pos, cu_in, num_acce
 def pe_draft_forward(dr: Drafter, ex: Expanded, block_table, k_cache: Sequence,
                      v_cache: Sequence, num_blocks: int, out_hidden, stream=None):
     L = len(k_cache)
+    if any(t.shape[0] < num_blocks for t in getattr(dr, "_kv_scores", None) or ()):
+        raise ValueError("the scores of pe_set_kv_scores hold fewer blocks than the pools")
     kc = (_vp * L)(*[ptr(t) for t in k_cache])
     vc = (_vp * L)(*[ptr(t) for t in v_cache])
     _check("pe_draft_forward", lib().pe_draft_forward(
@@ -701,3 +705,24 @@ def pe_kv_evict(pools: Sequence[KvPool], block_table, seq_lens, budget: int, sin
                 ptr(block_table), pages, ptr(seq_lens), budget, sinks, recent, rope_theta,
                 ptr(dst_table), dst_pages, ptr(kept), ptr(new_lens), ptr(err))
     return kept, new_lens
+
+
+def pe_set_kv_scores(dr: Drafter, scores: Optional[Sequence] = None) -> None:
+    """Let pe_draft_forward add the attention weights of every request's
+    next-token row to scores, one float32 tensor [num_blocks, n_kv_heads, 16]
+    a layer (None: collect no more)."""
+    if scores is None:
+        _check("pe_set_kv_scores", lib().pe_set_kv_scores(dr.handle, None))
+        dr._kv_scores = None
+        return
+    scores = list(scores)
+    sh, torch = dr.shape, _torch()
+    if len(scores) != sh.n_layers:
+        raise ValueError(f"one tensor for each of {sh.n_layers} layers")
+    for t in scores:
+        if (t.dtype != torch.float32 or t.dim() != 3 or not t.is_contiguous() or not t.is_cuda
+                or tuple(t.shape[1:]) != (sh.n_kv_heads, 16)):
+            raise ValueError(f"scores must be contiguous float32 [num_blocks, {sh.n_kv_heads}, 16]")
+    arr = (_vp * len(scores))(*[ptr(t) for t in scores])
+    _check("pe_set_kv_scores", lib().pe_set_kv_scores(dr.handle, arr))
+    dr._kv_scores = scores         # the library keeps the pointers

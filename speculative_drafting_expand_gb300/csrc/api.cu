@@ -7,6 +7,7 @@
 #include <tuple>
 #include <vector>
 
+#include "../../include/peagle_cache.h"
 #include "pe_common.cuh"
 #include "pe_kernels.h"
 
@@ -119,6 +120,11 @@ struct pe_handle {
   // fp8 (e4m3) KV pools: one K and one V scale per layer
   bool kv_fp8 = false;
   std::vector<float> k_scales, v_scales;
+  // scores of the cached positions, one array a layer (pe_set_kv_scores)
+  std::vector<float*> kv_scores;
+  void* score_out = nullptr;  // [max_reqs, Hq dh]
+  char* score_ws = nullptr;
+  int64_t score_ws_bytes = 0;
   float* trace = nullptr;
   void* attn_trace = nullptr;
   std::vector<cudaEvent_t> phase_events;  // 2 + 2 L events, or none
@@ -435,6 +441,34 @@ pe_status pe_set_kv_cache_fp8(pe_handle* h, const float* k_scales, const float* 
   return PE_OK;
 }
 
+pe_status pe_set_kv_scores(pe_handle* h, float* const* scores) {
+  if (!h) return PE_ERR_INVALID_ARGUMENT;
+  if (!scores) {
+    h->kv_scores.clear();
+    return PE_OK;
+  }
+  const pe_model_desc& d = h->desc;
+  for (int l = 0; l < d.n_layers; ++l)
+    if (!scores[l] || !aligned16(scores[l])) return PE_ERR_INVALID_ARGUMENT;
+  if (!h->score_ws) {
+    const int64_t bytes =
+        draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim);
+    if (bytes <= 0) return PE_ERR_CUDA;
+    const size_t out = static_cast<size_t>(h->max_reqs) * d.n_heads * d.head_dim * h->esize;
+    char* o = nullptr;
+    if (dev_alloc(h, &o, out)) return PE_ERR_OUT_OF_MEMORY;
+    h->score_out = o;
+    if (dev_alloc(h, &h->score_ws, static_cast<size_t>(bytes))) return PE_ERR_OUT_OF_MEMORY;
+    h->score_ws_bytes = bytes;
+  }
+  try {
+    h->kv_scores.assign(scores, scores + d.n_layers);
+  } catch (const std::bad_alloc&) {
+    return PE_ERR_OUT_OF_MEMORY;
+  }
+  return PE_OK;
+}
+
 pe_status pe_set_tuning(pe_handle* h, int32_t key, int32_t value) {
   if (!h) return PE_ERR_INVALID_ARGUMENT;
   switch (key) {
@@ -615,7 +649,24 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
   for (int l = 0; l < d.n_layers; ++l)
     if (!k_cache[l] || !v_cache[l]) return PE_ERR_INVALID_ARGUMENT;
   if (static_cast<long long>(B) * K > h->max_tokens) return PE_ERR_INVALID_ARGUMENT;
+  // the scores' pass counts pages in 32 bits
+  if (!h->kv_scores.empty() &&
+      static_cast<long long>(B) * bt_stride > 2147483647LL / d.n_heads)
+    return PE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!h->kv_scores.empty()) {
+    // room for the pass's logits grows with the batch and the block table;
+    // a captured step makes do with what there is
+    const int64_t want = pe_attn_decode_workspace(B, d.n_heads, d.n_kv_heads, d.head_dim, bt_stride);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (want > h->score_ws_bytes &&
+        cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone) {
+      char* ws = nullptr;
+      if (dev_alloc(h, &ws, static_cast<size_t>(want))) return PE_ERR_OUT_OF_MEMORY;
+      h->score_ws = ws;
+      h->score_ws_bytes = want;
+    }
+  }
   h->gemm_ordinal = 0;
   const int rows = ex->T_out;
   const int dt = d.dtype;
@@ -797,6 +848,36 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
       if ((e = trace_rows(static_cast<char*>(h->attn_trace) + l * h->max_tokens * per, h->attn,
                           per)))
         return PE_ERR_CUDA;
+    }
+    if (!h->kv_scores.empty()) {
+      DraftScoresArgs ds = {};
+      ds.B = B;
+      ds.rows = rows;
+      ds.Hq = d.n_heads;
+      ds.Hkv = d.n_kv_heads;
+      ds.dh = d.head_dim;
+      ds.dtype = dt == PE_DTYPE_F32 ? PE_KV_F32 : h->kv_fp8 ? PE_KV_E4M3 : PE_KV_BF16;
+      ds.num_blocks = num_blocks;
+      ds.bt_stride = bt_stride;
+      ds.k = k_cache[l];
+      ds.v = v_cache[l];
+      ds.scores = h->kv_scores[l];
+      if (h->kv_fp8) {
+        ds.k_scale = h->k_scales[l];
+        ds.v_scale = h->v_scales[l];
+      }
+      ds.q = h->q;
+      ds.q_rows = new_l;  // the first of a request's K sampled rows
+      ds.q_rows_stride = K;
+      ds.len_add = 1 - K;  // seq_lens counts the K - 1 MASK rows after it
+      ds.block_table = block_table;
+      ds.seq_lens = ex->seq_lens;
+      ds.out = h->score_out;
+      ds.workspace = h->score_ws;
+      ds.workspace_bytes = h->score_ws_bytes;
+      ds.err = h->err;
+      if (const pe_status st = launch_draft_scores(ds, s); st != PE_OK) return st;
+      h->launches += 3;
     }
     return PE_OK;
   };

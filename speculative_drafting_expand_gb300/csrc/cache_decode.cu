@@ -90,6 +90,10 @@ struct DecodeArgs {
   void* out;
   float* lse;      // caller's, or NULL
   int* err;
+  // drafting step: request b's query is row q_rows[b * q_rows_stride] of
+  // q_limit, and it attends seq_lens[b] + len_add positions; else NULL and 0
+  const int32_t* q_rows;
+  int q_rows_stride, q_limit, len_add;
   // workspace
   float* stash;    // logits of the line's first stash_pages pages, as the
                    // lanes hold them
@@ -107,7 +111,11 @@ struct Span {
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, bool record) {
   const long long cap = static_cast<long long>(a.bt_stride) * kPage;
   Span s;
-  s.n = a.seq_lens[b];
+  s.n = a.seq_lens[b] + a.len_add;
+  if (a.q_rows &&
+      static_cast<uint32_t>(a.q_rows[static_cast<size_t>(b) * a.q_rows_stride]) >=
+          static_cast<uint32_t>(a.q_limit))
+    s.n = 0;  // a bad row, recorded where it was made
   if (s.n < 0 || s.n > cap) {
     if (record) record_error(a.err, PE_DEV_BAD_POSITION);
     s.n = s.n < 0 ? 0 : static_cast<int>(cap);
@@ -116,6 +124,13 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, bool record)
   s.pf = s.lo / kPage;
   s.pe = s.n > s.lo ? (s.n - 1) / kPage + 1 : s.pf;
   return s;
+}
+
+// Element 0 of request b's query.
+template <typename A>
+__device__ __forceinline__ const A* query_of(const DecodeArgs& a, int b) {
+  const int row = a.q_rows ? a.q_rows[static_cast<size_t>(b) * a.q_rows_stride] : b;
+  return static_cast<const A*>(a.q) + static_cast<size_t>(row) * a.q_stride;
 }
 
 // The line of pages: where unit u lies.  Every thread sums the pages of an
@@ -415,8 +430,7 @@ struct QueryTile {
     for (int x = 0; x < GT; ++x) {
       const int r = g + 8 * x;
       const bool on = r < rows && A.scale != 0.f;
-      const bf16* q = static_cast<const bf16*>(A.q) + static_cast<size_t>(b) * A.q_stride +
-                      static_cast<size_t>(h0 + (on ? r : 0)) * DH;
+      const bf16* q = query_of<bf16>(A, b) + static_cast<size_t>(h0 + (on ? r : 0)) * DH;
       factor[x] = scale;
       if constexpr (DT == PE_KV_BF16) {
 #pragma unroll
@@ -741,8 +755,7 @@ struct F32Tile {
   __device__ __forceinline__ void start(const DecodeArgs& A, int b, int h0, int rows, char* scratch,
                                         int lane) {
     float* q = reinterpret_cast<float*>(scratch);
-    const float* src = static_cast<const float*>(A.q) + static_cast<size_t>(b) * A.q_stride +
-                       static_cast<size_t>(h0) * DH;
+    const float* src = query_of<float>(A, b) + static_cast<size_t>(h0) * DH;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < R * DH / 128; ++i) {
@@ -1574,6 +1587,51 @@ static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int h
          grid * (2 + kMaxWarps) * rows * (head_dim + 2) * 4;
 }
 
+static pe_status launch_decode_pool(DecodeArgs& a, int dtype, int dh, void* workspace,
+                                    int64_t workspace_bytes, int dev, int sms, bool acc,
+                                    cudaStream_t s) {
+  char* ws = static_cast<char*>(workspace);
+  char* end = ws + workspace_bytes;
+  if (dtype == PE_KV_F32)
+    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, end, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, end, dev, sms, acc, s);
+  if (dtype == PE_KV_BF16)
+    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, end, dev, sms, acc, s)
+                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, end, dev, sms, acc, s);
+  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, end, dev, sms, acc, s)
+                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, end, dev, sms, acc, s);
+}
+
+pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
+  int dev;
+  const int sms = sm_count(dev);
+  if (sms < 1) return PE_ERR_CUDA;
+  DecodeArgs a = {};
+  a.pool = CachePool{d.k, d.v, d.scores, d.num_blocks};
+  a.B = d.B;
+  a.Hq = d.Hq;
+  a.Hkv = d.Hkv;
+  a.G = d.Hq / d.Hkv;
+  a.bt_stride = d.bt_stride;
+  const bool codes = d.dtype == PE_KV_E4M3;
+  a.scale = kLog2e / std::sqrt(static_cast<float>(d.dh)) * (codes ? d.k_scale : 1.f);
+  a.v_scale = codes ? d.v_scale : 1.f;
+  a.q = d.q;
+  a.q_stride = a.out_stride = static_cast<long long>(d.Hq) * d.dh;
+  a.q_rows = d.q_rows;
+  a.q_rows_stride = d.q_rows_stride;
+  a.q_limit = d.rows;
+  a.len_add = d.len_add;
+  a.block_table = d.block_table;
+  a.seq_lens = d.seq_lens;
+  a.out = d.out;
+  a.err = d.err;
+  return launch_decode_pool(a, d.dtype, d.dh, d.workspace, d.workspace_bytes, dev, sms, true, s);
+}
+int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh) {
+  return pe_attn_decode_workspace(B, Hq, Hkv, dh, 0);
+}
+
 }  // namespace pe
 
 extern "C" {
@@ -1632,17 +1690,8 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   a.out = out;
   a.lse = lse;
   a.err = err;
-  char* ws = static_cast<char*>(workspace);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool acc = accumulate != 0;
-  if (pool->dtype == PE_KV_F32)
-    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
-  if (pool->dtype == PE_KV_BF16)
-    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
-  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, ws + workspace_bytes, dev, sms, acc, s)
-                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, ws + workspace_bytes, dev, sms, acc, s);
+  return launch_decode_pool(a, pool->dtype, dh, workspace, workspace_bytes, dev, sms,
+                            accumulate != 0, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/peagle.h"
+
 namespace pe {
 
 // Launch with programmatic stream serialization so a kernel's prologue
@@ -374,5 +376,29 @@ bool tensor_map_2d_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t
 // 128 / dh heads x both halves x dh/2 rows x 64 k lands in shared memory as
 // 128 rows with the halves interleaved (row 2i + b = feature i + b dh/2).
 bool tensor_map_qkv_interleaved(CUtensorMap* m, const void* ptr, int heads, int dh, uint64_t K);
+
+// ------------------------------------------------------- drafting scores
+// Adds the attention weights of every request's next-token row (row
+// q_rows[b * q_rows_stride] of q, positions 0 .. seq_lens[b] + len_add - 1)
+// to scores [num_blocks, Hkv, 16]; the attention output itself goes to `out`
+// [B, Hq, dh] and is of no further use.  dtype: pe_kv_dtype of the pools.
+struct DraftScoresArgs {
+  int B, rows, Hq, Hkv, dh, dtype, num_blocks, bt_stride;
+  void* k;
+  void* v;
+  float* scores;
+  float k_scale, v_scale;
+  const void* q;
+  const int32_t* q_rows;
+  int q_rows_stride, len_add;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* out;
+  void* workspace;
+  int64_t workspace_bytes;
+  int* err;
+};
+pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s);
+int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh);
 
 }  // namespace pe

@@ -152,6 +152,7 @@ def test_bad_pools_are_refused_by_every_operator(B, change, status):
 
 
 def test_null_pool(B):
+    assert B.lib().pe_set_kv_scores(None, None) == 1
     assert B.lib().pe_kv_append(None, *([1] * 3), 0.0, *([None, 0] * 3), None, None, None, 1,
                                 None, 0, None, None) == 1
     assert B.lib().pe_kv_evict(1, None, 1, None, 1, None, 1, 0, 0, 0.0, None, 0, None, None,

@@ -781,3 +781,115 @@ def test_drafting_step_on_a_trimmed_cache():
     got = G.f64(B.to_host(res["out_hidden"]), shape.dtype)
     assert np.abs(got - ref.out_hidden).max() <= 2e-2 * np.abs(ref.out_hidden).max()
     dr.close()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "bf16-128", "e4m3"])
+@pytest.mark.parametrize("K", [1, 4])
+def test_drafting_step_collects_scores(kind, K, monkeypatch):
+    """With pe_set_kv_scores the step's results are the same bit for bit, and
+    each layer's scores grow by the next-token rows' weights.  The pipeline
+    before a layer's logits is right to TOL of their size (the drafting
+    suite's rule), so a weight is right to a factor exp(4 TOL max|z|)."""
+    import oracle as O
+    from oracle import fp8_kv as F
+    from oracle import peagle_oracle as PO
+    from synthetic import workloads as W
+    from tests import gpu_helpers as G
+    torch, B = _lib()
+    dt = "f32" if kind == "f32" else "bf16"
+    tol = 1e-4 if kind == "f32" else 2e-2
+    dh = 128 if kind == "bf16-128" else 64
+    shape = W.small_shape("scored-" + kind, d=512, n_layers=2, n_heads=8, n_kv_heads=2,
+                          head_dim=dh, ffn=1024, vocab=4096)
+    if dt == "f32":
+        import dataclasses
+        shape = dataclasses.replace(shape, dtype="f32")
+    wl = W.custom("scored", 92, shape, K, [300, 40, 1, 129], [K + 1, K + 1, K + 1, 1],
+                  [K, 0, min(1, K), 0])
+    inp = W.make_step_inputs(wl)
+    w = W.make_weights(shape, wl.config_id, gains=wl.gains)
+    kc, vc = W.make_kv_cache(wl, inp)
+    scales = None
+    if kind == "e4m3":
+        scales = [(0.05, 0.05)] * 2
+        kc = [F.quantize(O.to_f64(k, dt), 0.05) for k in kc]
+        vc = [F.quantize(O.to_f64(v, dt), 0.05) for v in vc]
+    dr = G.make_drafter(shape, w, max(wl.T_out, wl.B * K), wl.B)
+    if scales:
+        B.pe_set_kv_cache_fp8(dr, [0.05] * 2, [0.05] * 2)
+    rng = np.random.default_rng(50)
+    start = [torch.from_numpy(rng.random(tuple(kc[0].shape[:3])).astype(np.float32)).cuda()
+             for _ in range(2)]
+    scores = [x.clone() for x in start]
+    results = []
+    for collect in (False, True, False):
+        B.pe_set_kv_scores(dr, scores if collect else None)
+        st = G.DeviceStep(wl, inp, kc, vc)
+        res = G.run_step(dr, st)
+        assert res["err"] == 0
+        results.append((res["tokens"], res["out_hidden"], res["logits"], *st.kc, *st.vc))
+    for other in results[1:]:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+                   for a, b in zip(results[0], other))
+
+    calls = []
+    plain = PO.attention_one_row
+
+    def recording(q, k_seq, v_seq, P):
+        z = np.stack([k_seq[:P + 1, h // (q.shape[0] // k_seq.shape[1])] @ q[h]
+                      for h in range(q.shape[0])]) / np.sqrt(q.shape[1])
+        calls.append((P, z))
+        return plain(q, k_seq, v_seq, P)
+
+    monkeypatch.setattr(PO, "attention_one_row", recording)
+    O.draft_step(shape, w, K, inp, kc, vc, kv_scales=scales)
+    a = np.asarray(inp.num_accepted)
+    per_layer = int((a + K).sum())            # rows 0..a and the K - 1 MASK rows
+    assert len(calls) == 2 * per_layer
+    for l in range(2):
+        want, tols = _host(start[l]), np.zeros(start[l].shape)
+        at = l * per_layer
+        for r in range(wl.B):
+            P, z = calls[at + int(a[r])]      # the row that follows the accepted ones
+            at += int(a[r]) + K
+            p = np.exp(z - z.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            e = np.expm1(4 * tol * np.abs(z).max())
+            for i in range(P + 1):
+                blk, off = C.slot(inp.block_table, r, i)
+                wt = p[:, i].reshape(2, -1).sum(1)
+                want[blk, :, off] += wt
+                tols[blk, :, off] += e * wt + 2.0 ** -20 * (1 + np.abs(want[blk, :, off]))
+        got = _host(scores[l])
+        assert np.all(np.abs(got - want) <= tols)
+        grew = got - _host(start[l])
+        for r in range(wl.B):                 # all of a row's weight is there
+            P = int(inp.target_pos[inp.cu_in[r]]) + int(a[r]) + 1
+            g = sum(grew[blk, :, off] for blk, off in
+                    (C.slot(inp.block_table, r, i) for i in range(P + 1)))
+            assert np.all(np.abs(g - 4) <= 4 * 2.0 ** -18 + (P + 1) * 2.0 ** -23)
+    dr.close()
+
+
+def test_score_collecting_refusals():
+    from synthetic import workloads as W
+    from tests import gpu_helpers as G
+    torch, B = _lib()
+    shape = W.small_shape("small-bf16", d=512, n_layers=2, n_heads=8, n_kv_heads=2, head_dim=64,
+                          ffn=1024, vocab=4096)
+    wl = W.custom("refused", 93, shape, 4, [30], [5], [4])
+    inp = W.make_step_inputs(wl)
+    w = W.make_weights(shape, wl.config_id, gains=wl.gains)
+    dr = G.make_drafter(shape, w, wl.T_out, 1)
+    ok = torch.zeros(inp.num_blocks, 2, 16, device="cuda")
+    for bad in ([ok], [ok, ok.double()], [ok, ok[:, :1]], [ok, ok.cpu()], [ok, ok.transpose(1, 2)]):
+        with pytest.raises(ValueError):
+            B.pe_set_kv_scores(dr, bad)
+    with pytest.raises(B.PeError):
+        B.pe_set_kv_scores(dr, [ok, torch.zeros(2 * 16 * 4 + 1, device="cuda")[1:].view(4, 2, 16)])
+    small = torch.zeros(inp.num_blocks - 1, 2, 16, device="cuda")
+    B.pe_set_kv_scores(dr, [ok, small])
+    kc, vc = W.make_kv_cache(wl, inp)
+    with pytest.raises(ValueError):
+        G.run_step(dr, G.DeviceStep(wl, inp, kc, vc))
+    dr.close()
