@@ -566,6 +566,25 @@ def _cache_empty(pool: KvPool, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=pool.device)
 
 
+# Workspaces of eager calls, one a device and stream: calls on one stream run
+# one after another, so they can share it.  A captured call gets memory of its
+# graph's (a replay may run beside anything), and so do calls whose logits it
+# holds (large) and calls on a stream other than the current one.
+_CACHE_WORKSPACES: Dict = {}
+
+
+def _cache_workspace(pool: KvPool, nbytes: int, shared: bool, stream):
+    torch = pool.torch
+    C = torch._C
+    if not shared or stream is not None or pool.index < 0 or C._cuda_isCurrentStreamCapturing():
+        return _cache_empty(pool, nbytes, torch.uint8, stream)
+    key = pool.index, C._cuda_getCurrentRawStream(pool.index)
+    ws = _CACHE_WORKSPACES.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _CACHE_WORKSPACES[key] = _cache_empty(pool, nbytes, torch.uint8, None)
+    return ws
+
+
 def _cache_call(pool: KvPool, stream, name, fn, *args) -> None:
     """Call into the library with the pool's device current; `stream` None is
     that device's current stream."""
@@ -633,8 +652,9 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
     its seq_lens [B] cached positions (the last `window` of them unless 0).
     scale None: head_dim ** -0.5.  accumulate: each position's weight is added
     to pool.scores.  Returns out and lse [B, n_heads] float32 (made when
-    None).  The workspace (uint8, pe_attn_decode_workspace bytes) is allocated
-    for the call when None."""
+    None).  workspace: uint8, pe_attn_decode_workspace bytes; None: the
+    stream's own, or for a call that is captured or accumulates, memory
+    allocated for the call."""
     torch = pool.torch
     _cache_ints(window=window)
     B, n_heads = q.shape[0], q.shape[1]
@@ -657,7 +677,7 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
             with torch.cuda.device(pool.index):
                 n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh, room)
             pool._workspace[B, n_heads, room] = n
-        workspace = _cache_empty(pool, n, torch.uint8, stream)
+        workspace = _cache_workspace(pool, n, not accumulate, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != pool.index:
         raise ValueError("workspace must be contiguous on the pool's device")
     else:

@@ -420,6 +420,36 @@ def test_calls_on_another_stream():
     assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in outs)
 
 
+def test_streams_and_captures_have_workspaces_of_their_own():
+    """Eager calls on two streams at once, beside replays of a graph captured
+    on one of them, larger and smaller calls in turn."""
+    torch, B = _lib()
+    rng = np.random.default_rng(12)
+    jobs = []
+    for D, lens in ((64, [6000, 900]), (128, [20, 4001, 7, 0])):
+        c = Cache(rng, lens, 4, D, "bf16")
+        q, n = _make(rng, (len(lens), 32, D), "bf16", 2.0), _i32(lens)
+        jobs.append((c, q, n, B.pe_attn_decode(c.pool, q, c.t, n)))
+    c, q, n, want = jobs[0]
+    out, lse = torch.empty_like(q), torch.empty(2, 32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.pe_attn_decode(c.pool, q, c.t, n, out=out, lse=lse)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(12):
+        g.replay()
+        for side in sides:
+            with torch.cuda.stream(side):
+                for c, q, n, w in (jobs, jobs[::-1])[turn % 2]:
+                    got.append((B.pe_attn_decode(c.pool, q, c.t, n), w))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for (o, l), (wo, wl) in got:
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
 # ------------------------------------------------------------------ append
 
 def _rot_tol(x, dt):
