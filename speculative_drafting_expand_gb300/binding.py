@@ -567,16 +567,18 @@ def _cache_empty(pool: KvPool, shape, dtype, stream):
 
 
 # Workspaces of eager calls, one a device and stream: calls on one stream run
-# one after another, so they can share it.  A captured call gets memory of its
-# graph's (a replay may run beside anything), and so do calls whose logits it
-# holds (large) and calls on a stream other than the current one.
+# one after another, so they can share it.  Memory of its own goes to a
+# captured call (its graph's: a replay may run beside anything), to a call on
+# a stream other than the current one, and to one that wants a lot.
 _CACHE_WORKSPACES: Dict = {}
+_CACHE_SHARED_MOST = 64 << 20
 
 
-def _cache_workspace(pool: KvPool, nbytes: int, shared: bool, stream):
+def _cache_workspace(pool: KvPool, nbytes: int, stream):
     torch = pool.torch
     C = torch._C
-    if not shared or stream is not None or pool.index < 0 or C._cuda_isCurrentStreamCapturing():
+    if (nbytes > _CACHE_SHARED_MOST or stream is not None or pool.index < 0
+            or C._cuda_isCurrentStreamCapturing()):
         return _cache_empty(pool, nbytes, torch.uint8, stream)
     key = pool.index, C._cuda_getCurrentRawStream(pool.index)
     ws = _CACHE_WORKSPACES.get(key)
@@ -653,8 +655,8 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
     scale None: head_dim ** -0.5.  accumulate: each position's weight is added
     to pool.scores.  Returns out and lse [B, n_heads] float32 (made when
     None).  workspace: uint8, pe_attn_decode_workspace bytes; None: the
-    stream's own, or for a call that is captured or accumulates, memory
-    allocated for the call."""
+    stream's own, or memory allocated for the call where it is captured or
+    wants more than 64 MiB."""
     torch = pool.torch
     _cache_ints(window=window)
     B, n_heads = q.shape[0], q.shape[1]
@@ -677,7 +679,7 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
             with torch.cuda.device(pool.index):
                 n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh, room)
             pool._workspace[B, n_heads, room] = n
-        workspace = _cache_workspace(pool, n, not accumulate, stream)
+        workspace = _cache_workspace(pool, n, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != pool.index:
         raise ValueError("workspace must be contiguous on the pool's device")
     else:
