@@ -109,8 +109,9 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * has a fixed order; where several requests of the call share a page, the
  * order of the requests' additions is not fixed.
  *
- * q [B, n_heads, head_dim] and out like q, of the activation type: rows
- * `*_stride` elements apart, heads contiguous, rows 16-byte aligned.  lse:
+ * q [B, n_heads, head_dim] and out like q (not q itself, nor overlapping it),
+ * of the activation type: rows `*_stride` elements apart, heads contiguous,
+ * rows 16-byte aligned.  lse:
  * NULL, or fp32 [B, n_heads].  block_table [B, bt_stride], seq_lens [B].
  * Sums, maxima and weights are held in fp32.  workspace: 16-byte aligned,
  * workspace_bytes at least pe_attn_decode_workspace(.., 0); contents need not
@@ -118,7 +119,8 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * Device errors: PE_DEV_BAD_POSITION (seq_lens[b] < 0 or past the table:
  * read as 0 or the table's end), PE_DEV_BAD_BLOCK (the page's positions are
  * left out).
- * PE_ERR_INVALID_ARGUMENT: B < 1, window < 0, scale not finite, n_heads not
+ * PE_ERR_INVALID_ARGUMENT: B < 1, window < 0, scale (times the K scale) not
+ * finite or too large for its sums to be, out == q, n_heads not
  * a positive multiple of n_kv_heads, accumulate without pool->scores, a
  * stride shorter than a row, a null or misaligned pointer, a short
  * workspace.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128, or B *
@@ -147,8 +149,8 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  *
  * dst_table [B, dst_stride]: the pages that receive the result, none of
  * which may be a page of block_table that the call reads (pages shared with
- * other requests can be trimmed this way).  dst_table NULL: in place, in the
- * request's first pages; its pages may then not be shared, and scores up to
+ * other requests can be trimmed this way).  dst_table NULL or block_table: in
+ * place, in the request's first pages; its pages may then not be shared, and scores up to
  * L are set to 0.  In place needs whole requests to be trimmed by one call
  * for each layer; the layers of one call are independent.
  *
@@ -179,7 +181,7 @@ pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
  * [num_blocks, Hkv, 16] fp32, 16-byte aligned, of the pools that the step is
  * given.  No other result changes.  The step's attention computes rows in
  * tiles and keeps no weights, so they come from a pass of their own over each
- * layer's K and V (three launches a layer): collect on the steps where they
+ * layer's K (three launches a layer): collect on the steps where they
  * are worth it.
  * scores: HOST array of n_layers device pointers, copied; NULL turns the
  * collecting off.  The first call allocates the pass's workspace on the

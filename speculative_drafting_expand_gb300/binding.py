@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
@@ -572,18 +573,22 @@ def _cache_empty(pool: KvPool, shape, dtype, stream):
 # a stream other than the current one, and to one that wants a lot.
 _CACHE_WORKSPACES: Dict = {}
 _CACHE_SHARED_MOST = 64 << 20
+# held while the launches of a call with a shared workspace are queued: another
+# thread's must not come between them
+_CACHE_LOCK = threading.Lock()
 
 
-def _cache_workspace(pool: KvPool, nbytes: int, stream):
-    torch = pool.torch
-    C = torch._C
-    if (nbytes > _CACHE_SHARED_MOST or stream is not None or pool.index < 0
-            or C._cuda_isCurrentStreamCapturing()):
-        return _cache_empty(pool, nbytes, torch.uint8, stream)
+def _cache_shares(pool: KvPool, nbytes: int, stream) -> bool:
+    return (nbytes <= _CACHE_SHARED_MOST and stream is None and pool.index >= 0
+            and not pool.torch._C._cuda_isCurrentStreamCapturing())
+
+
+def _cache_shared_workspace(pool: KvPool, nbytes: int):
+    C = pool.torch._C
     key = pool.index, C._cuda_getCurrentRawStream(pool.index)
     ws = _CACHE_WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _CACHE_WORKSPACES[key] = _cache_empty(pool, nbytes, torch.uint8, None)
+        ws = _CACHE_WORKSPACES[key] = _cache_empty(pool, nbytes, pool.torch.uint8, None)
     return ws
 
 
@@ -679,16 +684,25 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
             with torch.cuda.device(pool.index):
                 n = pe_attn_decode_workspace(B, n_heads, pool.n_kv_heads, dh, room)
             pool._workspace[B, n_heads, room] = n
-        workspace = _cache_workspace(pool, n, stream)
+        if not _cache_shares(pool, n, stream):
+            workspace = _cache_empty(pool, n, torch.uint8, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != pool.index:
         raise ValueError("workspace must be contiguous on the pool's device")
     else:
         n = workspace.numel() * workspace.element_size()
     if err is not None:
         _cache_i32(pool, "err", err, (1,))
-    _cache_call(pool, stream, "pe_attn_decode", pool.lib.pe_attn_decode, pool._ref, B, n_heads,
-                dh ** -0.5 if scale is None else scale, ptr(q), qs, ptr(block_table), pages,
-                ptr(seq_lens), window, ptr(out), os_, ptr(lse), int(accumulate), ptr(workspace), n, ptr(err))
+    args = (pool._ref, B, n_heads, dh ** -0.5 if scale is None else scale, ptr(q), qs,
+            ptr(block_table), pages, ptr(seq_lens), window, ptr(out), os_, ptr(lse),
+            int(accumulate))
+    if workspace is not None:
+        _cache_call(pool, stream, "pe_attn_decode", pool.lib.pe_attn_decode, *args,
+                    ptr(workspace), n, ptr(err))
+    else:
+        with _CACHE_LOCK:
+            ws = _cache_shared_workspace(pool, n)
+            _cache_call(pool, stream, "pe_attn_decode", pool.lib.pe_attn_decode, *args, ptr(ws),
+                        n, ptr(err))
     return out, lse
 
 

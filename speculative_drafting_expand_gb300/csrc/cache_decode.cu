@@ -74,6 +74,7 @@ struct DecodeShape {
   static constexpr int S_STAGES = PAGEB == 1024 ? 8 : PAGEB == 2048 ? 6 : 3;
   static constexpr int S_RING = S_STAGES * PAGEB;
   static constexpr int S_SMEM = WARPS * (S_RING + SCRATCH);
+  static_assert(REC * 4 <= S_RING, "the same without values");
   static_assert(REC * 4 <= RING, "a warp leaves its last partial in its ring");
 };
 
@@ -534,7 +535,7 @@ struct MmaTile {
   // stash: where the logits of the first stash_n pages go, LOGITS floats a
   // lane and page.
   static constexpr int LOGITS = 4 * GT;
-  template <int NP>
+  template <int NP, bool VALUES>
   __device__ __forceinline__ void pages(const uint32_t (&stage)[NP], int v_lo, int v_hi,
                                         uint32_t none, char*, float* stash, int stash_n, int lane) {
     const int t = lane & 3;
@@ -584,6 +585,7 @@ struct MmaTile {
         m[x] = mn;
         l[x] *= c[x];
       }
+      if (VALUES)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         o[i][0] *= c[0];
@@ -607,7 +609,8 @@ struct MmaTile {
         }
     }
 #pragma unroll
-    for (int n = 0; n < NP; ++n) add_values(stage[n] + SH::PAGEB, hi[n], lo[n], lane);
+    for (int n = 0; VALUES && n < NP; ++n)
+      add_values(stage[n] + SH::PAGEB, hi[n], lo[n], lane);
   }
 
   // O += P V of a page
@@ -823,7 +826,7 @@ struct F32Tile {
   }
 
   static constexpr int LOGITS = R / 2;
-  template <int NP>
+  template <int NP, bool VALUES>
   __device__ __forceinline__ void pages(const uint32_t (&at)[NP], int v_lo, int v_hi,
                                         uint32_t none, char* scratch, float* stash, int stash_n,
                                         int lane) {
@@ -876,6 +879,7 @@ struct F32Tile {
       }
     }
     __syncwarp();
+    if (!VALUES) return;
     if (scale)
 #pragma unroll
       for (int h = 0; h < R; ++h) {
@@ -1034,12 +1038,15 @@ __device__ __forceinline__ void join_in_cta(const DecodeArgs& a, int b, int hh, 
 // after it, the request (.x, else -1), the head tile (.y) and the number of
 // CTAs that have parts of it (.z).
 
-template <int DT, int DH, int GT>
+// VALUES false: K alone, for the lse (and the logits); out gets zeros.
+template <int DT, int DH, int GT, bool VALUES>
 __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
                                   DecodeShape<DT, DH, GT>::CTAS)
     attn_decode_kernel(const __grid_constant__ DecodeArgs a) {
   using SH = DecodeShape<DT, DH, GT>;
   using Tile = typename TileOf<DT, DH, GT>::type;
+  using Feed = Feeder<SH, VALUES>;
+  constexpr int RING = VALUES ? SH::RING : SH::S_RING;
   constexpr int W = SH::WARPS, THREADS = W * 32;
   extern __shared__ __align__(128) char smem[];
   __shared__ int prefix[THREADS];
@@ -1064,8 +1071,8 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   }
   const Share mine = share_of(cta.count, W, w);
   const int working = min(cta.count, W);
-  char* ring_p = smem + w * SH::RING;
-  char* scratch = smem + W * SH::RING + w * SH::SCRATCH;
+  char* ring_p = smem + w * RING;
+  char* scratch = smem + W * RING + w * SH::SCRATCH;
   const uint32_t ring = smem_u32(ring_p);
   float* my_last = reinterpret_cast<float*>(ring_p);
   float* my_head = a.head + (static_cast<size_t>(blockIdx.x) * W + w) * SH::REC;
@@ -1074,11 +1081,11 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
   int state = 0;
   if (mine.count > 0) {
     Place pl = place_of<THREADS>(a, ln, heads, prefix, cta.first + mine.first);
-    Feeder<SH, true> feed;
+    Feed feed;
     feed.start(a, pl, a.tiles, mine.count, lane);
     int unit = cta.first + mine.first;  // of the page that is taken next
 #pragma unroll 1
-    for (int i = 0; i < SH::STAGES; ++i) feed.step(a, heads, a.tiles, ring, lane, true);
+    for (int i = 0; i < Feed::STAGES; ++i) feed.step(a, heads, a.tiles, ring, lane, true);
     int left = mine.count, stage = 0;
     Tile tile;
     while (true) {
@@ -1090,17 +1097,17 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
       left -= stop - pl.p;
       auto take = [&](auto count) {
         constexpr int NP = decltype(count)::value;
-        cp_async_wait<SH::STAGES - NP>();
+        cp_async_wait<Feed::STAGES - NP>();
         __syncwarp();  // other lanes' copies, and their reads of the pages before
         uint32_t at[NP], none = 0;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-          at[n] = ring + stage * 2 * SH::PAGEB;
+          at[n] = ring + stage * Feed::STRIDE;
           none |= ((feed.bad >> stage) & 1) << n;
-          if (++stage == SH::STAGES) stage = 0;
+          if (++stage == Feed::STAGES) stage = 0;
         }
         const int first = pl.p * kPage;
-        tile.template pages<NP>(at, pl.s.lo - first, pl.s.n - first, none, scratch,
+        tile.template pages<NP, VALUES>(at, pl.s.lo - first, pl.s.n - first, none, scratch,
                                 a.stash + static_cast<size_t>(unit) * Tile::LOGITS * 32,
                                 a.stash_pages - unit, lane);
         unit += NP;
@@ -1183,7 +1190,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
         }
         const int y = from + i;
         parts[i] = (i == 0 && !before) || ((in_ring >> y) & 1)
-                       ? reinterpret_cast<const float*>(smem + y * SH::RING)
+                       ? reinterpret_cast<const float*>(smem + y * RING)
                        : a.head + (static_cast<size_t>(blockIdx.x) * W + y) * SH::REC;
       }
       const int y = over ? from : x, k = over && !before ? 1 : 0;
@@ -1524,13 +1531,14 @@ static int sm_count(int& dev) {
 }
 
 // The kernels' shared memory, asked for once per device.
-template <int DT, int DH, int GT>
+template <int DT, int DH, int GT, bool VALUES>
 static cudaError_t allow_smem(int dev) {
   using SH = DecodeShape<DT, DH, GT>;
   static std::atomic<uint64_t> done{0};
   if (dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DT, DH, GT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DT, DH, GT, VALUES>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       VALUES ? SH::SMEM : SH::S_SMEM);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(attn_scores_kernel<DT, DH, GT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SH::S_SMEM);
@@ -1538,7 +1546,7 @@ static cudaError_t allow_smem(int dev) {
   return e;
 }
 
-template <int DT, int DH, int GT>
+template <int DT, int DH, int GT, bool VALUES>
 static pe_status launch_decode(DecodeArgs& a, char* ws, char* ws_end, int dev, int sms,
                                bool accumulate, cudaStream_t s) {
   using SH = DecodeShape<DT, DH, GT>;
@@ -1558,9 +1566,10 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, char* ws_end, int dev, i
   a.stash_pages = accumulate && a.tiles == 1 && ws_end > ws
                       ? static_cast<int>(std::min<int64_t>((ws_end - ws) / page, 1 << 30))
                       : 0;
-  cudaError_t e = allow_smem<DT, DH, GT>(dev);
+  cudaError_t e = allow_smem<DT, DH, GT, VALUES>(dev);
   if (e == cudaSuccess)
-    e = launch_pdl(attn_decode_kernel<DT, DH, GT>, dim3(grid), dim3(SH::WARPS * 32), SH::SMEM, s, a);
+    e = launch_pdl(attn_decode_kernel<DT, DH, GT, VALUES>, dim3(grid), dim3(SH::WARPS * 32),
+                   VALUES ? SH::SMEM : SH::S_SMEM, s, a);
   if (e == cudaSuccess)
     e = launch_pdl(attn_join_kernel<DT, DH, GT>, dim3(grid, kJoinRows), dim3(kJoinThreads), 0, s, a);
   if (e == cudaSuccess && accumulate)
@@ -1569,12 +1578,12 @@ static pe_status launch_decode(DecodeArgs& a, char* ws, char* ws_end, int dev, i
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
 
-template <int DT, int DH>
+template <bool VALUES, int DT, int DH>
 static pe_status launch_decode_heads(DecodeArgs& a, char* ws, char* ws_end, int dev, int sms,
                                      bool accumulate, cudaStream_t s) {
   if constexpr (DT != PE_KV_F32)
-    if (a.G > 8) return launch_decode<DT, DH, 2>(a, ws, ws_end, dev, sms, accumulate, s);
-  return launch_decode<DT, DH, 1>(a, ws, ws_end, dev, sms, accumulate, s);
+    if (a.G > 8) return launch_decode<DT, DH, 2, VALUES>(a, ws, ws_end, dev, sms, accumulate, s);
+  return launch_decode<DT, DH, 1, VALUES>(a, ws, ws_end, dev, sms, accumulate, s);
 }
 
 // Logits that a call with accumulate may keep: more are worked out again.
@@ -1587,19 +1596,20 @@ static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int h
          grid * (2 + kMaxWarps) * rows * (head_dim + 2) * 4;
 }
 
+template <bool VALUES>
 static pe_status launch_decode_pool(DecodeArgs& a, int dtype, int dh, void* workspace,
                                     int64_t workspace_bytes, int dev, int sms, bool acc,
                                     cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
   char* end = ws + workspace_bytes;
   if (dtype == PE_KV_F32)
-    return dh == 64 ? launch_decode_heads<PE_KV_F32, 64>(a, ws, end, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_F32, 128>(a, ws, end, dev, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<VALUES, PE_KV_F32, 64>(a, ws, end, dev, sms, acc, s)
+                    : launch_decode_heads<VALUES, PE_KV_F32, 128>(a, ws, end, dev, sms, acc, s);
   if (dtype == PE_KV_BF16)
-    return dh == 64 ? launch_decode_heads<PE_KV_BF16, 64>(a, ws, end, dev, sms, acc, s)
-                    : launch_decode_heads<PE_KV_BF16, 128>(a, ws, end, dev, sms, acc, s);
-  return dh == 64 ? launch_decode_heads<PE_KV_E4M3, 64>(a, ws, end, dev, sms, acc, s)
-                  : launch_decode_heads<PE_KV_E4M3, 128>(a, ws, end, dev, sms, acc, s);
+    return dh == 64 ? launch_decode_heads<VALUES, PE_KV_BF16, 64>(a, ws, end, dev, sms, acc, s)
+                    : launch_decode_heads<VALUES, PE_KV_BF16, 128>(a, ws, end, dev, sms, acc, s);
+  return dh == 64 ? launch_decode_heads<VALUES, PE_KV_E4M3, 64>(a, ws, end, dev, sms, acc, s)
+                  : launch_decode_heads<VALUES, PE_KV_E4M3, 128>(a, ws, end, dev, sms, acc, s);
 }
 
 pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
@@ -1626,7 +1636,7 @@ pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
   a.seq_lens = d.seq_lens;
   a.out = d.out;
   a.err = d.err;
-  return launch_decode_pool(a, d.dtype, d.dh, d.workspace, d.workspace_bytes, dev, sms, true, s);
+  return launch_decode_pool<false>(a, d.dtype, d.dh, d.workspace, d.workspace_bytes, dev, sms, true, s);
 }
 int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh) {
   return pe_attn_decode_workspace(B, Hq, Hkv, dh, 0);
@@ -1661,7 +1671,7 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   const int64_t qw = static_cast<int64_t>(n_heads) * dh;
   if (B < 1 || n_heads < 1 || n_heads % pool->n_kv_heads || !std::isfinite(scale) ||
       !block_table || bt_stride < 1 || !seq_lens || window < 0 || !row_ok(q, q_stride, qw, eb) ||
-      !row_ok(out, out_stride, qw, eb) || (accumulate && !pool->scores) || !workspace ||
+      !row_ok(out, out_stride, qw, eb) || out == q || (accumulate && !pool->scores) || !workspace ||
       !is_aligned16(workspace) || workspace_bytes <= 0)
     return PE_ERR_INVALID_ARGUMENT;
   // the pages are counted in 32 bits (a table of that size is 8 GB)
@@ -1681,6 +1691,7 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   a.window = window;
   const bool codes = pool->dtype == PE_KV_E4M3;
   a.scale = scale * kLog2e * (codes ? pool->k_scale : 1.f);
+  if (!std::isfinite(a.scale)) return PE_ERR_INVALID_ARGUMENT;
   a.v_scale = codes ? pool->v_scale : 1.f;
   a.q = q;
   a.q_stride = q_stride;
@@ -1690,7 +1701,7 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   a.out = out;
   a.lse = lse;
   a.err = err;
-  return launch_decode_pool(a, pool->dtype, dh, workspace, workspace_bytes, dev, sms,
+  return launch_decode_pool<true>(a, pool->dtype, dh, workspace, workspace_bytes, dev, sms,
                             accumulate != 0, static_cast<cudaStream_t>(stream));
 }
 

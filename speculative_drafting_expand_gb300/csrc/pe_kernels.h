@@ -380,8 +380,8 @@ bool tensor_map_qkv_interleaved(CUtensorMap* m, const void* ptr, int heads, int 
 // ------------------------------------------------------- drafting scores
 // Adds the attention weights of every request's next-token row (row
 // q_rows[b * q_rows_stride] of q, positions 0 .. seq_lens[b] + len_add - 1)
-// to scores [num_blocks, Hkv, 16]; the attention output itself goes to `out`
-// [B, Hq, dh] and is of no further use.  dtype: pe_kv_dtype of the pools.
+// to scores [num_blocks, Hkv, 16]; `out` [B, Hq, dh] is scratch (zeros).
+// dtype: pe_kv_dtype of the pools.
 struct DraftScoresArgs {
   int B, rows, Hq, Hkv, dh, dtype, num_blocks, bt_stride;
   void* k;

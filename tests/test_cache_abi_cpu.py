@@ -91,7 +91,7 @@ def test_append_refusals(B, change, status):
 
 def _decode(B, pool=None, change=()):
     f = dict(B=3, n_heads=4, scale=0.1, q=BASE, qs=256, table=BASE, stride=2, lens=BASE,
-             window=0, out=BASE, os=256, lse=0, acc=0, ws=BASE, bytes=1 << 40, err=0, stream=0)
+             window=0, out=BASE + 4096, os=256, lse=0, acc=0, ws=BASE, bytes=1 << 40, err=0, stream=0)
     f.update(change)
     pool = pool or _pool(B)
     return B.lib().pe_attn_decode(ctypes.byref(pool), *f.values())
@@ -101,7 +101,7 @@ def _decode(B, pool=None, change=()):
     (dict(B=0), 1), (dict(n_heads=3), 1), (dict(n_heads=0), 1), (dict(scale=float("nan")), 1),
     (dict(q=0), 1), (dict(q=BASE + 8), 1), (dict(qs=128), 1), (dict(qs=257), 1),
     (dict(table=0), 1), (dict(stride=0), 1), (dict(lens=0), 1), (dict(window=-1), 1),
-    (dict(out=0), 1), (dict(os=128), 1), (dict(ws=0), 1), (dict(ws=BASE + 8), 1),
+    (dict(out=0), 1), (dict(out=BASE), 1), (dict(os=128), 1), (dict(ws=0), 1), (dict(ws=BASE + 8), 1),
     (dict(bytes=0), 1), (dict(stride=1 << 28), 2)])
 def test_decode_refusals(B, change, status):
     assert _decode(B, change=change) == status

@@ -450,6 +450,35 @@ def test_streams_and_captures_have_workspaces_of_their_own():
         assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
+def test_threads_on_one_stream():
+    """Two host threads that share a stream: neither call's launches fall
+    between the other's."""
+    import threading
+    torch, B = _lib()
+    rng = np.random.default_rng(13)
+    jobs = []
+    for lens in ([3000, 2999], [700, 5000]):
+        c = Cache(rng, lens, 4, 64, "bf16")
+        q, n = _make(rng, (2, 32, 64), "bf16", 2.0), _i32(lens)
+        jobs.append((c, q, n, B.pe_attn_decode(c.pool, q, c.t, n)))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        c, q, n, _ = jobs[i]
+        for _ in range(200):
+            got[i].append(B.pe_attn_decode(c.pool, q, c.t, n))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 200
+        assert all(torch.equal(o, jobs[i][3][0]) and torch.equal(l, jobs[i][3][1])
+                   for o, l in got[i])
+
+
 # ------------------------------------------------------------------ append
 
 def _rot_tol(x, dt):
@@ -653,6 +682,17 @@ def test_evict_long_rows(n, budget, fresh):
                               rope_theta=1e4, dst_table=None if dst is None else _i32(dst))
     ref = C.evict(*before, c.table, np.array([n]), budget, 5, 700, 1e4, dst)
     _check_evict(c, before, ref, "bf16", 1e4, kept, new)
+
+
+def test_evict_into_its_own_table_is_in_place():
+    torch, B = _lib()
+    lens, got = [900, 30], []
+    for own_table in (False, True):
+        c = Cache(np.random.default_rng(36), lens, 8, 64, "bf16")
+        r = B.pe_kv_evict([c.pool], c.t, _i32(lens), 500, 4, 100, 1e4,
+                          dst_table=c.t if own_table else None)
+        got.append((*r, c.k, c.v, c.scores))
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got))
 
 
 @pytest.mark.parametrize("fresh", [False, True])
