@@ -244,14 +244,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64
 // K and V pass through L2 once.  With logits to keep there (written by this
 // kernel, read by the last) they are the first to leave it: batch 64, e4m3,
 // with scores 91 -> 85 us, batch 16 66 -> 60; without, small caches that a
-// program reads again soon may stay.
+// program reads again soon may stay.  Made once, by whole warps (volatile: not
+// again at a copy that some lanes skip), and the same in every lane.
 __device__ __forceinline__ uint64_t kv_policy(bool first_to_leave) {
-  uint64_t p;
-  if (first_to_leave)
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  else
-    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-  return p;
+  uint64_t normal;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  const uint64_t first = l2_policy_evict_first();
+  return first_to_leave ? first : normal;
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
