@@ -78,7 +78,10 @@ __device__ __forceinline__ int page_of(const int32_t* table, int stride, int b, 
 
 
 constexpr int kEvictThreads = 512;
-constexpr int kMostKeys = 24576;  // scores that are held in shared memory
+// Scores that are held in shared memory, with two CTAs an SM and with one
+// (few rows); the rest of a longer row is read again from L2 at every step.
+constexpr int kMostKeys = 24576;
+constexpr int kMostKeysAlone = 49152;
 constexpr int kRanked = 128;      // keys that are ranked at once
 
 // A row on its way: its number in the pool where it goes (-1: nowhere) and by
@@ -111,7 +114,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 
 template <typename S, int DH, bool IN_PLACE>
 __global__ void __launch_bounds__(kEvictThreads, 2)
-    kv_evict_kernel(const __grid_constant__ EvictArgs a, int cluster) {
+    kv_evict_kernel(const __grid_constant__ EvictArgs a, int cluster, int key_room) {
   using SH = EvictShape<S, DH>;
   constexpr int T = SH::T, WARPS = T / 32, LANES = SH::LANES, ROUND = SH::ROUND;
   constexpr int HALF = LANES / 2, AHEAD = SH::AHEAD;
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   __shared__ int4 found[2][WARPS];  // counts of a bisection step, by warp
   __shared__ int scan[2][WARPS];
   __shared__ uint32_t ranked[kRanked], cut_key;
-  __shared__ int n_ranked;
+  __shared__ int n_ranked, cut_ties;
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,17 +151,19 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
     // four positions of a page
     auto load_keys = [&](int p) -> uint4 {
       const int blk = table[p / kPage];
-      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (blk < 0 || blk >= pool.num_blocks)
+      const bool ok = blk >= 0 && blk < pool.num_blocks;
+      // read in any case, so that several reads can be under way
+      float4 x = *reinterpret_cast<const float4*>(
+          pool.scores + (static_cast<size_t>(ok ? blk : 0) * a.Hkv + h) * kPage + p % kPage);
+      if (!ok) {
         record_error(a.err, PE_DEV_BAD_BLOCK);
-      else
-        x = *reinterpret_cast<const float4*>(
-            pool.scores + (static_cast<size_t>(blk) * a.Hkv + h) * kPage + p % kPage);
+        x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      }
       auto in = [&](int i) { return p + i >= lo && p + i < hi; };
       return make_uint4(in(0) ? score_key(x.x) : 0u, in(1) ? score_key(x.y) : 0u,
                         in(2) ? score_key(x.z) : 0u, in(3) ? score_key(x.w) : 0u);
     };
-    const int held = min((hi + 3) / 4 * 4, kMostKeys);  // positions whose keys are held
+    const int held = min((hi + 3) / 4 * 4, key_room);  // positions whose keys are held
     if (need > 0)
 #pragma unroll 2
       for (int p = tid * 4; p < held; p += T * 4)
@@ -181,6 +186,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
         };
 #pragma unroll 2
         for (int p = tid * 4; p < held; p += T * 4) add(*reinterpret_cast<const uint4*>(keys + p));
+#pragma unroll 4
         for (int p = held + tid * 4; p < hi; p += T * 4) add(load_keys(p));
         c1 = __reduce_add_sync(0xffffffffu, c1);
         c2 = __reduce_add_sync(0xffffffffu, c2);
@@ -209,6 +215,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
     }
     // stay: key > cut, and the first `ties` of key == cut
     uint32_t cut = at_floor == need ? floor - 1 : floor;
+    int ties = at_floor == need ? 0 : need - above;
     if (need > 0 && at_floor != need && shift > 0) {
       auto add = [&](uint32_t k) {
         if (k != 0 && (shift == 32 || k - floor < 1u << shift)) {
@@ -223,6 +230,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
         add(k.w);
       };
       for (int p = tid * 4; p < held; p += T * 4) add4(*reinterpret_cast<const uint4*>(keys + p));
+#pragma unroll 4
       for (int p = held + tid * 4; p < hi; p += T * 4) add4(load_keys(p));
       __syncthreads();
       const int count = at_floor - above;
@@ -234,64 +242,77 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
           more += ranked[i] > k;
           same_key += ranked[i] == k;
         }
-        if (above + more < need && need <= above + more + same_key) cut_key = k;
+        if (above + more < need && need <= above + more + same_key) {
+          cut_key = k;
+          cut_ties = need - above - more;
+        }
       }
       __syncthreads();
       cut = cut_key;
+      ties = cut_ties;
     }
-    // ---- the list, in order: each thread an odd number of positions in a row
-    auto key = [&](int p) -> uint32_t {
-      if (p < held) return keys[p];
-      const uint4 k = load_keys(p & ~3);
-      return (p & 3) == 0 ? k.x : (p & 3) == 1 ? k.y : (p & 3) == 2 ? k.z : k.w;
-    };
-    const int mid = hi - lo, seg = ((mid + T - 1) / T) | 1;
-    const int p0 = lo + min(tid * seg, mid), p1 = min(p0 + seg, hi);
-    int gt = 0, eq = 0;
-    if (need > 0)
+    // ---- the list, in order: each thread an odd number of positions in a row,
+    // of as many as the shared memory holds at a time
+    int kept_before = lo, eq_before = 0;
+    for (int w0 = 0; need > 0 && w0 < hi; w0 += key_room) {
+      const int w1 = min(w0 + key_room, hi);
+      if (w0 > 0) {
+        __syncthreads();
+#pragma unroll 4
+        for (int p = w0 + tid * 4; p < w1; p += T * 4)
+          *reinterpret_cast<uint4*>(keys + p - w0) = load_keys(p);
+        __syncthreads();
+      }
+      const int from = max(lo, w0), count = max(w1 - from, 0), seg = ((count + T - 1) / T) | 1;
+      const int p0 = from + min(tid * seg, count), p1 = min(p0 + seg, from + count);
+      int gt = 0, eq = 0;
 #pragma unroll 4
       for (int p = p0; p < p1; ++p) {
-        const uint32_t k = key(p);
+        const uint32_t k = keys[p - w0];
         gt += k > cut;
         eq += k == cut;
       }
-    int g = gt, q = eq;
+      int g = gt, q = eq;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, g, o), y = __shfl_up_sync(0xffffffffu, q, o);
-      if (lane >= o) {
-        g += x;
-        q += y;
-      }
-    }
-    if (lane == 31) {
-      scan[0][warp] = g;
-      scan[1][warp] = q;
-    }
-    __syncthreads();
-    int all_gt = 0;
-    g -= gt;
-    q -= eq;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const int x = scan[0][w], y = scan[1][w];
-      all_gt += x;
-      g += w < warp ? x : 0;
-      q += w < warp ? y : 0;
-    }
-    const int ties = need - all_gt;
-    int at = lo + g + min(q, ties);
-    if (gt + eq > 0)
-#pragma unroll 4
-      for (int p = p0; p < p1; ++p) {
-        const uint32_t k = key(p);
-        const bool tie = k == cut;
-        if (k > cut || (tie && q < ties)) {
-          if (owns(at)) kept[at] = p;
-          ++at;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, g, o), y = __shfl_up_sync(0xffffffffu, q, o);
+        if (lane >= o) {
+          g += x;
+          q += y;
         }
-        q += tie;
       }
+      if (lane == 31) {
+        scan[0][warp] = g;
+        scan[1][warp] = q;
+      }
+      __syncthreads();
+      int all_gt = 0, all_eq = 0;
+      g -= gt;
+      q -= eq;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const int x = scan[0][w], y = scan[1][w];
+        all_gt += x;
+        all_eq += y;
+        g += w < warp ? x : 0;
+        q += w < warp ? y : 0;
+      }
+      const int t = max(ties - eq_before, 0);  // that stay of this window's
+      int at = kept_before + g + min(q, t);
+      if (gt + eq > 0)
+#pragma unroll 4
+        for (int p = p0; p < p1; ++p) {
+          const uint32_t k = keys[p - w0];
+          const bool tie = k == cut;
+          if (k > cut || (tie && q < t)) {
+            if (owns(at)) kept[at] = p;
+            ++at;
+          }
+          q += tie;
+        }
+      kept_before += all_gt + min(all_eq, t);
+      eq_before += all_eq;
+    }
     for (int j = tid; j < lo; j += T)
       if (owns(j)) kept[j] = j;
     for (int j = m - a.recent + tid; j < m; j += T)
@@ -433,17 +454,22 @@ static cudaError_t launch_evict_one(const EvictArgs& a, int n_layers, int dev, i
   const long long rows = static_cast<long long>(a.B) * a.Hkv * n_layers;
   int cluster = 1;
   while (cluster < 8 && rows * cluster * 2 <= sms) cluster *= 2;
+  const bool alone = rows * cluster <= sms &&
+                     static_cast<long long>(a.bt_stride) * kPage > kMostKeys;
+  const int room = alone ? kMostKeysAlone : kMostKeys;
+  const size_t smem = std::max(EvictShape<S, DH>::SMEM, room * 4);
   static std::atomic<uint64_t> done{0};
   if (dev >= 64 || !((done.load(std::memory_order_relaxed) >> dev) & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<S, DH, IN_PLACE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               EvictShape<S, DH>::SMEM);
+                                               std::max(EvictShape<S, DH>::SMEM,
+                                                        kMostKeysAlone * 4));
     if (e != cudaSuccess) return e;
     if (dev < 64) done.fetch_or(1ull << dev);
   }
   return launch_pdl_cluster(kv_evict_kernel<S, DH, IN_PLACE>,
                             dim3(static_cast<unsigned>(a.B) * a.Hkv * cluster, n_layers),
-                            dim3(kEvictThreads), EvictShape<S, DH>::SMEM, s, cluster, a, cluster);
+                            dim3(kEvictThreads), smem, s, cluster, a, cluster, room);
 }
 
 template <typename S>

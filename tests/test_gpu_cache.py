@@ -670,7 +670,8 @@ def test_evict(dt, D, H, fresh, case):
     _check_evict(c, before, ref, dt, theta, kept, new)
 
 
-@pytest.mark.parametrize("n,budget", [(70_001, 65_537), (70_001, 900), (40_000, 20_000)])
+@pytest.mark.parametrize("n,budget", [(70_001, 65_537), (70_001, 900), (40_000, 20_000),
+                                      (120_000, 5_000)])
 @pytest.mark.parametrize("fresh", [False, True])
 def test_evict_long_rows(n, budget, fresh):
     torch, B = _lib()
@@ -682,6 +683,24 @@ def test_evict_long_rows(n, budget, fresh):
                               rope_theta=1e4, dst_table=None if dst is None else _i32(dst))
     ref = C.evict(*before, c.table, np.array([n]), budget, 5, 700, 1e4, dst)
     _check_evict(c, before, ref, "bf16", 1e4, kept, new)
+
+
+def test_evict_long_rows_of_equal_scores():
+    """Ties that cross what the shared memory holds at once, alone on the
+    device and beside other rows."""
+    torch, B = _lib()
+    for lens, H in (([60_000], 1), ([30_000, 100] * 20, 4)):
+        c = Cache(np.random.default_rng(37), lens, H, 64, "f32")
+        s = np.zeros(tuple(c.scores.shape), np.float32)
+        s[::3] = 0.25
+        c.scores.copy_(torch.from_numpy(s))
+        before = _host(c.scores)
+        n = lens[0]
+        kept, new = B.pe_kv_evict([c.pool], c.t, _i32(lens), n - 7_000, 3, 11)
+        for b in (0, len(lens) - 2 if len(lens) > 1 else 0):
+            row = np.concatenate([before[c.table[b, i], 0] for i in range(-(-n // 16))])[:n]
+            want = C.keep(row, n - 7_000, 3, 11)
+            assert np.array_equal(kept[0, b, 0].cpu().numpy(), want)
 
 
 def test_evict_into_its_own_table_is_in_place():
