@@ -1244,7 +1244,7 @@ __global__ void __launch_bounds__(DecodeShape<DT, DH, GT>::WARPS * 32,
 // Items that several CTAs share: block c joins the one whose first part is
 // CTA c's last; blocks of y take a share of the rows.  The parts' m and l come
 // in at once, then the products with every part's load in flight together.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;  // blocks of y
 template <int DT, int DH, int GT>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
