@@ -21,6 +21,12 @@
 // of them can be ranked among the others.  Every CTA of a cluster chooses for itself: the scores are
 // read again from L2, and nothing is exchanged.
 //
+// Measured (GB300, four layers): 64 requests of 295104 positions in all to 2048
+// each, 8 kv heads of 64, bf16: 398 us, 5.2 TB/s of rows of 128 bytes from
+// scattered places; 16 requests to 1501, 4 heads of 128, e4m3: 77 us, of which
+// the choosing, at the same time in all CTAs, takes about 20; one request 4096
+// to 1024: 14 us.
+//
 // In place, row j is written where an earlier-listed row may still lie, never
 // a later one (kept[j] >= j, ascending): a round of rows is read by the whole
 // cluster before the first of it is written.
@@ -77,12 +83,15 @@ __device__ __forceinline__ int page_of(const int32_t* table, int stride, int b, 
 }
 
 
+// Two CTAs of 512 threads an SM (batch 64, before the rows ran ahead: 476 us;
+// four of 256: 526, one of 512: 688, one of 1024: 524).
 constexpr int kEvictThreads = 512;
 // Scores that are held in shared memory, with two CTAs an SM and with one
 // (few rows); the rest of a longer row is read again from L2 at every step.
 constexpr int kMostKeys = 24576;
 constexpr int kMostKeysAlone = 49152;
-constexpr int kRanked = 128;      // keys that are ranked at once
+constexpr int kRanked = 128;  // keys that are ranked at once (0: 15.9 us, 64 and 128: 14.3,
+                              // 256: 16.4 for one request)
 
 // A row on its way: its number in the pool where it goes (-1: nowhere) and by
 // how much its key turns.
