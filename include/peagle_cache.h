@@ -182,7 +182,9 @@ pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
  * given.  No other result changes.  The step's attention computes rows in
  * tiles and keeps no weights, so they come from a pass of their own over each
  * layer's K (three launches a layer): collect on the steps where they
- * are worth it.
+ * are worth it.  The step does not clear scores: a request that takes over
+ * pages finds theirs (pe_kv_append and pe_kv_evict clear what they free or
+ * fill).
  * scores: HOST array of n_layers device pointers, copied; NULL turns the
  * collecting off.  The first call allocates the pass's workspace on the
  * handle: make it outside a graph capture.  A step with a larger batch or
