@@ -150,6 +150,7 @@ struct pe_handle {
   // i + b dh/2), one copy per layer, for the fused RoPE epilogue
   std::vector<void*> qkv_il;
   std::vector<void*> allocations;
+  cudaStream_t clears = nullptr;  // clears new allocations, nothing else
 };
 
 namespace {
@@ -162,14 +163,25 @@ cudaError_t counted(pe_handle* h, cudaError_t e) {
   return e;
 }
 
+// Device memory of the handle, cleared.  The clear runs on a stream of its own
+// and has ended when this returns: cudaMemset's would run on the default
+// stream, behind whatever is queued there, and nothing orders that before a
+// step on a non-blocking stream.
 template <typename T>
 cudaError_t dev_alloc(pe_handle* h, T** p, size_t count) {
+  const size_t bytes = std::max<size_t>(count, 1) * sizeof(T);
+  if (!h->clears)
+    if (cudaError_t e = cudaStreamCreateWithFlags(&h->clears, cudaStreamNonBlocking);
+        e != cudaSuccess)
+      return e;
   void* raw = nullptr;
-  cudaError_t e = cudaMalloc(&raw, std::max<size_t>(count, 1) * sizeof(T));
+  cudaError_t e = cudaMalloc(&raw, bytes);
   if (e != cudaSuccess) return e;
   h->allocations.push_back(raw);
-  *p = static_cast<T*>(raw);
-  return cudaMemset(raw, 0, std::max<size_t>(count, 1) * sizeof(T));
+  e = cudaMemsetAsync(raw, 0, bytes, h->clears);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(h->clears);
+  if (e == cudaSuccess) *p = static_cast<T*>(raw);
+  return e;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -286,6 +298,7 @@ pe_status pe_destroy(pe_handle* h) {
   if (!h) return PE_ERR_INVALID_ARGUMENT;
   cudaDeviceSynchronize();
   for (void* p : h->allocations) cudaFree(p);
+  if (h->clears) cudaStreamDestroy(h->clears);
   delete h;
   return PE_OK;
 }
