@@ -10,6 +10,7 @@
 #include "../../include/peagle_cache.h"
 #include "pe_common.cuh"
 #include "pe_kernels.h"
+#include "score_room.h"
 
 namespace pe {
 cudaError_t launch_gemm_tc_maps(const CUtensorMap& wa, const CUtensorMap& wa2,
@@ -123,8 +124,7 @@ struct pe_handle {
   // scores of the cached positions, one array a layer (pe_set_kv_scores)
   std::vector<float*> kv_scores;
   void* score_out = nullptr;  // [max_reqs, Hq dh]
-  char* score_ws = nullptr;
-  int64_t score_ws_bytes = 0;
+  pe::ScoreRoom score_room;
   float* trace = nullptr;
   void* attn_trace = nullptr;
   std::vector<cudaEvent_t> phase_events;  // 2 + 2 L events, or none
@@ -182,6 +182,17 @@ cudaError_t dev_alloc(pe_handle* h, T** p, size_t count) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(h->clears);
   if (e == cudaSuccess) *p = static_cast<T*>(raw);
   return e;
+}
+
+// Device memory of the handle as it comes, nullptr where there is none.
+char* dev_alloc_uncleared(pe_handle* h, int64_t bytes) {
+  void* raw = nullptr;
+  if (cudaMalloc(&raw, static_cast<size_t>(bytes)) != cudaSuccess) {
+    cudaGetLastError();  // not an error of the caller's
+    return nullptr;
+  }
+  h->allocations.push_back(raw);
+  return static_cast<char*>(raw);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -463,16 +474,18 @@ pe_status pe_set_kv_scores(pe_handle* h, float* const* scores) {
   const pe_model_desc& d = h->desc;
   for (int l = 0; l < d.n_layers; ++l)
     if (!scores[l] || !aligned16(scores[l])) return PE_ERR_INVALID_ARGUMENT;
-  if (!h->score_ws) {
+  if (!h->score_room.ptr) {
     const int64_t bytes =
-        draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim);
+        draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim, 0);
     if (bytes <= 0) return PE_ERR_CUDA;
     const size_t out = static_cast<size_t>(h->max_reqs) * d.n_heads * d.head_dim * h->esize;
-    char* o = nullptr;
-    if (dev_alloc(h, &o, out)) return PE_ERR_OUT_OF_MEMORY;
-    h->score_out = o;
-    if (dev_alloc(h, &h->score_ws, static_cast<size_t>(bytes))) return PE_ERR_OUT_OF_MEMORY;
-    h->score_ws_bytes = bytes;
+    if (!h->score_out) {
+      char* o = nullptr;
+      if (dev_alloc(h, &o, out)) return PE_ERR_OUT_OF_MEMORY;
+      h->score_out = o;
+    }
+    h->score_room.grow(bytes, bytes, [&](int64_t n) { return dev_alloc_uncleared(h, n); });
+    if (!h->score_room.ptr) return PE_ERR_OUT_OF_MEMORY;
   }
   try {
     h->kv_scores.assign(scores, scores + d.n_layers);
@@ -668,17 +681,18 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
     return PE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!h->kv_scores.empty()) {
-    // room for the pass's logits grows with the batch and the block table;
-    // a captured step makes do with what there is
-    const int64_t want = pe_attn_decode_workspace(B, d.n_heads, d.n_kv_heads, d.head_dim, bt_stride);
+    // room for the pass's logits grows with the batch and the block table; a
+    // captured step makes do with what there is
+    auto room = [&](int32_t reqs, int32_t width) {
+      return draft_scores_workspace(reqs, d.n_heads, d.n_kv_heads, d.head_dim, width);
+    };
+    const int64_t want = room(B, bt_stride);
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (want > h->score_ws_bytes &&
-        cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone) {
-      char* ws = nullptr;
-      if (dev_alloc(h, &ws, static_cast<size_t>(want))) return PE_ERR_OUT_OF_MEMORY;
-      h->score_ws = ws;
-      h->score_ws_bytes = want;
-    }
+    if (want > h->score_room.bytes &&
+        cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
+        !h->score_room.grow(want, room(h->max_reqs, INT32_MAX),
+                            [&](int64_t n) { return dev_alloc_uncleared(h, n); }))
+      return PE_ERR_OUT_OF_MEMORY;
   }
   h->gemm_ordinal = 0;
   const int rows = ex->T_out;
@@ -886,8 +900,8 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
       ds.block_table = block_table;
       ds.seq_lens = ex->seq_lens;
       ds.out = h->score_out;
-      ds.workspace = h->score_ws;
-      ds.workspace_bytes = h->score_ws_bytes;
+      ds.workspace = h->score_room.ptr;
+      ds.workspace_bytes = h->score_room.bytes;
       ds.err = h->err;
       if (const pe_status st = launch_draft_scores(ds, s); st != PE_OK) return st;
       h->launches += 3;

@@ -1673,8 +1673,8 @@ pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
   a.err = d.err;
   return launch_decode_pool<false>(a, d.dtype, d.dh, d.workspace, d.workspace_bytes, dev, sms, true, s);
 }
-int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh) {
-  return pe_attn_decode_workspace(B, Hq, Hkv, dh, 0);
+int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh, int bt_stride) {
+  return pe_attn_decode_workspace(B, Hq, Hkv, dh, bt_stride);
 }
 
 }  // namespace pe

@@ -71,3 +71,31 @@ def test_first_steps_on_a_side_stream_beside_queued_work(dtype, collect):
         dr.close()
         got.append(results)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got))
+
+
+def test_a_table_that_widens_step_by_step_keeps_memory_bounded():
+    """The room for the scores' logits at least doubles when it grows, so
+    that all of it stays below twice the last (here below 4 times what the
+    widest table wants), however many steps widen the table."""
+    import torch
+    from tests import gpu_helpers as G
+    B, wl, inp, w, cache = _setup()
+    narrow = np.asarray(inp.block_table).shape[1]
+    widths = [narrow + 25 * i for i in range(80)]
+    want = B.pe_attn_decode_workspace(wl.B, 8, 2, 64, widths[-1])
+    used = []
+    for collect in (False, True):
+        dr = G.make_drafter(wl.shape, w, wl.T_out, wl.B)
+        B.pe_set_kv_scores(dr, _scores(inp) if collect else None)
+        st = _step_inputs(wl, inp, cache, widths[0])
+        assert G.run_step(dr, st)["err"] == 0
+        tables = [_step_inputs(wl, inp, cache, x).block_table for x in widths]
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        held = torch.cuda.memory_reserved()
+        for t in tables:
+            st.block_table = t
+            assert G.run_step(dr, st, want_logits=False)["err"] == 0
+        used.append(before - torch.cuda.mem_get_info()[0] - (torch.cuda.memory_reserved() - held))
+        dr.close()
+    assert used[1] - used[0] <= 4 * want + (8 << 20), (used, want)
