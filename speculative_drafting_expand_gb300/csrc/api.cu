@@ -474,6 +474,7 @@ pe_status pe_set_kv_scores(pe_handle* h, float* const* scores) {
   const pe_model_desc& d = h->desc;
   for (int l = 0; l < d.n_layers; ++l)
     if (!scores[l] || !aligned16(scores[l])) return PE_ERR_INVALID_ARGUMENT;
+  h->score_room.refused = INT64_MAX;  // there may be memory again
   if (!h->score_room.ptr) {
     const int64_t bytes =
         draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim, 0);
@@ -689,10 +690,9 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
     const int64_t want = room(B, bt_stride);
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (want > h->score_room.bytes &&
-        cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone &&
-        !h->score_room.grow(want, room(h->max_reqs, INT32_MAX),
-                            [&](int64_t n) { return dev_alloc_uncleared(h, n); }))
-      return PE_ERR_OUT_OF_MEMORY;
+        cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap == cudaStreamCaptureStatusNone)
+      h->score_room.grow(want, room(h->max_reqs, INT32_MAX),
+                         [&](int64_t n) { return dev_alloc_uncleared(h, n); });
   }
   h->gemm_ordinal = 0;
   const int rows = ex->T_out;
