@@ -165,7 +165,7 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  * PE_ERR_INVALID_ARGUMENT: n_layers outside [1, 64], B < 1, budget < 1,
  * sinks or recent < 0 or together above budget, rope_theta negative or not
  * finite, pools that differ or have no scores, a null or misaligned pointer,
- * new_lens == seq_lens.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128,
+ * new_lens == seq_lens, dst_table == block_table with another stride.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128,
  * more than 2^31 - 1 entries of kept, budget past 2^30 or bt_stride past
  * 2^26. */
 pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,

@@ -514,7 +514,10 @@ extern "C" pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int3
     return PE_ERR_INVALID_ARGUMENT;
   const int64_t rows = static_cast<int64_t>(B) * pools[0].n_kv_heads;
   // the same pages as before: in place
-  if (dst_table == block_table && dst_stride == bt_stride) dst_table = nullptr;
+  if (dst_table == block_table) {
+    if (dst_stride != bt_stride) return PE_ERR_INVALID_ARGUMENT;
+    dst_table = nullptr;
+  }
   // positions and list entries are counted in 32 bits
   if (budget > (1 << 30) || bt_stride > (1 << 26) || rows * n_layers > 2147483647LL / budget)
     return PE_ERR_UNSUPPORTED;
