@@ -570,7 +570,8 @@ def _cache_empty(pool: KvPool, shape, dtype, stream):
 # Workspaces of eager calls, one a device and stream: calls on one stream run
 # one after another, so they can share it.  Memory of its own goes to a
 # captured call (its graph's: a replay may run beside anything), to a call on
-# a stream other than the current one, and to one that wants a lot.
+# a stream other than the current one or a device other than the current one,
+# and to one that wants a lot.
 _CACHE_WORKSPACES: Dict = {}
 _CACHE_SHARED_MOST = 64 << 20
 # held while the launches of a call with a shared workspace are queued: another
@@ -579,8 +580,10 @@ _CACHE_LOCK = threading.Lock()
 
 
 def _cache_shares(pool: KvPool, nbytes: int, stream) -> bool:
+    # the last question is about the current device's stream
+    C = pool.torch._C
     return (nbytes <= _CACHE_SHARED_MOST and stream is None and pool.index >= 0
-            and not pool.torch._C._cuda_isCurrentStreamCapturing())
+            and C._cuda_getDevice() == pool.index and not C._cuda_isCurrentStreamCapturing())
 
 
 def _cache_shared_workspace(pool: KvPool, nbytes: int):
