@@ -90,7 +90,9 @@ pe_status pe_kv_append(const pe_kv_pool* pool, int32_t T, int32_t B, int32_t n_h
  * device; 0 on a bad argument.  bt_stride 0: what every call needs (the
  * lengths do not matter).  bt_stride > 0: with room for the logits of a table
  * of that width, at most 1 GiB of them, which a call with accumulate keeps
- * there instead of working them out twice. */
+ * there instead of working them out twice.  It keeps those of up to 16 query
+ * heads a kv head (fp32 pools: 8 of head_dim 64, 4 of 128); with more heads
+ * none, and bt_stride changes nothing past 16 (fp32: give 0). */
 int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
                                  int32_t head_dim, int32_t bt_stride);
 

@@ -647,12 +647,19 @@ def pe_attn_decode_workspace(B: int, n_heads: int, n_kv_heads: int, head_dim: in
                              pages: int = 0) -> int:
     """Bytes of workspace of a pe_attn_decode call on the current device; with
     `pages`, the block table's width, room for the logits of a call that
-    accumulates (it then works them out once instead of twice)."""
+    accumulates (it then works them out once instead of twice; not beyond 16
+    query heads a kv head, with float32 pools 8 of head_dim 64 and 4 of 128)."""
     _cache_ints(B=B, n_heads=n_heads, pages=pages)
     n = lib().pe_attn_decode_workspace(B, n_heads, n_kv_heads, head_dim, pages)
     if n <= 0:
         raise ValueError("pe_attn_decode_workspace: bad sizes")
     return n
+
+
+def _cache_logits_width(pool: KvPool, n_heads: int, pages: int) -> int:
+    """Table width to make room for: 0 where a call keeps no logits."""
+    most = 16 if pool.dtype != PE_KV_F32 else 8 if pool.head_dim == 64 else 4
+    return pages if n_heads <= most * pool.n_kv_heads else 0
 
 
 def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float] = None,
@@ -681,7 +688,7 @@ def pe_attn_decode(pool: KvPool, q, block_table, seq_lens, scale: Optional[float
         raise ValueError(f"lse must be contiguous float32 [{B}, {n_heads}]")
     os_ = _cache_rows(pool, "out", out, B, n_heads)
     if workspace is None:
-        room = pages if accumulate else 0
+        room = _cache_logits_width(pool, n_heads, pages) if accumulate else 0
         n = pool._workspace.get((B, n_heads, room))
         if n is None:
             with torch.cuda.device(pool.index):

@@ -284,6 +284,11 @@ cudaError_t linear(pe_handle* h, const void* x, int ldx, const void* w, const vo
                                         h->err, s));
 }
 
+// pe_kv_dtype of the pools that the step is given.
+int pool_dtype(const pe_handle* h) {
+  return h->desc.dtype == PE_DTYPE_F32 ? PE_KV_F32 : h->kv_fp8 ? PE_KV_E4M3 : PE_KV_BF16;
+}
+
 EpiArgs epi_none() {
   EpiArgs e = {};
   return e;
@@ -477,7 +482,7 @@ pe_status pe_set_kv_scores(pe_handle* h, float* const* scores) {
   h->score_room.refused = INT64_MAX;  // there may be memory again
   if (!h->score_room.ptr) {
     const int64_t bytes =
-        draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim, 0);
+        draft_scores_workspace(h->max_reqs, d.n_heads, d.n_kv_heads, d.head_dim, pool_dtype(h), 0);
     if (bytes <= 0) return PE_ERR_CUDA;
     const size_t out = static_cast<size_t>(h->max_reqs) * d.n_heads * d.head_dim * h->esize;
     if (!h->score_out) {
@@ -685,7 +690,8 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
     // room for the pass's logits grows with the batch and the block table; a
     // captured step makes do with what there is
     auto room = [&](int32_t reqs, int32_t width) {
-      return draft_scores_workspace(reqs, d.n_heads, d.n_kv_heads, d.head_dim, width);
+      return draft_scores_workspace(reqs, d.n_heads, d.n_kv_heads, d.head_dim, pool_dtype(h),
+                                    width);
     };
     const int64_t want = room(B, bt_stride);
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -883,7 +889,7 @@ pe_status pe_draft_forward(pe_handle* h, const pe_expanded* ex, int32_t B, int32
       ds.Hq = d.n_heads;
       ds.Hkv = d.n_kv_heads;
       ds.dh = d.head_dim;
-      ds.dtype = dt == PE_DTYPE_F32 ? PE_KV_F32 : h->kv_fp8 ? PE_KV_E4M3 : PE_KV_BF16;
+      ds.dtype = pool_dtype(h);
       ds.num_blocks = num_blocks;
       ds.bt_stride = bt_stride;
       ds.k = k_cache[l];

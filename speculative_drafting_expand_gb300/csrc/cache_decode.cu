@@ -1624,6 +1624,12 @@ static pe_status launch_decode_heads(DecodeArgs& a, char* ws, char* ws_end, int 
 // Logits that a call with accumulate may keep: more are worked out again.
 constexpr int64_t kMostLogits = int64_t{1} << 30;  // bytes
 
+// Query heads a kv head whose logits a call can keep: those of one tile.
+static int most_kept_heads(int dtype, int dh) {
+  if (dtype != PE_KV_F32) return DecodeShape<PE_KV_BF16, 64, 2>::ROWS;
+  return dh == 64 ? DecodeShape<PE_KV_F32, 64, 1>::ROWS : DecodeShape<PE_KV_F32, 128, 1>::ROWS;
+}
+
 // The largest of the pool types: two CTAs an SM, 8 or 16 rows a tile.
 static int64_t workspace_bytes_for(int64_t B, int n_heads, int n_kv_heads, int head_dim, int sms) {
   const int64_t grid = 2 * sms, rows = n_heads / n_kv_heads > 8 ? 16 : 8;
@@ -1673,8 +1679,9 @@ pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
   a.err = d.err;
   return launch_decode_pool<false>(a, d.dtype, d.dh, d.workspace, d.workspace_bytes, dev, sms, true, s);
 }
-int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh, int bt_stride) {
-  return pe_attn_decode_workspace(B, Hq, Hkv, dh, bt_stride);
+int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh, int dtype, int bt_stride) {
+  return pe_attn_decode_workspace(B, Hq, Hkv, dh,
+                                  Hq / Hkv <= most_kept_heads(dtype, dh) ? bt_stride : 0);
 }
 
 }  // namespace pe
@@ -1690,7 +1697,10 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
   const int sms = pe::sm_count(dev);
   if (sms < 1) return 0;
   const int64_t rows = n_heads / n_kv_heads > 8 ? 16 : 8;
-  const double logits = 1.0 * B * bt_stride * n_kv_heads * pe::kPage * rows * 4;
+  // (fp32 pools keep those of fewer heads; the type is not known here)
+  const double logits = n_heads / n_kv_heads > pe::most_kept_heads(PE_KV_BF16, head_dim)
+                            ? 0.0
+                            : 1.0 * B * bt_stride * n_kv_heads * pe::kPage * rows * 4;
   return pe::workspace_bytes_for(B, n_heads, n_kv_heads, head_dim, sms) +
          (logits < pe::kMostLogits ? static_cast<int64_t>(logits) : pe::kMostLogits);
 }

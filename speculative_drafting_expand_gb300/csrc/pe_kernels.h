@@ -399,7 +399,8 @@ struct DraftScoresArgs {
   int* err;
 };
 pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s);
-// Bytes for B requests; bt_stride > 0: with room for that table's logits.
-int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh, int bt_stride);
+// Bytes for B requests; bt_stride > 0: with room for that table's logits,
+// where they are kept.
+int64_t draft_scores_workspace(int B, int Hq, int Hkv, int dh, int dtype, int bt_stride);
 
 }  // namespace pe

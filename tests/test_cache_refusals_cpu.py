@@ -27,3 +27,15 @@ def test_a_captured_call_never_takes_a_shared_workspace(B, current, capturing, s
     assert B._cache_shares(pool, 1024, None) is shares
     assert not B._cache_shares(pool, 1 << 40, None)
     assert not B._cache_shares(pool, 1024, object())
+
+
+@pytest.mark.parametrize("dt,dim,group,keeps", [
+    ("bf16", 64, 16, True), ("bf16", 128, 17, False), ("e4m3", 64, 9, True), ("e4m3", 64, 40, False),
+    ("f32", 64, 8, True), ("f32", 64, 9, False), ("f32", 128, 4, True), ("f32", 128, 5, False)])
+def test_room_for_logits_only_where_they_are_kept(B, dt, dim, group, keeps):  # noqa: F811
+    """One tile of query heads a kv head: 16 for 16- and 8-bit pools; 8 or 4
+    for fp32 ones of 64 or 128."""
+    import types
+    kind = {"bf16": B.PE_KV_BF16, "e4m3": B.PE_KV_E4M3, "f32": B.PE_KV_F32}[dt]
+    pool = types.SimpleNamespace(dtype=kind, head_dim=dim, n_kv_heads=2)
+    assert B._cache_logits_width(pool, 2 * group, 100) == (100 if keeps else 0)

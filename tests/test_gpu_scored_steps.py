@@ -99,3 +99,16 @@ def test_a_table_that_widens_step_by_step_keeps_memory_bounded():
         used.append(before - torch.cuda.mem_get_info()[0] - (torch.cuda.memory_reserved() - held))
         dr.close()
     assert used[1] - used[0] <= 4 * want + (8 << 20), (used, want)
+
+
+def test_room_for_logits_only_where_they_are_kept():
+    """Logits are kept where one tile holds all query heads of a kv head; more
+    heads ask for no room for them."""
+    from speculative_drafting_expand_gb300 import binding as B
+    for heads, kv_heads in ((17, 1), (40, 1), (96, 4)):
+        for dim in (64, 128):
+            assert B.pe_attn_decode_workspace(3, heads, kv_heads, dim, 50) == \
+                B.pe_attn_decode_workspace(3, heads, kv_heads, dim)
+    for heads in (1, 8, 9, 16):
+        assert B.pe_attn_decode_workspace(3, heads, 1, 64, 50) - \
+            B.pe_attn_decode_workspace(3, heads, 1, 64) == 3 * 50 * 16 * (16 if heads > 8 else 8) * 4
