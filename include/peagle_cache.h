@@ -115,7 +115,11 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * of the activation type: rows `*_stride` elements apart, heads contiguous,
  * rows 16-byte aligned.  lse:
  * NULL, or fp32 [B, n_heads].  block_table [B, bt_stride], seq_lens [B].
- * Sums, maxima and weights are held in fp32.  workspace: 16-byte aligned,
+ * Logits, maxima, sums and lse are held in fp32, and so are the weights of
+ * fp32 pools and those added to scores.  The weights that multiply v beside
+ * other pools are pairs of 16-bit numbers: right to 2^-17 of themselves, with
+ * e4m3 pools to 2^-21 of themselves or 2^-37 of the largest.  Exponentials are
+ * the hardware's, right to 2^-21.  workspace: 16-byte aligned,
  * workspace_bytes at least pe_attn_decode_workspace(.., 0); contents need not
  * be set and do not carry over; calls that may overlap need one each.
  * Device errors: PE_DEV_BAD_POSITION (seq_lens[b] < 0 or past the table:

@@ -30,10 +30,11 @@
 // bytes an element and 8 heads it is far from its rate.  The orders of the
 // elements along k and of the positions are free as long as both operands
 // share them: they are chosen such that every lane's operand is 16 contiguous
-// bytes of a row.  P enters as two 16-bit numbers (value and remainder, 2^-17
-// of it); with 8 heads the remainders are the otherwise unused rows 8..15.
-// e4m3 pools go through fp16, which holds every code; q is scaled there by a
-// power of two to [1, 2) so that fp16's range does not matter.
+// bytes of a row.  P enters as two 16-bit numbers (value and remainder, which
+// leave 2^-17 of it; fp16: 2^-22, or 2^-37 of the largest weight); with 8
+// heads the remainders are the otherwise unused rows 8..15.  e4m3 pools go
+// through fp16, which holds every code; q is scaled there by a power of two to
+// [1, 2) so that fp16's range does not matter.
 //
 // Measured (GB300, launches alone; 64 query heads on 8 kv heads of 64): 64
 // requests of 372575 positions in all, bf16, 130 us, 5.9 TB/s of K and V (a
@@ -544,8 +545,16 @@ template <int DT, int DH, int GT>
 struct MmaTile {
   using SH = DecodeShape<DT, DH, GT>;
   static constexpr int NT = DH / 8;  // tiles of 8 elements
+  // Weights enter P V as pairs of 16-bit numbers.  fp16 ends at 2^-24, so the
+  // weights are 2^LIFT times those that the running maximum gives: one below
+  // 2^-25 of the largest would be nothing there, while l counts it in full
+  // (31 positions of 2^-26 beside one whose value is 0: an output of 0).
+  // Lifted, what a pair loses is at most 2^-37 of the largest.  2^4 is left
+  // below fp16's end for a logit that its own rounding puts above the maximum.
+  static constexpr float LIFT = DT == PE_KV_E4M3 ? 12.f : 0.f;
   QueryTile<DT, DH, GT> q;
-  float m[GT], l[GT];                // head g + 8 x; l of this lane's positions
+  float m[GT], l[GT];                // head g + 8 x, m: the maximum less LIFT; l of
+                                     // this lane's positions
   float o[NT][4];
 
   __device__ __forceinline__ void start(const DecodeArgs& A, int b, int h0, int rows, char*,
@@ -605,7 +614,7 @@ struct MmaTile {
         top[x] = fmax3(top[x], fmaxf(z[n][x][0][0], z[n][x][0][1]),
                        fmaxf(z[n][x][1][0], z[n][x][1][1]));
       top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * q.factor[x];
+      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * q.factor[x] - LIFT;
       grow |= top[x] > m[x];
     }
     if (__any_sync(0xffffffffu, grow)) {

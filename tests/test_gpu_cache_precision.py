@@ -1,0 +1,56 @@
+"""Where pe_attn_decode could lose what its types hold: weights far below the
+largest, and queries near the ends of bf16's range, beside e4m3 pools."""
+
+import numpy as np
+import pytest
+
+from oracle import kv_cache_oracle as C
+from oracle.fp8_kv import e4m3_encode
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _pools(k, v, k_scale=1.0):
+    """One request's rows k, v [n, D] (values that e4m3 holds) in pages."""
+    import torch
+    from speculative_drafting_expand_gb300 import binding as B
+    n, D = k.shape
+    pages = -(-n // 16)
+    pools = []
+    for x in (k, v):
+        codes = np.zeros((pages * 16, D), np.uint8)
+        codes[:n] = e4m3_encode(x)
+        pools.append(torch.from_numpy(codes.reshape(pages, 1, 16, D)).cuda())
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    return B, B.KvPool(*pools, None, k_scale, 1.0), table
+
+
+@pytest.mark.parametrize("heads", [1, 8, 16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("below", [10, 14, 16, 18, 20, 24])
+def test_e4m3_weights_far_below_the_largest(D, heads, below):
+    """One position holds (almost) all the weight and a value of 0, 31 others
+    e^-below of it each and a value of 1: the output is their weights' sum.
+
+    Tolerance: a weight is a pair of fp16 numbers whose step is at most 2^-24
+    of 2^12 times the largest weight's 1, so off by at most 2^-37 each, or
+    2^-17 of itself for larger ones; the logits are exact here (products of
+    small whole numbers), their scaling to units of ln 2 is off by 3 u of it,
+    twice, and the exponential by 2^-21; then half a step of bf16."""
+    import torch
+    n = 32
+    k, v = np.zeros((n, D)), np.ones((n, D))
+    k[5, 3], v[5] = below, 0.0
+    B, pool, table = _pools(k, v)
+    q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 3] = 1.0
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = B.pe_attn_decode(pool, q, table, lens, scale=1.0)
+    small = (n - 1) * np.exp(-float(below))
+    want = small / (1 + small)
+    got = out.double().cpu().numpy()
+    exact = (n - 1) * 2.0 ** -37 + want * (2.0 ** -17 + 6 * U * below * np.log2(np.e) + 2.0 ** -20)
+    assert np.all(np.abs(got - want) <= exact + 2.0 ** -8 * (want + exact))
+    ref = below + np.log1p(small)
+    assert np.all(np.abs(lse.double().cpu().numpy() - ref) <= 2.0 ** -20 + 8 * U * ref)
