@@ -33,8 +33,9 @@
 // bytes of a row.  P enters as two 16-bit numbers (value and remainder, which
 // leave 2^-17 of it; fp16: 2^-22, or 2^-37 of the largest weight); with 8
 // heads the remainders are the otherwise unused rows 8..15.  e4m3 pools go
-// through fp16, which holds every code; q is scaled there by a power of two to
-// [1, 2) so that fp16's range does not matter.
+// through fp16, which holds every code; q is scaled there by a power of two so
+// that its largest element is in [1, 2) and fp16's range does not matter
+// (elements below 2^-24 of that vanish).
 //
 // Measured (GB300, launches alone; 64 query heads on 8 kv heads of 64): 64
 // requests of 372575 positions in all, bf16, 130 us, 5.9 TB/s of K and V (a
@@ -44,6 +45,7 @@
 // and V to the join, and two launches.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "cache_common.cuh"
@@ -493,10 +495,13 @@ struct QueryTile {
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent
-        const bool norm = ex > 1 && ex < 253;
-        const float down = norm ? __uint_as_float(static_cast<uint32_t>(254 - ex) << 23) : 1.f;
-        factor[x] *= norm ? __uint_as_float(static_cast<uint32_t>(ex) << 23) : 1.f;
+        // biased exponent, as far as 2^ex and 2^-ex are both normal numbers: at
+        // the ends q lands in [1, 4) or below 2 instead
+        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+        const float down = __uint_as_float((254 - ex) << 23);
+        // neither 0 nor inf, which would make NaN of the masked positions' -inf
+        // or of sums of 0
+        factor[x] = fminf(fmaxf(factor[x] * __uint_as_float(ex << 23), FLT_MIN), FLT_MAX);
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll

@@ -54,3 +54,38 @@ def test_e4m3_weights_far_below_the_largest(D, heads, below):
     assert np.all(np.abs(got - want) <= exact + 2.0 ** -8 * (want + exact))
     ref = below + np.log1p(small)
     assert np.all(np.abs(lse.double().cpu().numpy() - ref) <= 2.0 ** -20 + 8 * U * ref)
+
+
+@pytest.mark.parametrize("heads", [1, 9])
+@pytest.mark.parametrize("q_size,scale", [
+    (2.0 ** -120, 2.0 ** -32), (2.0 ** -126, 2.0 ** -100), (2.0 ** -126, 2.0 ** 120),
+    (2.0 ** -130, 2.0 ** 126), (2.0 ** 126, 2.0 ** -126), (2.0 ** 127, 2.0 ** -127),
+    (2.0 ** 120, 2.0 ** -120), (1.0, 1.0)])
+def test_e4m3_queries_near_the_ends_of_the_range(heads, q_size, scale):
+    """q and the scale at opposite (or the same) ends of fp32's range, over a
+    page that the request does not fill: logits are their product's.
+
+    Tolerance: q is a power of two and k whole numbers below 16, so sums are
+    exact; scale and factor are rounded a few times (8 u of the logit), the
+    exponentials and pairs of weights as above."""
+    import torch
+    n, D = 21, 64
+    rng = np.random.default_rng(60)
+    k = rng.integers(-3, 4, size=(n, D)).astype(np.float64)
+    v = rng.integers(-8, 9, size=(n, D)).astype(np.float64)
+    B, pool, table = _pools(k, v)
+    signs = rng.choice((-1.0, 1.0), size=(1, heads, D)) * (np.arange(D) < 5)
+    q = torch.from_numpy((signs * q_size).astype(np.float32)).to(torch.bfloat16).cuda()
+    assert np.array_equal(q.double().cpu().numpy(), signs * q_size)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = B.pe_attn_decode(pool, q, table, lens, scale=scale)
+    z = np.einsum("hd,nd->hn", signs[0] * q_size, k) * scale
+    p = np.exp(z - z.max(1, keepdims=True))
+    lse_want = z.max(1) + np.log(p.sum(1))
+    p /= p.sum(1, keepdims=True)
+    want, spread = p @ v, p @ np.abs(v)
+    ez = 8 * U * np.abs(z).max(1)
+    tol = (2 * ez + 2.0 ** -16)[:, None] * spread + 2.0 ** -8 * np.abs(want) + n * 2.0 ** -37 * 8
+    assert np.all(np.abs(out.double().cpu().numpy()[0] - want) <= tol)
+    tol = ez + 2.0 ** -19 + 8 * U * np.abs(lse_want)
+    assert np.all(np.abs(lse.double().cpu().numpy()[0] - lse_want) <= tol)
