@@ -160,8 +160,8 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  * L are set to 0.  In place needs whole requests to be trimmed by one call
  * for each layer; the layers of one call are independent.
  *
- * pools: HOST array of n_layers pools (all with scores, and of the same
- * shape and dtype; num_blocks may differ), copied.  block_table [B,
+ * pools: HOST array of n_layers pools (all with scores, of the same shape and
+ * dtype, each in memory of its own; num_blocks may differ), copied.  block_table [B,
  * bt_stride], seq_lens [B], kept [n_layers, B, n_kv_heads, budget], new_lens
  * [B] (not seq_lens itself).
  * Device errors: PE_DEV_BAD_POSITION (seq_lens[b] < 0 or past the table:
@@ -170,10 +170,10 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  * destination page is not written).
  * PE_ERR_INVALID_ARGUMENT: n_layers outside [1, 64], B < 1, budget < 1,
  * sinks or recent < 0 or together above budget, rope_theta negative or not
- * finite, pools that differ or have no scores, a null or misaligned pointer,
- * new_lens == seq_lens, dst_table == block_table with another stride.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128,
- * more than 2^31 - 1 entries of kept, budget past 2^30 or bt_stride past
- * 2^26. */
+ * finite, pools that differ, share memory or have no scores, a null or
+ * misaligned pointer, new_lens == seq_lens, dst_table == block_table with
+ * another stride.  PE_ERR_UNSUPPORTED: head_dim other than 64 and 128, more
+ * than 2^31 - 1 entries of kept, budget past 2^30 or bt_stride past 2^26. */
 pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                       int32_t budget, int32_t sinks, int32_t recent, float rope_theta,

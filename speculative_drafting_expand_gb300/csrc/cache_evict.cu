@@ -506,6 +506,11 @@ extern "C" pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int3
     if (!pools[l].scores || pools[l].n_kv_heads != pools[0].n_kv_heads ||
         pools[l].head_dim != pools[0].head_dim || pools[l].dtype != pools[0].dtype)
       return PE_ERR_INVALID_ARGUMENT;
+    // layers run at the same time
+    for (int o = 0; o < l; ++o)
+      if (pools[l].k == pools[o].k || pools[l].v == pools[o].v ||
+          pools[l].scores == pools[o].scores)
+        return PE_ERR_INVALID_ARGUMENT;
   }
   if (B < 1 || !block_table || bt_stride < 1 || !seq_lens || budget < 1 || sinks < 0 ||
       recent < 0 || static_cast<int64_t>(sinks) + recent > budget || !std::isfinite(rope_theta) ||

@@ -39,3 +39,13 @@ def test_room_for_logits_only_where_they_are_kept(B, dt, dim, group, keeps):  # 
     kind = {"bf16": B.PE_KV_BF16, "e4m3": B.PE_KV_E4M3, "f32": B.PE_KV_F32}[dt]
     pool = types.SimpleNamespace(dtype=kind, head_dim=dim, n_kv_heads=2)
     assert B._cache_logits_width(pool, 2 * group, 100) == (100 if keeps else 0)
+
+
+@pytest.mark.parametrize("shared", ["k", "v", "scores"])
+def test_evict_layers_that_share_a_pool(B, shared):  # noqa: F811
+    """In place, two layers over the same memory would move it at once."""
+    from tests.test_cache_abi_cpu import _pool
+    apart = [dict(k=BASE * (3 * i + 1), v=BASE * (3 * i + 2), scores=BASE * (3 * i + 3))
+             for i in range(3)]
+    apart[2][shared] = apart[0][shared]
+    assert _evict(B, [_pool(B, **x) for x in apart], dict(n=3)) == 1
