@@ -64,8 +64,8 @@ typedef struct {
  * Row t belongs to request req[t] (req NULL: request t, and T = B) and sits
  * at position pos[t].  q_out[t] = rotated q[t]; the page slot of pos[t] gets
  * the rotated k[t] and v[t], and its score (where the pool has scores) 0.
- * rope_theta 0 rotates nothing.  Angles are exact to 2^-32 of a turn;
- * results are rounded once to their type (e4m3: x / scale, nearest even,
+ * rope_theta 0 rotates nothing.  Angles are right to 2^-26 of a turn and, for
+ * rope_theta >= 1, pos * 2^-51 of one; results are rounded once to their type (e4m3: x / scale, nearest even,
  * saturated at +-448).  A row with pos[t] < 0 is padding: nothing of it is
  * written.
  *
@@ -118,8 +118,9 @@ int64_t pe_attn_decode_workspace(int32_t B, int32_t n_heads, int32_t n_kv_heads,
  * Logits, maxima, sums and lse are held in fp32, and so are the weights of
  * fp32 pools and those added to scores.  The weights that multiply v beside
  * other pools are pairs of 16-bit numbers: right to 2^-17 of themselves, with
- * e4m3 pools to 2^-21 of themselves or 2^-37 of the largest.  Exponentials are
- * the hardware's, right to 2^-21.  workspace: 16-byte aligned,
+ * e4m3 pools to 2^-21 of themselves or 2^-37 of the largest.  Beside e4m3
+ * pools an element of q is right to 2^-25 of its row's largest.  Exponentials
+ * are the hardware's, right to 2^-21.  workspace: 16-byte aligned,
  * workspace_bytes at least pe_attn_decode_workspace(.., 0); contents need not
  * be set and do not carry over; calls that may overlap need one each.
  * Device errors: PE_DEV_BAD_POSITION (seq_lens[b] < 0 or past the table:
@@ -150,7 +151,8 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
  * the key of position j (rope_theta 0: keys are moved as they are; a key
  * that stays at its position is copied bit for bit; e4m3: the codes'
  * rotation, rounded and saturated; each trim of a request rounds its moved
- * keys once).  Scores of positions new_lens[b] .. the end of its page are
+ * keys once, after a rotation that with 16- and 8-bit pools is right to 2^-20
+ * of a pair's length).  Scores of positions new_lens[b] .. the end of its page are
  * set to 0.  A drafter or decoder then goes on at position new_lens[b].
  *
  * dst_table [B, dst_stride]: the pages that receive the result, none of

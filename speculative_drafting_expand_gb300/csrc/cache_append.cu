@@ -47,10 +47,12 @@ __device__ __forceinline__ void store_kv(void* base, size_t at, const float (&x)
 // copy v.  Bound by bytes for many rows and by latency for few: every load is
 // on its way before the first use, and the row's sines and cosines (one pair
 // a thread, shared by all heads) are worked out meanwhile.  With more rows
-// than CTAs fit, a CTA takes every grid-th row and the next row's loads are
-// under way while it finishes one.  Measured (GB300): one row of 64 + 8 heads
-// of 64, 2.5 us, a launch's latency; 2048 rows of 32 + 4 heads of 128, 11 us,
-// 3.8 TB/s, about seven rows a CTA one after another.
+// than CTAs fit, a CTA takes every grid-th row and the next row's first loads,
+// one item a thread, are under way while it finishes one.  Measured (GB300):
+// one row of 64 + 8 heads of 64, 2.4 us, a launch's latency; 2048 rows of 32 +
+// 4 heads of 128, 11 us, 3.8 TB/s: 912 CTAs of 192 threads take 2.2 rows each,
+// and of a row's 320 items the 128 that no thread has loaded ahead wait for
+// memory when they are used.
 constexpr int kAppendMost = 384;
 constexpr int kAppendCtas = 3;  // an SM
 

@@ -47,10 +47,11 @@ inline bool row_ok(const void* p, int64_t stride, int64_t width, int elem_bytes)
 
 // ------------------------------------------------------------------ rotary
 // Turns per position of every pair, as a 64-bit fraction of a turn: position
-// times step, modulo 2^64, is the angle's fraction of a turn exactly to the
-// step's own rounding (double: 2^-53 of it), at any position and for
-// negative differences too.  No fp64 arithmetic and no range reduction is
-// left to the kernel.
+// times step, modulo 2^64, is the angle's fraction of a turn, negative
+// differences included, but for the step's own error times the position.  The
+// steps are products of doubles: off by less than 2^-53 of a turn for theta
+// from 10 on, 2^-51 from 1 on (more below, where turns per position exceed 1).
+// No fp64 arithmetic and no range reduction is left to the kernel.
 struct RopeSteps {
   uint64_t step[64];
   int on;
@@ -74,7 +75,9 @@ inline RopeSteps rope_steps(float theta, int head_dim) {
 }
 
 // cos and sin of pos * step: the top 32 bits of the product are the angle in
-// 2^-32 turns, as a signed number in half turns for sincospif.
+// 2^-32 turns, as a signed number in half turns for sincospif.  The float of
+// them has 24 bits, which leaves 2^-26 of a turn (1.6 half steps of fp32 in
+// cos and sin).
 __device__ __forceinline__ void rope_cos_sin(uint64_t step, long long pos, float& c, float& s) {
   const uint64_t turn = step * static_cast<uint64_t>(pos);
   const int32_t top = static_cast<int32_t>(static_cast<uint32_t>(turn >> 32));

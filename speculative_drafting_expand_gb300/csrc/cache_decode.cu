@@ -39,7 +39,7 @@
 //
 // Measured (GB300, launches alone; 64 query heads on 8 kv heads of 64): 64
 // requests of 372575 positions in all, bf16, 130 us, 5.9 TB/s of K and V (a
-// copy: 6.8); 265096 positions, e4m3, with scores, 86 us, where the
+// copy: 6.8); 265096 positions, e4m3, with scores, 87 us, where the
 // instructions of a page (half of it conversions and their shifts) bound it;
 // one request of 4096 positions 9.9 us, the way from length to page ids to K
 // and V to the join, and two launches.
@@ -83,8 +83,8 @@ struct DecodeShape {
   static constexpr int SCRATCH = DT == PE_KV_F32 ? (ROWS * DH + kPage * ROWS + ROWS) * 4 : 0;
   static constexpr int SMEM = WARPS * (RING + SCRATCH);
   // CTAs a SM: one of 8 warps with all the registers, or for the short e4m3
-  // pages two (batch 64, bf16: 130 us with one, 135 with two; e4m3 with
-  // scores: 122 with one, 111 with two)
+  // pages two (batch 64, bf16: 130 us with one, 135 with two and half the
+  // stages; e4m3 with scores: 93.5 with one, 88.5 with two)
   static constexpr int CTAS = DT == PE_KV_E4M3 && DH == 64 ? 2 : 1;
   // the scores' kernel: K alone, two CTAs an SM
   static constexpr int S_TAKE = DT == PE_KV_F32 ? 1 : 2;
