@@ -55,6 +55,7 @@ namespace pe {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLift = 4096.f;  // of weights beside e4m3 pools, see MmaTile
 constexpr int kMaxWarps = 8;  // warps a CTA
 constexpr int kMostCtas = 512;  // so that the join of an item over all of them fits
 // Pages a warp, where there are fewer than the grid could take (one request of
@@ -100,7 +101,7 @@ struct DecodeArgs {
   int B, Hq, Hkv, G, bt_stride, window;
   int tiles;       // tiles of query heads a kv head
   float scale;     // of the logits, with ln 2 and the K scale divided in
-  float v_scale;
+  float v_scale;   // divided by the lift of the weights
   const void* q;
   long long q_stride, out_stride;
   const int32_t* block_table;
@@ -550,16 +551,18 @@ template <int DT, int DH, int GT>
 struct MmaTile {
   using SH = DecodeShape<DT, DH, GT>;
   static constexpr int NT = DH / 8;  // tiles of 8 elements
-  // Weights enter P V as pairs of 16-bit numbers.  fp16 ends at 2^-24, so the
-  // weights are 2^LIFT times those that the running maximum gives: one below
-  // 2^-25 of the largest would be nothing there, while l counts it in full
-  // (31 positions of 2^-26 beside one whose value is 0: an output of 0).
-  // Lifted, what a pair loses is at most 2^-37 of the largest.  2^4 is left
-  // below fp16's end for a logit that its own rounding puts above the maximum.
-  static constexpr float LIFT = DT == PE_KV_E4M3 ? 12.f : 0.f;
+  // Weights enter P V as pairs of 16-bit numbers.  fp16 ends at 2^-24, so they
+  // enter 2^12 times larger (v_scale has the inverse): one below 2^-25 of the
+  // largest would be nothing there, while l counts it in full (31 positions of
+  // 2^-26 beside one whose value is 0: an output of 0).  Lifted, what a pair
+  // loses is at most 2^-37 of the largest.  2^4 is left below fp16's end for a
+  // logit that its own rounding puts above the maximum.  A product a weight
+  // (batch 64 with scores: 88.6 -> 88.9 us); a running maximum 12 lower would
+  // do the same for nothing, but then l and the maximum cancel in an lse near
+  // 0, whose error grows to 2^-21.
+  static constexpr float LIFT = DT == PE_KV_E4M3 ? kLift : 1.f;
   QueryTile<DT, DH, GT> q;
-  float m[GT], l[GT];                // head g + 8 x, m: the maximum less LIFT; l of
-                                     // this lane's positions
+  float m[GT], l[GT];                // head g + 8 x; l of this lane's positions
   float o[NT][4];
 
   __device__ __forceinline__ void start(const DecodeArgs& A, int b, int h0, int rows, char*,
@@ -619,7 +622,7 @@ struct MmaTile {
         top[x] = fmax3(top[x], fmaxf(z[n][x][0][0], z[n][x][0][1]),
                        fmaxf(z[n][x][1][0], z[n][x][1][1]));
       top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * q.factor[x] - LIFT;
+      top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * q.factor[x];
       grow |= top[x] > m[x];
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -651,7 +654,7 @@ struct MmaTile {
           const float p0 = fast_exp2(fmaf(z[n][x][j][0], q.factor[x], -base));
           const float p1 = fast_exp2(fmaf(z[n][x][j][1], q.factor[x], -base));
           l[x] += p0 + p1;
-          split2<DT>(p0, p1, hi[n][x][j], lo[n][x][j]);
+          split2<DT>(p0 * LIFT, p1 * LIFT, hi[n][x][j], lo[n][x][j]);
         }
     }
 #pragma unroll
@@ -1680,7 +1683,7 @@ pe_status launch_draft_scores(const DraftScoresArgs& d, cudaStream_t s) {
   a.bt_stride = d.bt_stride;
   const bool codes = d.dtype == PE_KV_E4M3;
   a.scale = kLog2e / std::sqrt(static_cast<float>(d.dh)) * (codes ? d.k_scale : 1.f);
-  a.v_scale = codes ? d.v_scale : 1.f;
+  a.v_scale = codes ? d.v_scale / kLift : 1.f;
   a.q = d.q;
   a.q_stride = a.out_stride = static_cast<long long>(d.Hq) * d.dh;
   a.q_rows = d.q_rows;
@@ -1751,7 +1754,7 @@ pe_status pe_attn_decode(const pe_kv_pool* pool, int32_t B, int32_t n_heads, flo
   const bool codes = pool->dtype == PE_KV_E4M3;
   a.scale = scale * kLog2e * (codes ? pool->k_scale : 1.f);
   if (!std::isfinite(a.scale)) return PE_ERR_INVALID_ARGUMENT;
-  a.v_scale = codes ? pool->v_scale : 1.f;
+  a.v_scale = codes ? pool->v_scale / kLift : 1.f;
   a.q = q;
   a.q_stride = q_stride;
   a.out_stride = out_stride;

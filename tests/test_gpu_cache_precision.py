@@ -89,3 +89,27 @@ def test_e4m3_queries_near_the_ends_of_the_range(heads, q_size, scale):
     assert np.all(np.abs(out.double().cpu().numpy()[0] - want) <= tol)
     tol = ez + 2.0 ** -19 + 8 * U * np.abs(lse_want)
     assert np.all(np.abs(lse.double().cpu().numpy()[0] - lse_want) <= tol)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("heads", [1, 12])
+@pytest.mark.parametrize("logit", [2.0 ** -30, 2.0 ** -12, 2.0 ** -3, 37.0])
+def test_lse_of_one_position_is_its_logit(dt, heads, logit):
+    """The sum is one exponential of 0, whose logarithm is 0: what is left is
+    the logit, times log2 e and ln 2 in fp32 (6 half steps)."""
+    import torch
+    from speculative_drafting_expand_gb300 import binding as B
+    D = 64
+    act = torch.float32 if dt == "f32" else torch.bfloat16
+    k = torch.zeros(1, 1, 16, D, dtype=act, device="cuda")
+    k[0, 0, 0, 7] = 1.0
+    if dt == "e4m3":
+        k = k.float().to(torch.float8_e4m3fn)
+    q = torch.zeros(1, heads, D, dtype=act, device="cuda")
+    q[:, :, 7] = logit
+    table, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0]], [1]))
+    out, lse = B.pe_attn_decode(B.KvPool(k, k.clone()), q, table, lens, scale=1.0)
+    assert np.all(np.abs(lse.double().cpu().numpy() - logit) <= 6 * U * logit)
+    want = torch.zeros_like(q)
+    want[:, :, 7] = 1.0
+    assert torch.equal(out, want)
