@@ -199,8 +199,9 @@ pe_status pe_kv_evict(int32_t n_layers, const pe_kv_pool* pools, int32_t B,
  * table than before allocates room for its logits: at least twice the room
  * before and at most 1 GiB, all of which stays with the handle (2 GiB in the
  * end).  Logits that find no room, because the step is being captured or
- * there is no memory, are worked out twice.  Calls on one handle must not
- * overlap.  PE_ERR_INVALID_ARGUMENT: a null or misaligned entry;
+ * there is no memory, are worked out twice; room that could not be had is
+ * asked for again after the next pe_set_kv_scores.  Calls on one handle must
+ * not overlap.  PE_ERR_INVALID_ARGUMENT: a null or misaligned entry;
  * PE_ERR_OUT_OF_MEMORY. */
 pe_status pe_set_kv_scores(pe_handle* h, float* const* scores);
 

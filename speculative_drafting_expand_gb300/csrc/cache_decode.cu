@@ -39,7 +39,7 @@
 //
 // Measured (GB300, launches alone; 64 query heads on 8 kv heads of 64): 64
 // requests of 372575 positions in all, bf16, 130 us, 5.9 TB/s of K and V (a
-// copy: 6.8); 265096 positions, e4m3, with scores, 87 us, where the
+// copy: 6.8); 265096 positions, e4m3, with scores, 88 us, where the
 // instructions of a page (half of it conversions and their shifts) bound it;
 // one request of 4096 positions 9.9 us, the way from length to page ids to K
 // and V to the join, and two launches.
