@@ -36,6 +36,7 @@ PE_KV_E4M3 = 2
 
 PE_DEV_BAD_BLOCK = 2
 PE_DEV_BAD_POSITION = 3
+PE_DEV_BAD_TOKEN = 4
 PE_DEV_BAD_ROW = 6
 
 # include/peagle.h and include/peagle_train.h (pe_status_string last: it is
@@ -54,6 +55,10 @@ EXPORTED = ("pe_create", "pe_destroy", "pe_expand_batch", "pe_draft_forward",
 # include/peagle_cache.h
 CACHE_EXPORTED = ("pe_kv_append", "pe_attn_decode_workspace", "pe_attn_decode", "pe_kv_evict",
                   "pe_set_kv_scores")
+
+# include/peagle_w4.h and include/peagle_sample.h
+HEAD_EXPORTED = ("pe_w4_bytes", "pe_w4_pack", "pe_w4_quantize", "pe_w4_linear", "pe_sample",
+                 "pe_verify")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -88,6 +93,11 @@ class pe_kv_pool(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("scores", _vp), ("num_blocks", _i32),
                 ("n_kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class pe_dist(ctypes.Structure):
+    _fields_ = [("max", ctypes.c_float), ("inv", ctypes.c_float), ("cut", ctypes.c_float),
+                ("cut_token", _i32), ("total", _i64), ("token", _i32), ("reserved", _i32)]
 
 
 class PeError(RuntimeError):
@@ -140,9 +150,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pe_set_kv_scores.argtypes = [_vp, P(_vp)]
     lib.pe_kv_evict.argtypes = [_i32, P(pe_kv_pool), _i32, _vp, _i32, _vp, _i32, _i32, _i32,
                                 ctypes.c_float, _vp, _i32, _vp, _vp, _vp, _vp]
-    for name in EXPORTED[:-1] + CACHE_EXPORTED:
+    lib.pe_w4_bytes.argtypes = [_i32, _i32, _i32]
+    lib.pe_w4_pack.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp]
+    lib.pe_w4_quantize.argtypes = [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]
+    lib.pe_w4_linear.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i64,
+                                 _vp]
+    lib.pe_sample.argtypes = [_i32, _i32, _i32, _vp, _i64] + [_vp] * 9
+    lib.pe_verify.argtypes = ([_i32] * 4 + [_vp, _i64] + [_vp] * 9 + [_i64] + [_vp] * 7)
+    for name in EXPORTED[:-1] + CACHE_EXPORTED + HEAD_EXPORTED:
         getattr(lib, name).restype = _i32
     lib.pe_attn_decode_workspace.restype = _i64
+    lib.pe_w4_bytes.restype = _i64
     return lib
 
 
@@ -772,3 +790,233 @@ def pe_set_kv_scores(dr: Drafter, scores: Optional[Sequence] = None) -> None:
     arr = (_vp * len(scores))(*[ptr(t) for t in scores])
     _check("pe_set_kv_scores", lib().pe_set_kv_scores(dr.handle, arr))
     dr._kv_scores = scores         # the library keeps the pointers
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights, sampling and the verification of drafts (include/peagle_w4.h,
+# include/peagle_sample.h)
+# ---------------------------------------------------------------------------
+
+def _op_vector(name: str, t, n: int, dtype, index: int) -> int:
+    """Address of a contiguous vector of n elements on device `index`."""
+    if (t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous()
+            or t.get_device() != index):
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on the same device")
+    return t.data_ptr()
+
+
+def _op_rows(name: str, t, rows: int, width: int, index: int) -> int:
+    """Row stride (elements) of a [rows, width] matrix of contiguous rows."""
+    if t.shape != (rows, width) or t.get_device() != index:
+        raise ValueError(f"{name} must be [{rows}, {width}] on the same device")
+    row, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return row if rows > 1 else width
+
+
+def _op_kind(name: str, t) -> int:
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
+        return PE_DTYPE_BF16
+    if t.dtype is torch.float32:
+        return PE_DTYPE_F32
+    raise ValueError(f"{name} must be bfloat16 or float32")
+
+
+def _op_empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`, from that stream's share of the
+    allocator."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _op_call(index: int, stream, name, fn, *args) -> None:
+    """Call into the library with device `index` current; `stream` None is
+    that device's current stream."""
+    if index < 0:
+        raise ValueError(f"{name} needs tensors on a GPU")
+    torch = _torch()
+    C = torch._C
+    s = C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if C._cuda_getDevice() == index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status != PE_OK:
+        raise PeError(name, status)
+
+
+class W4Weight:
+    """A matrix [n, k] of 4-bit codes with a bfloat16 scale for each `group`
+    (32, 64 or 128) inputs of a row, laid out for pe_w4_linear.  Entry (i, j)
+    is (code - 8) * scale[i, j // group].
+
+    codes uint8 [n, (k + 1) // 2], input 2 j in the low half of byte j; scales
+    bfloat16 [n, ceil(k / group)].  The layout is made once, here, on `stream`
+    (None: the current one); codes and scales are not kept."""
+
+    def __init__(self, codes, scales, k: int, group: int, stream=None):
+        torch = _torch()
+        n, index = codes.shape[0], codes.get_device()
+        self._prepare(n, k, group, codes.device, stream)
+        if (codes.dtype is not torch.uint8 or codes.shape != (n, (k + 1) // 2)
+                or not codes.is_contiguous()):
+            raise ValueError(f"codes must be contiguous uint8 [{n}, {(k + 1) // 2}]")
+        if (scales.dtype is not torch.bfloat16 or scales.shape != (n, -(-k // group))
+                or not scales.is_contiguous() or scales.get_device() != index):
+            raise ValueError(f"scales must be contiguous bfloat16 [{n}, {-(-k // group)}] "
+                             "on the codes' device")
+        _op_call(index, stream, "pe_w4_pack", lib().pe_w4_pack, ptr(codes), ptr(scales), n, k,
+                 group, ptr(self.packed))
+
+    def _prepare(self, n, k, group, device, stream):
+        torch = _torch()
+        _cache_ints(n=n, k=k, group=group)
+        nbytes = lib().pe_w4_bytes(n, k, group)
+        if nbytes <= 0:
+            raise ValueError("a 4-bit matrix has n, k >= 1 (k up to 2**18, n up to 2**24) and a "
+                             "group of 32, 64 or 128")
+        self.n, self.k, self.group, self.device = n, k, group, device
+        self.packed = _op_empty(nbytes, torch.uint8, device, stream)
+        self.index = self.packed.get_device()
+
+    @classmethod
+    def quantize(cls, weight, group: int = 32, stream=None) -> "W4Weight":
+        """Round a bfloat16 or float32 matrix [n, k] to 4 bits: a group's
+        scale is its largest absolute value over 7."""
+        self = cls.__new__(cls)
+        if weight.dim() != 2:
+            raise ValueError("weight must be [n, k]")
+        n, k = weight.shape
+        kind = _op_kind("weight", weight)
+        self._prepare(n, k, group, weight.device, stream)
+        stride = _op_rows("weight", weight, n, k, self.index)
+        _op_call(self.index, stream, "pe_w4_quantize", lib().pe_w4_quantize, ptr(weight), kind,
+                 stride, n, k, group, ptr(self.packed))
+        return self
+
+
+def pe_w4_linear(w: W4Weight, x, out=None, out_dtype=None, stream=None):
+    """x [rows, k] (bfloat16 or float32) times the 4-bit matrix w, [rows, n]
+    in out_dtype (None: x's type; float32 beside bfloat16 x for logits), in
+    `out` where given."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, k]")
+    rows = x.shape[0]
+    kind = _op_kind("x", x)
+    xs = _op_rows("x", x, rows, w.k, w.index)
+    if out is None:
+        out = _op_empty((rows, w.n), out_dtype or x.dtype, x.device, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out is of another type than out_dtype")
+    ok = _op_kind("out", out)
+    ys = _op_rows("out", out, rows, w.n, w.index)
+    _op_call(w.index, stream, "pe_w4_linear", lib().pe_w4_linear, w.packed.data_ptr(), w.n, w.k,
+             w.group, rows, kind, x.data_ptr(), xs, ok, out.data_ptr(), ys)
+    return out
+
+
+def _op_filters(n: int, index: int, temperature, top_k, top_p, min_p):
+    """Addresses of the filters, None where not set."""
+    torch = _torch()
+    f32 = torch.float32
+    return [None if t is None else _op_vector(name, t, n, dtype, index)
+            for name, t, dtype in (("temperature", temperature, f32),
+                                   ("top_k", top_k, torch.int32), ("top_p", top_p, f32),
+                                   ("min_p", min_p, f32))]
+
+
+def _op_dist(name: str, t, n: int, index: int) -> int:
+    if (t.dtype is not _torch().int32 or t.shape != (n, 8) or not t.is_contiguous()
+            or t.get_device() != index):
+        raise ValueError(f"{name} must be contiguous int32 [{n}, 8] on the same device")
+    return t.data_ptr()
+
+
+def pe_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+              logprobs=None, dist=None, stream=None):
+    """A token for each row of logits [rows, vocab] (float32 or bfloat16),
+    drawn with u [rows] float32 of [0, 1).  Filters, each None or a vector
+    [rows]: temperature (float32; not above 0: greedy), top_k (int32), top_p,
+    min_p (float32).  Returns tokens [rows] int32 (-1: a row without any),
+    logprobs [rows] float32 and dist [rows, 8] int32, the rows' pe_dist records
+    that pe_verify takes of sampled drafts (made when None)."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    index, device = logits.get_device(), logits.device
+    kind = _op_kind("logits", logits)
+    stride = _op_rows("logits", logits, rows, vocab, index)
+    pu = _op_vector("u", u, rows, torch.float32, index)
+    filters = _op_filters(rows, index, temperature, top_k, top_p, min_p)
+    if tokens is None:
+        tokens = _op_empty(rows, torch.int32, device, stream)
+    if logprobs is None:
+        logprobs = _op_empty(rows, torch.float32, device, stream)
+    if dist is None:
+        dist = _op_empty((rows, 8), torch.int32, device, stream)
+    _op_call(index, stream, "pe_sample", lib().pe_sample, rows, vocab, kind, logits.data_ptr(),
+             stride, *filters, pu, _op_vector("tokens", tokens, rows, torch.int32, index),
+             _op_vector("logprobs", logprobs, rows, torch.float32, index),
+             _op_dist("dist", dist, rows, index))
+    return tokens, logprobs, dist
+
+
+def pe_verify(logits, ids, cu_in, accept_u, u, temperature=None, top_k=None, top_p=None,
+              min_p=None, draft_logits=None, draft_dist=None, num_accepted=None,
+              sampled_ids=None, logprobs=None, dist=None, err=None, stream=None):
+    """Verify drafts by rejection sampling: logits [T, vocab] of the target at
+    the rows of the B requests' windows, ids [T] the windows' tokens (a
+    window's first token, then its drafts), cu_in [B + 1] where they start, as
+    in pe_expand_batch.  accept_u [T] and u [B] float32 of [0, 1); filters as
+    in pe_sample, [B].  draft_logits None: the drafts are the drafter's
+    largest logits; else [T - B, vocab], the drafter's logits of all drafts in
+    order, and draft_dist what pe_sample returned for them.  Returns
+    num_accepted [B], sampled_ids [B] (the next pe_expand_batch takes both),
+    logprobs [T] and dist [T, 8] (made when None)."""
+    torch = _torch()
+    if logits.dim() != 2 or cu_in.dim() != 1:
+        raise ValueError("logits must be [T, vocab] and cu_in [B + 1]")
+    T, vocab = logits.shape
+    B = cu_in.shape[0] - 1
+    index, device = logits.get_device(), logits.device
+    i32, f32 = torch.int32, torch.float32
+    kind = _op_kind("logits", logits)
+    stride = _op_rows("logits", logits, T, vocab, index)
+    pids = _op_vector("ids", ids, T, i32, index)
+    pcu = _op_vector("cu_in", cu_in, B + 1, i32, index)
+    pau = _op_vector("accept_u", accept_u, T, f32, index)
+    pu = _op_vector("u", u, B, f32, index)
+    filters = _op_filters(B, index, temperature, top_k, top_p, min_p)
+    dl = dd = None
+    ds = 0
+    if (draft_logits is None) != (draft_dist is None):
+        raise ValueError("draft_logits and draft_dist go together")
+    if draft_logits is not None:
+        if draft_logits.dtype is not logits.dtype:
+            raise ValueError("draft_logits must be of the type of logits")
+        ds = _op_rows("draft_logits", draft_logits, T - B, vocab, index)
+        dd = _op_dist("draft_dist", draft_dist, T - B, index)
+        # without any draft there is no row to point to: any address says "sampled"
+        dl = draft_logits.data_ptr() or logits.data_ptr()
+    if num_accepted is None:
+        num_accepted = _op_empty(B, i32, device, stream)
+    if sampled_ids is None:
+        sampled_ids = _op_empty(B, i32, device, stream)
+    if logprobs is None:
+        logprobs = _op_empty(T, f32, device, stream)
+    if dist is None:
+        dist = _op_empty((T, 8), i32, device, stream)
+    _op_call(index, stream, "pe_verify", lib().pe_verify, B, T, vocab, kind, logits.data_ptr(),
+             stride, pids, pcu, *filters, pau, pu, dl, ds, dd,
+             _op_vector("num_accepted", num_accepted, B, i32, index),
+             _op_vector("sampled_ids", sampled_ids, B, i32, index),
+             _op_vector("logprobs", logprobs, T, f32, index), _op_dist("dist", dist, T, index),
+             None if err is None else _op_vector("err", err, 1, i32, index))
+    return num_accepted, sampled_ids, logprobs, dist
