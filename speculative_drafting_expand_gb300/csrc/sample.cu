@@ -100,6 +100,12 @@ __device__ __forceinline__ float logprob_of(float x, RowScale s, long long total
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+// The same place in the shared memory of cluster CTA `rank`.
+__device__ __forceinline__ const uint32_t* cluster_pointer(const uint32_t* p, int rank) {
+  uint64_t to;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(to) : "l"(p), "r"(rank));
+  return reinterpret_cast<const uint32_t*>(to);
+}
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
@@ -112,6 +118,13 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     v = o > v ? o : v;
   }
   return v;
+}
+
+// The cluster's barrier.  Each thread arrives for itself: after a loop whose
+// length differs between lanes nothing promises that a warp arrives as one.
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive_release();
+  cluster_wait_acquire();
 }
 
 struct Exchange {
@@ -144,7 +157,7 @@ __device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cl
       st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][1][rank]), lane), y);
     }
   }
-  cluster_sync_all();
+  cluster_barrier();
   a = b = 0;
   for (int r = 0; r < cluster; ++r) {
     const unsigned long long x = ex.slot[parity][0][r];
@@ -159,8 +172,11 @@ __device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cl
 template <typename T>
 struct Part {
   static constexpr int E = 16 / static_cast<int>(sizeof(T));
-  int first;   // id of the first chunk's first element (may be negative)
+  int mis;     // elements of the first chunk of all that lie before the row
+  int per;     // chunks of a CTA (the last ones may have fewer)
+  int first;   // id of this CTA's first element (may be negative)
   int chunks;  // of this CTA
+  __device__ __forceinline__ int owner(int id) const { return (id + mis) / E / per; }
 };
 template <typename T>
 __device__ __forceinline__ Part<T> part_of(const T* row, int V, int cluster, int rank) {
@@ -168,71 +184,133 @@ __device__ __forceinline__ Part<T> part_of(const T* row, int V, int cluster, int
   const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % E);
   const int all = (mis + V + E - 1) / E, per = (all + cluster - 1) / cluster;
   const int lo = min(rank * per, all);
-  return Part<T>{lo * E - mis, min(lo + per, all) - lo};
+  return Part<T>{mis, per, lo * E - mis, min(lo + per, all) - lo};
 }
 template <typename T>
 __device__ __forceinline__ uint4 load_chunk(const T* row, int V, int id) {
   constexpr int E = Part<T>::E;
-  if (id >= 0 && id + E <= V) return __ldg(reinterpret_cast<const uint4*>(row + id));
+  if (id >= 0 && id + E <= V) return __ldcs(reinterpret_cast<const uint4*>(row + id));
   uint4 v;
   T* t = reinterpret_cast<T*>(&v);
 #pragma unroll
   for (int e = 0; e < E; ++e) t[e] = id + e >= 0 && id + e < V ? row[id + e] : from_f<T>(-INFINITY);
   return v;
 }
+// The logits of a chunk in shared memory.  fp32 ones were cleaned on their
+// way in; 16-bit ones have no room for the largest fp32 number.
+template <typename T>
+__device__ __forceinline__ void chunk_logits(const uint4* p, float (&x)[Part<T>::E]) {
+  const uint4 v = *p;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      x[2 * i] = clean_logit(__uint_as_float(w[i] << 16));
+      x[2 * i + 1] = clean_logit(__uint_as_float(w[i] & 0xffff0000u));
+    }
+  }
+}
 
-// The token at which the kept weights, in the order of the ids, first exceed
-// `at`; weight(chunk, e) of this CTA's elements.  Every warp has a contiguous
-// segment of chunks.  Returns the id on one thread of the cluster, -1 on all
-// others.
+// Contiguous chunks of a warp, and of a lane within them, so that sums over
+// warps and lanes are in the order of the ids.
 struct Segment {
   int lo, hi;
 };
+__device__ __forceinline__ int warp_segment_size(int chunks) {
+  return (chunks + kSampleWarps - 1) / kSampleWarps;
+}
 __device__ __forceinline__ Segment warp_segment(int chunks) {
-  const int per = ((chunks + 31) / 32 + kSampleWarps - 1) / kSampleWarps * 32;
+  const int per = warp_segment_size(chunks);
   const int lo = min(static_cast<int>(threadIdx.x) / 32 * per, chunks);
   return Segment{lo, min(lo + per, chunks)};
 }
-template <int E, typename W>
-__device__ __forceinline__ int find_in_segment(Segment seg, long long at, int first, W&& weight) {
+__device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v) {
   const int lane = threadIdx.x % 32;
-  for (int c0 = seg.lo; c0 < seg.hi; c0 += 32) {
-    const int c = c0 + lane;
-    unsigned long long own = 0;
-    if (c < seg.hi)
 #pragma unroll
-      for (int e = 0; e < E; ++e) own += weight(c, e);
-    unsigned long long run = own;
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+// The element of a warp's segment at which the weights, in order, first
+// exceed `at`: the lane's part that holds it, then the element.  Returns chunk
+// * E + element on one lane, -1 on the others.
+template <int E, typename W>
+__device__ __forceinline__ int find_in_segment(Segment seg, long long at, W&& weight) {
+  const int lane = threadIdx.x % 32;
+  const int per = (seg.hi - seg.lo + 31) / 32;
+  const int lo = min(seg.lo + lane * per, seg.hi), hi = min(lo + per, seg.hi);
+  unsigned long long own = 0;
+  for (int c = lo; c < hi; ++c)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long o = __shfl_up_sync(0xffffffffu, run, d);
-      if (lane >= d) run += o;
-    }
-    const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, run, 31));
+    for (int e = 0; e < E; ++e) own += weight(c, e);
+  const unsigned long long run = warp_scan_u64(own);
+  const unsigned hit = __ballot_sync(0xffffffffu, static_cast<long long>(run) > at);
+  if (hit == 0) return -1;  // not reached: the sums agree
+  const int who = __ffs(hit) - 1;
+  at -= static_cast<long long>(__shfl_sync(0xffffffffu, run - own, who));
+  const int from = __shfl_sync(0xffffffffu, lo, who) * E, to = __shfl_sync(0xffffffffu, hi, who) * E;
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned long long w = i < to ? weight(i / E, i % E) : 0u;
+    const unsigned long long sum = warp_scan_u64(w);
+    const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31));
     if (at >= all) {
       at -= all;
       continue;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, static_cast<long long>(run) > at);
-    if (lane != __ffs(hit) - 1) return -1;
-    at -= static_cast<long long>(run - own);
-    for (int e = 0; e < E; ++e) {
-      const long long w = weight(c, e);
-      if (at < w) return first + c * E + e;
-      at -= w;
-    }
-    return -1;  // not reached: the sums agree
+    const unsigned h = __ballot_sync(0xffffffffu, static_cast<long long>(sum) > at);
+    return lane == __ffs(h) - 1 ? i : -1;
   }
   return -1;
 }
 
 // ------------------------------------------------------------- sampling rows
+// Bins of falling logits, 48 an octave of e = 2^(-bin / 48): rounding is
+// monotonic, so a larger logit never has a larger bin.  Bins below kSure hold
+// W > 0 alone, bins from kBins on (and NaN, which -inf gives) W = 0 alone.
+constexpr int kPerOctave = 48;
+constexpr int kSure = 32 * kPerOctave - 1;
+constexpr int kBins = 32 * kPerOctave + 4;
+__device__ __forceinline__ int bin_of(float z) {
+  // 8388608 + n has the bits 0x4B000000 + n
+  const float f = fmaf(z, -69.24936196f, 8388608.f);  // 48 / ln 2
+  return __float_as_int(fminf(f, 8388608.f + kBins)) - 0x4B000000;
+}
+
+// Tokens that are ranked one by one, from all CTAs of the cluster.
+constexpr int kListed = 640;
+struct Listed {
+  unsigned long long key[kListed];
+  uint32_t w[kListed];
+  uint16_t own[kListed];  // this CTA's: element of its part
+  uint32_t digits[3][256];
+};
+union Scratch {
+  uint32_t bins[2][kBins];  // counts, or sums of the weights' low and high halves
+  Listed list;
+};
+struct Found {
+  unsigned long long before, inside;
+  int bin;
+};
+struct SampleShared {
+  Exchange ex;
+  Found found;
+  unsigned long long warp_mass[kSampleWarps];
+  unsigned long long scan[kSampleWarps];
+  unsigned long long digit_before, digit_inside;
+  int digit, listed;
+};
+
 template <typename T, bool VERIFY>
-__global__ void __launch_bounds__(kSampleThreads) sample_rows_kernel(
+__global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) unsigned char held[];
-  __shared__ Exchange ex;
-  __shared__ unsigned long long warp_mass[kSampleWarps];
+  __shared__ SampleShared sh;
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int cluster = a.cluster, rank = cluster_ctarank(), r = blockIdx.x / cluster;
@@ -260,79 +338,376 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rows_kernel(
   float inv = __fdiv_rn(1.f, temp);
   const bool greedy = !(temp > 0.f) || isinf(inv);
   if (greedy) inv = 0.f;
-  int k = a.top_k ? a.top_k[q] : 0;
-  if (k <= 0) k = a.V;
   const float p = a.top_p ? a.top_p[q] : 1.f;
-  if (greedy || p <= 0.f) k = 1;  // top-p of nothing: the first token alone
+  int k = a.top_k ? a.top_k[q] : 0;
+  if (p <= 0.f) k = 1;  // top-p of nothing: the first token alone
+  const bool by_count = k > 0 && k < a.V;
   const bool by_mass = p < 1.f && p > 0.f;
-  const float mp = a.min_p ? fminf(a.min_p[q], 1.f) : 0.f;  // NaN: 1, see below
-  const float min_p = a.min_p && isnan(a.min_p[q]) ? 0.f : mp;
+  float min_p = a.min_p ? a.min_p[q] : 0.f;
+  min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;  // NaN: 0
+  const bool by_share = min_p > 2.328306436538696e-10f;  // 2^-32: W > 0 implies e >= 2^-32
 
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   const Part<T> part = part_of(row, a.V, cluster, rank);
   uint4* mine = reinterpret_cast<uint4*>(held);
+  Scratch& scr = *reinterpret_cast<Scratch*>(held + static_cast<size_t>(part.per) * 16);
   float top = -INFINITY;
-  for (int c = tid; c < part.chunks; c += kSampleThreads) {
-    const uint4 v = load_chunk(row, a.V, part.first + c * E);
-    mine[c] = v;
-    const T* t = reinterpret_cast<const T*>(&v);
+  constexpr int kFly = 4;  // chunks of a thread on their way
+  for (int c0 = tid; c0 < part.chunks; c0 += kFly * kSampleThreads) {
+    uint4 v[kFly];
 #pragma unroll
-    for (int e = 0; e < E; ++e) top = fmaxf(top, clean_logit(to_f<T>(t[e])));
+    for (int i = 0; i < kFly; ++i)
+      if (c0 + i * kSampleThreads < part.chunks)
+        v[i] = load_chunk(row, a.V, part.first + (c0 + i * kSampleThreads) * E);
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int c = c0 + i * kSampleThreads;
+      if (c >= part.chunks) break;
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = make_float4(
+            clean_logit(__uint_as_float(v[i].x)), clean_logit(__uint_as_float(v[i].y)),
+            clean_logit(__uint_as_float(v[i].z)), clean_logit(__uint_as_float(v[i].w)));
+        reinterpret_cast<float4*>(mine)[c] = f;
+        top = fmaxf(fmaxf(top, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
+      } else {
+        mine[c] = v[i];
+        const T* t = reinterpret_cast<const T*>(&v[i]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = fmaxf(top, clean_logit(to_f<T>(t[e])));
+      }
+    }
   }
   unsigned long long x = float_order_key(top), y = 0;
-  cluster_reduce<true>(ex, parity, cluster, rank, x, y);
+  cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
   const RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
-  const T* elems = reinterpret_cast<const T*>(held);
 
-  // counts and sums of the tokens that a test takes
-  auto sums = [&](auto&& test, unsigned long long& count, unsigned long long& mass) {
-    count = mass = 0;
-    for (int c = tid; c < part.chunks; c += kSampleThreads)
+  // Every element of this CTA, in no order: test(logit, id).
+  auto each = [&](auto&& test) {
+    for (int c = tid; c < part.chunks; c += kSampleThreads) {
+      float v[E];
+      chunk_logits<T>(mine + c, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float v = raw_logit(elems + c * E + e);
-        const float ev = exp_of(v, sc);
-        const uint32_t w = weight_of(ev);
-        if (w && test(v, ev, part.first + c * E + e)) {
-          ++count;
-          mass += w;
-        }
-      }
-    cluster_reduce<false>(ex, parity, cluster, rank, count, mass);
-  };
-  unsigned long long positive, able, mass, count;
-  sums([&](float, float, int) { return true; }, positive, mass);
-  sums([&](float, float ev, int) { return ev >= min_p; }, able, mass);
-  // Tokens in their order are falling 64-bit keys.  The last one of which
-  // fewer than `limit` (tokens, or weight) come before:
-  unsigned long long border = 0;
-  const unsigned long long most = argmax_key(sc.max, 0);
-  auto bisect = [&](bool by_count, double limit) {
-    const unsigned long long floor_key = border;
-    unsigned long long lo = 0, hi = most;
-    while (lo < hi) {
-      const unsigned long long mid = lo + (hi - lo) / 2;
-      sums([&](float v, float ev, int id) {
-        const unsigned long long key = argmax_key(v, id);
-        return ev >= min_p && key >= floor_key && key > mid;
-      }, count, mass);
-      if (static_cast<double>(by_count ? count : mass) < limit) hi = mid;
-      else lo = mid + 1;
+      for (int e = 0; e < E; ++e) test(v[e], c * E + e);
     }
-    border = hi;
   };
-  const unsigned long long first_n = min(static_cast<unsigned long long>(k), able);
-  if (positive) {
-    const unsigned long long able_mass = mass;
-    if (first_n < positive) bisect(true, static_cast<double>(first_n));
-    if (by_mass) {
-      mass = able_mass;
-      if (border)
-        sums([&](float v, float ev, int id) { return ev >= min_p && argmax_key(v, id) >= border; },
-             count, mass);
-      bisect(false, static_cast<double>(p) * static_cast<double>(mass));
-      sums([&](float v, float ev, int id) { return argmax_key(v, id) >= border; }, count, mass);
-      if (count == positive) border = 0;
+
+  // The last kept token's key; 0: every token of W > 0 is kept.
+  unsigned long long border = 0;
+  const Segment seg = warp_segment(part.chunks);
+  unsigned long long own = 0;      // kept weight of this warp's segment
+  bool summed = false;             // ... and is it there yet
+  if (sc.max > -INFINITY && greedy) {
+    // the lowest id of the largest logit, and whether any other logit is finite
+    unsigned long long best = 0, others = 0;
+    each([&](float v, int i) {
+      if (v == sc.max) {
+        const unsigned long long key = argmax_key(v, part.first + i);
+        best = key > best ? key : best;
+      }
+      others += __fsub_rn(v, sc.max) > -INFINITY;
+    });
+    cluster_reduce<true>(sh.ex, parity, cluster, rank, best, others);
+    border = others > 1 ? best : 0;
+  } else if (sc.max > -INFINITY && (by_count || by_mass || by_share)) {
+    // Which tokens pass the filters other than the one that is being applied:
+    // bins below `sure` do, bins above `last` do not, the rest are looked at.
+    int sure = kSure, last = kBins - 1;
+    if (by_share) {
+      const int at = bin_of(logf(min_p));
+      sure = min(sure, at - 2);
+      last = min(last, at + 2);
+    }
+    unsigned long long floor_key = 0;
+    auto able = [&](float v, float z, int bin, int i) {
+      if (bin < sure) return true;
+      if (bin > last) return false;
+      const float e = expf(z);
+      return weight_of(e) > 0 && e >= min_p && argmax_key(v, part.first + i) >= floor_key;
+    };
+    // The bin, and within it the range of keys, that a limit falls into, and
+    // the measure of what comes before.
+    auto histogram = [&](bool count, auto&& place) {
+      for (int i = tid; i < kBins; i += kSampleThreads) scr.bins[0][i] = scr.bins[1][i] = 0;
+      __syncthreads();
+      each([&](float v, int i) {
+        const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
+        const int bin = bin_of(z);
+        const int at = place(v, bin, i);
+        if (at < 0 || !able(v, z, bin, i)) return;
+        if (count) {
+          atomicAdd(&scr.bins[0][at], 1u);
+        } else {
+          const uint32_t w = weight_of(expf(z));
+          atomicAdd(&scr.bins[0][at], w & 0xffffu);  // at most 2^16 elements a CTA
+          atomicAdd(&scr.bins[1][at], w >> 16);
+        }
+      });
+      cluster_barrier();
+    };
+    // Every CTA adds up its share of the bins over the cluster; whoever finds
+    // the limit tells the others.  `limit` gets the measure of all bins.
+    auto search = [&](bool count, unsigned long long base, auto&& limit) {
+      constexpr int kMost = (kBins + kSampleThreads - 1) / kSampleThreads;
+      const int share = (kBins + cluster - 1) / cluster, lo = rank * share;
+      const int each_bins = (share + kSampleThreads - 1) / kSampleThreads;
+      unsigned long long v[kMost], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        v[j] = 0;
+        const int at = tid * each_bins + j;
+        if (j < each_bins && at < share && lo + at < kBins) {
+          for (int c = 0; c < cluster; ++c) {
+            const uint32_t* from = cluster_pointer(&scr.bins[0][lo + at], c);
+            v[j] += from[0] + (static_cast<unsigned long long>(from[kBins]) << 16);
+          }
+        }
+        sum += v[j];
+      }
+      const unsigned long long run = warp_scan_u64(sum);
+      if (lane == 31) sh.scan[warp] = run;
+      unsigned long long all = sum, none = 0;
+      const int par = parity;
+      cluster_reduce<false>(sh.ex, parity, cluster, rank, all, none);
+      unsigned long long before = base + run - sum;
+      for (int i = 0; i < rank; ++i) before += sh.ex.slot[par][0][i];
+      for (int i = 0; i < warp; ++i) before += sh.scan[i];
+      const double stop = limit(all);
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        if (v[j] && static_cast<double>(before) < stop &&
+            !(static_cast<double>(before + v[j]) < stop))
+          for (int c = 0; c < cluster; ++c) {
+            const uint32_t to = cluster_map_shared(smem_u32(&sh.found), c);
+            st_cluster_u64(to, before);
+            st_cluster_u64(to + 8, v[j]);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 16),
+                         "r"(lo + tid * each_bins + j)
+                         : "memory");
+          }
+        before += v[j];
+      }
+      cluster_barrier();
+      return sh.found;
+    };
+    // The last token of `listed` ones before which the measure is below the
+    // limit: eight bits of the keys at a time.  Every CTA has the whole list.
+    auto select = [&](int listed, bool count, unsigned long long base, double stop,
+                      unsigned long long floor) {
+      constexpr int kEach = (kListed + kSampleThreads - 1) / kSampleThreads;
+      unsigned long long key[kEach];
+      uint32_t w[kEach];
+      bool on[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = tid + j * kSampleThreads;
+        on[j] = i < listed;
+        key[j] = on[j] ? scr.list.key[i] : 0;
+        w[j] = on[j] ? scr.list.w[i] : 0;
+        on[j] = on[j] && key[j] >= floor;
+      }
+      unsigned long long result = 0;
+      for (int shift = 56; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kSampleThreads)
+          scr.list.digits[0][i] = scr.list.digits[1][i] = scr.list.digits[2][i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (on[j]) {
+            const int d = static_cast<int>(key[j] >> shift) & 255;
+            atomicAdd(&scr.list.digits[0][d], 1u);
+            atomicAdd(&scr.list.digits[1][d], w[j] & 0xffffu);
+            atomicAdd(&scr.list.digits[2][d], w[j] >> 16);
+          }
+        __syncthreads();
+        if (warp == 0) {
+          // lane 0 has the largest digits
+          unsigned long long v[8], sum = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = 255 - lane * 8 - i;
+            v[i] = count ? scr.list.digits[0][d]
+                         : scr.list.digits[1][d] + (static_cast<unsigned long long>(scr.list.digits[2][d]) << 16);
+            sum += v[i];
+          }
+          unsigned long long before = base + warp_scan_u64(sum) - sum;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (v[i] && static_cast<double>(before) < stop &&
+                !(static_cast<double>(before + v[i]) < stop)) {
+              sh.digit = 255 - lane * 8 - i;
+              sh.digit_before = before;
+              sh.digit_inside = scr.list.digits[0][255 - lane * 8 - i];
+            }
+            before += v[i];
+          }
+        }
+        __syncthreads();
+        const unsigned long long d = static_cast<unsigned long long>(sh.digit);
+        base = sh.digit_before;
+        result |= d << shift;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) on[j] = on[j] && ((key[j] >> shift) & 255) == d;
+        if (sh.digit_inside == 1) {
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            if (on[j]) sh.found.before = key[j];
+          __syncthreads();
+          result = sh.found.before;
+          break;
+        }
+        __syncthreads();
+      }
+      return result;
+    };
+
+    // by number (top-k, min-p), by weight (top-p), or one after the other
+    for (int stage = by_count || !by_mass ? 0 : 1; stage < (by_mass ? 2 : 1); ++stage) {
+      const bool count = stage == 0;
+      const double want = by_count ? static_cast<double>(k) : 9e15;
+      double stop = 0.0;
+      auto limit = [&](unsigned long long all) {
+        const double n = static_cast<double>(all);
+        return stop = count ? fmin(want, n) : __dmul_rn(static_cast<double>(p), n);
+      };
+      histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
+      Found f = search(count, 0, limit);
+      unsigned long long low = 0, high = ~0ull;  // keys within the bin
+      int lo_bin = f.bin;
+      if (count && f.before + f.inside <= kListed) {
+        lo_bin = 0;  // few tokens in all: rank every one
+        f.before = 0;
+      }
+      const int hi_bin = f.bin;
+      int listed;
+      unsigned long long dropped;
+      while (true) {
+        // weights before the range, by segments; the range's own tokens
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        own = 0;
+        bool drop = false;
+        unsigned long long least = ~0ull, most = 0;
+        for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+          float v[E];
+          chunk_logits<T>(mine + c, v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float z = __fmul_rn(__fsub_rn(v[e], sc.max), sc.inv);
+            const int bin = bin_of(z);
+            if (bin >= kBins) continue;
+            if (bin > hi_bin) {
+              drop = drop || bin < kSure || weight_of(expf(z)) > 0;
+              continue;
+            }
+            if (!able(v[e], z, bin, c * E + e)) {
+              drop = drop || bin < kSure || weight_of(expf(z)) > 0;
+              continue;
+            }
+            if (bin < lo_bin) {
+              own += weight_of(expf(z));
+              continue;
+            }
+            const unsigned long long key = argmax_key(v[e], part.first + c * E + e);
+            if (key > high) {
+              own += weight_of(expf(z));
+            } else if (key < low) {
+              drop = true;
+            } else {
+              least = key < least ? key : least;
+              most = key > most ? key : most;
+              const int at = atomicAdd(&sh.listed, 1);
+              if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(c * E + e);
+            }
+          }
+        }
+        __syncthreads();
+        unsigned long long n = static_cast<unsigned long long>(tid == 0 ? sh.listed : 0);
+        dropped = drop;
+        const int par = parity;
+        cluster_reduce<false>(sh.ex, parity, cluster, rank, n, dropped);
+        listed = static_cast<int>(n);
+        if (listed <= kListed) {
+          int at = 0;
+          for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i]);
+          const int here = static_cast<int>(sh.ex.slot[par][0][rank]);
+          for (int i = tid; i < here * cluster; i += kSampleThreads) {
+            const int to = i / here, j = i % here, el = scr.list.own[j];
+            const float v = to_f<T>(reinterpret_cast<const T*>(held)[el]);
+            const float xv = sizeof(T) == 4 ? v : clean_logit(v);
+            st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), to),
+                           argmax_key(xv, part.first + el));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                             cluster_map_shared(smem_u32(&scr.list.w[at + j]), to)),
+                         "r"(weight_of(exp_of(xv, sc)))
+                         : "memory");
+          }
+          cluster_barrier();
+          break;
+        }
+        // too many to rank: bins of the range's keys (ties go by their ids)
+        unsigned long long inverse = ~least;
+        cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, dropped);
+        low = ~inverse;
+        unsigned long long none = 0;
+        cluster_reduce<true>(sh.ex, parity, cluster, rank, most, none);
+        high = most;
+        int shift = 0;
+        while (((high - low) >> shift) >= kBins) ++shift;
+        lo_bin = hi_bin;  // (the range is that bin's: lists of all bins are short)
+        const unsigned long long lowest = low, highest = high;
+        histogram(count, [&](float v, int bin, int i) {
+          if (bin != hi_bin) return -1;
+          const unsigned long long key = argmax_key(v, part.first + i);
+          return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
+        });
+        f = search(count, f.before, [&](unsigned long long) { return stop; });
+        high = highest - (static_cast<unsigned long long>(f.bin) << shift);
+        const unsigned long long end = high - ((1ull << shift) - 1);
+        low = end > lowest && end <= high ? end : lowest;
+      }
+      border = select(listed, count, f.before, stop, 0);
+      if (count && by_mass && lo_bin == 0 && listed <= kListed && hi_bin == f.bin && high == ~0ull) {
+        // all that is left is in the list: the weights' limit in it
+        unsigned long long mass = 0, none = 0;
+        for (int i = tid; i < listed; i += kSampleThreads)
+          if (scr.list.key[i] >= border) mass += scr.list.w[i];
+        mass = warp_sum_u64(mass);
+        if (lane == 0) sh.scan[warp] = mass;
+        __syncthreads();
+        for (int i = 0; i < kSampleWarps; ++i) none += sh.scan[i];
+        __syncthreads();
+        border = select(listed, false, 0, __dmul_rn(static_cast<double>(p), static_cast<double>(none)),
+                        border);
+        stage = 2;
+      } else if (count && by_mass) {
+        // the second stage's tokens: at or above this border
+        floor_key = border;
+        const float v = key_float(static_cast<uint32_t>(border >> 32));
+        const int at = bin_of(__fmul_rn(__fsub_rn(v, sc.max), sc.inv));
+        sure = min(sure, at);
+        last = min(last, at);
+        cluster_barrier();  // the list is read: its memory may be bins again
+        continue;
+      }
+      // the list's kept tokens join their segments
+      __syncthreads();
+      own = warp_sum_u64(own);
+      if (lane == 0) sh.warp_mass[warp] = own;
+      __syncthreads();
+      const int per = warp_segment_size(part.chunks);
+      bool left = false;
+      for (int i = tid; i < listed; i += kSampleThreads) {
+        const unsigned long long key = scr.list.key[i], w = scr.list.w[i];
+        if (key < border) {
+          left = true;
+          continue;
+        }
+        const int id = argmax_key_index(key);
+        if (part.owner(id) == rank) atomicAdd(&sh.warp_mass[(id - part.first) / E / per], w);
+      }
+      if (!__syncthreads_or(left) && !dropped) border = 0;
+      own = sh.warp_mass[warp];
+      summed = true;
     }
   }
   const float cut = border ? key_float(static_cast<uint32_t>(border >> 32)) : -INFINITY;
@@ -341,34 +716,48 @@ __global__ void __launch_bounds__(kSampleThreads) sample_rows_kernel(
   // Draw.  A greedy draft that this row may reject has no share.
   const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
   auto weight = [&](int c, int e) -> uint32_t {
-    const float v = raw_logit(elems + c * E + e);
+    const T t = reinterpret_cast<const T*>(held)[c * E + e];
+    const float v = sizeof(T) == 4 ? to_f<T>(t) : clean_logit(to_f<T>(t));
     const int id = part.first + c * E + e;
     if (!is_kept(v, id, cut, cut_token) || id == left_out) return 0;
     return weight_of(exp_of(v, sc));
   };
-  const Segment seg = warp_segment(part.chunks);
-  unsigned long long own = 0;
-  for (int c = seg.lo + lane; c < seg.hi; c += 32)
+  if (!summed) {
+    own = 0;
+    for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+      float v[E];
+      chunk_logits<T>(mine + c, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) own += weight(c, e);
-  unsigned long long total = own, none = 0;
-  own = warp_sum_u64(own);
-  if (lane == 0) warp_mass[warp] = own;
+      for (int e = 0; e < E; ++e)
+        if (is_kept(v[e], part.first + c * E + e, cut, cut_token)) own += weight_of(exp_of(v[e], sc));
+    }
+    own = warp_sum_u64(own);
+    if (lane == 0) sh.warp_mass[warp] = own;
+  }
+  unsigned long long total = lane == 0 ? own : 0, none = 0;
   const int par = parity;
-  cluster_reduce<false>(ex, parity, cluster, rank, total, none);
-  long long all = static_cast<long long>(total);
+  cluster_reduce<false>(sh.ex, parity, cluster, rank, total, none);
+  const long long all = static_cast<long long>(total);
+  long long share = all, out = 0;  // what is drawn from, and what is left out of it
   if (left_out >= 0) {
     const float v = raw_logit(row + left_out);
-    if (is_kept(v, left_out, cut, cut_token)) all += weight_of(exp_of(v, sc));
+    if (is_kept(v, left_out, cut, cut_token)) out = weight_of(exp_of(v, sc));
+    share -= out;
   }
-  const bool draws = total > 0 && !(VERIFY && judges && !a.greedy_drafts);
+  const bool draws = share > 0 && !(VERIFY && judges && !a.greedy_drafts);
   int token = -1;
   if (draws) {
-    long long at = place_of(a.u[q], static_cast<long long>(total));
-    for (int i = 0; i < rank; ++i) at -= static_cast<long long>(ex.slot[par][0][i]);
-    for (int i = 0; i < warp; ++i) at -= static_cast<long long>(warp_mass[i]);
-    if (at >= 0 && at < static_cast<long long>(own))
-      token = find_in_segment<E>(seg, at, part.first, weight);
+    long long at = place_of(a.u[q], share);
+    const int of = out ? part.owner(left_out) : -1;
+    for (int i = 0; i < rank; ++i)
+      at -= static_cast<long long>(sh.ex.slot[par][0][i]) - (i == of ? out : 0);
+    const int in = of == rank ? (left_out - part.first) / E / warp_segment_size(part.chunks) : -1;
+    for (int i = 0; i < warp; ++i)
+      at -= static_cast<long long>(sh.warp_mass[i]) - (i == in ? out : 0);
+    if (at >= 0 && at < static_cast<long long>(own) - (warp == in ? out : 0)) {
+      const int i = find_in_segment<E>(seg, at, weight);
+      if (i >= 0) token = part.first + i;
+    }
   }
   if (token >= 0 || (!draws && rank == 0 && tid == 0)) {
     if (!VERIFY) {
@@ -501,11 +890,12 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
     for (int i = 0; i < rank; ++i) at -= static_cast<long long>(ex.slot[0][use][i]);
     for (int i = 0; i < warp; ++i) at -= static_cast<long long>(warp_mass[use][i]);
     if (at >= 0 && at < own) {
-      token = find_in_segment<E>(seg, at, part.first, [&](int c, int e) {
+      const int i = find_in_segment<E>(seg, at, [&](int c, int e) {
         uint32_t m, n;
         weights(c, e, m, n);
         return use ? n : m;
       });
+      if (i >= 0) token = part.first + i;
       writes = token >= 0;
     }
   }
@@ -544,15 +934,15 @@ struct SampleShape {
 // Few rows: as many CTAs a row as a cluster has, for the shortest way; more
 // rows than that fills: as few as hold the row.
 static SampleShape sample_shape(int rows, int V, int elem, int sms) {
-  constexpr size_t kHalf = 100 * 1024;
+  constexpr size_t kHalf = 113 * 1024 - sizeof(SampleShared);
   auto bytes = [&](int c) {
     const int e = 16 / elem, all = (V + 2 * (e - 1)) / e;
-    return static_cast<size_t>((all + c - 1) / c) * 16;
+    return static_cast<size_t>((all + c - 1) / c) * 16 + sizeof(Scratch);
   };
   int c = 1;
   while (c < kMostCluster && bytes(c) > kHalf) c *= 2;
   while (c < kMostCluster && static_cast<long long>(rows) * c * 2 <= 2 * sms &&
-         bytes(c) > 4096)
+         bytes(c) > sizeof(Scratch) + 4096)
     c *= 2;
   return SampleShape{c, bytes(c)};
 }
