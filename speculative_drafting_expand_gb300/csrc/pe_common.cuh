@@ -353,6 +353,20 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 __device__ __forceinline__ void cluster_wait_acquire() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+// The cluster's barrier.  Each thread arrives for itself: after a loop whose
+// length differs between lanes nothing promises that a warp arrives as one.
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+// The same place in the shared memory of cluster CTA `rank`, as a generic
+// pointer for plain loads.
+template <typename T>
+__device__ __forceinline__ const T* cluster_pointer(const T* p, int rank) {
+  uint64_t to;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(to) : "l"(p), "r"(rank));
+  return reinterpret_cast<const T*>(to);
+}
 // 16 bytes from registers into the shared memory of a cluster peer (a
 // shared::cluster address); their arrival completes 16 bytes of the
 // transaction count of the peer's mbarrier `mbar` (also shared::cluster).

@@ -100,12 +100,6 @@ __device__ __forceinline__ float logprob_of(float x, RowScale s, long long total
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-// The same place in the shared memory of cluster CTA `rank`.
-__device__ __forceinline__ const uint32_t* cluster_pointer(const uint32_t* p, int rank) {
-  uint64_t to;
-  asm("mapa.u64 %0, %1, %2;" : "=l"(to) : "l"(p), "r"(rank));
-  return reinterpret_cast<const uint32_t*>(to);
-}
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
@@ -118,13 +112,6 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     v = o > v ? o : v;
   }
   return v;
-}
-
-// The cluster's barrier.  Each thread arrives for itself: after a loop whose
-// length differs between lanes nothing promises that a warp arrives as one.
-__device__ __forceinline__ void cluster_barrier() {
-  cluster_arrive_release();
-  cluster_wait_acquire();
 }
 
 struct Exchange {

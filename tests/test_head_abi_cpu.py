@@ -95,10 +95,11 @@ def test_w4_sizes_are_refused_by_every_call(B, change, status):
 
 def test_w4_bytes_is_16_rows_by_64_inputs_and_scales(B):
     f = B.lib().pe_w4_bytes
-    assert f(1, 1, 32) == 512 + 32
+    assert f(1, 1, 32) == 512 + 64
     assert f(16, 64, 32) == 512 + 64
     assert f(17, 65, 64) == 2 * 2 * 512 + 2 * 2 * 32
     assert f(201088, 2880, 32) == 201088 * 2880 // 2 + 201088 * 90 * 2
+    assert f(16, 65, 32) == 2 * 512 + 4 * 32 and f(16, 65, 128) == 2 * 512 + 32
 
 
 @pytest.mark.parametrize("change", [dict(codes=0), dict(scales=0), dict(packed=0),
