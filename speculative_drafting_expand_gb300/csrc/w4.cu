@@ -2,8 +2,8 @@
 // each group of inputs (include/peagle_w4.h).
 //
 // Packed layout.  The matrix is cut into tiles of 16 rows and units of 64
-// inputs (groups of 128: an even number), filled up with zeros.  First the codes, [tile][unit][lane][16
-// bytes]: word j of a lane is its part of the left operand of one m16n8k16
+// inputs (groups of 128: an even number), filled up with zeros.  First the
+// codes, [tile][unit][lane][16 bytes]: word j of a lane is its part of the left operand of one m16n8k16
 // product (inputs 16 j .. 16 j + 15 of the unit), so a warp reads a unit as
 // one 512-byte line and needs no exchange.  Register i of the operand takes
 // nibbles i (low half) and i + 4 (high half) of the word: one shift and one
@@ -173,8 +173,8 @@ struct W4Args {
   W4Shape sh;
   int rows;  // of this launch, at most 8 NT
   int cluster;
-  int whole;  // tiles that one warp each takes; the rest are taken by
-  int split;  // this many warps each
+  int chunk;  // tiles of a cluster that meet at once
+  int ring;   // where the warps' rings start in shared memory
   const void* packed;
   const void* x;
   long long x_stride;
@@ -184,13 +184,31 @@ struct W4Args {
 
 constexpr int kW4Threads = 512;
 constexpr int kW4Warps = kW4Threads / 32;
-// Units on their way to a warp, and CTAs an SM: with one column tile, 64
-// registers and 32 warps an SM; with more, half the warps and more ahead.
+// CTAs an SM: with one column tile 64 registers and 32 warps an SM, with more
+// half the warps.
 template <int NT>
 struct W4Tune {
-  static constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 8 : 6;
   static constexpr int CTAS = NT == 1 ? 2 : 1;
+  static constexpr int AHEAD = NT == 1 ? 4 : 6;  // pairs of units in a warp's ring
 };
+// A ring's slot: a pair of units and their scales.
+__host__ __device__ constexpr int w4_slot(int group) {
+  return 2 * kUnitBytes + (group == 32 ? 128 : group == 64 ? 64 : 32);
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -198,6 +216,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Pairs of codes - 8, exact: 0x4300 is 128 in bf16, whose last bit is 1.
 __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&a)[4]) {
@@ -215,39 +241,56 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&a)[4]) {
 // reads the last row again; its column of the result is not used.
 template <typename TX, int PARTS>
 __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0, int units) {
-  const int eights = units * (kUnit / 8);  // a thread takes eight inputs of a row
+  const int eights = units * (kUnit / 8), all = eights * a.rows;  // a thread takes eight inputs
   const TX* x = static_cast<const TX*>(a.x);
   const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                     a.x_stride * static_cast<long long>(sizeof(TX)) % 16 == 0;
-  for (int r = 0; r < a.rows; ++r)
-    for (int i = threadIdx.x; i < eights; i += blockDim.x) {
-      const int unit = i / 8, in = i % 8 * 8;  // of the unit
-      const int j = (unit0 + unit) * kUnit + in;
-      const TX* from = x + r * a.x_stride + j;
+  constexpr int FLY = 2 * sizeof(TX) == 4 ? 4 : 2;  // of a thread on their way
+  constexpr int W = sizeof(TX) / 2;                 // 16-byte loads of eight inputs
+  for (int i0 = threadIdx.x; i0 < all; i0 += FLY * kW4Threads) {
+    uint4 q[FLY][W];
+    int row[FLY], at[FLY];
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      const int i = i0 + f * kW4Threads;
+      row[f] = i / eights;
+      at[f] = i - row[f] * eights;
+      const int j = unit0 * kUnit + at[f] * 8;
+      if (i < all && wide && j + 8 <= a.sh.k) {
+        const uint4* from = reinterpret_cast<const uint4*>(x + row[f] * a.x_stride + j);
+#pragma unroll
+        for (int e = 0; e < W; ++e) q[f][e] = __ldg(from + e);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      const int i = i0 + f * kW4Threads, j = unit0 * kUnit + at[f] * 8;
+      if (i >= all) break;
       float v[8];
       if (wide && j + 8 <= a.sh.k) {
-        if constexpr (sizeof(TX) == 4) {
-          const float4 lo = __ldg(reinterpret_cast<const float4*>(from));
-          const float4 hi = __ldg(reinterpret_cast<const float4*>(from) + 1);
-          v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-          v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-        } else {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(from));
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        for (int e = 0; e < W; ++e) {
+          const uint32_t w[4] = {q[f][e].x, q[f][e].y, q[f][e].z, q[f][e].w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if constexpr (sizeof(TX) == 4) {
+              v[4 * e + n] = __uint_as_float(w[n]);
+            } else {
+              v[2 * n] = __uint_as_float(w[n] << 16);
+              v[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
+            }
           }
         }
       } else {
+        const TX* from = x + row[f] * a.x_stride + j;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = j + e < a.sh.k ? to_f<TX>(from[e]) : 0.f;
       }
+      const int unit = at[f] / 8, in = at[f] % 8 * 8;  // of the unit
       const int half = in / 32, reg = in / 16 % 2 * 2 + in / 8 % 2;
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) {
-        uint32_t* to = xs + (((unit * PARTS + part) * 2 + half) * a.rows + r) * 16 + reg;
+        uint32_t* to = xs + (((unit * PARTS + part) * 2 + half) * a.rows + row[f]) * 16 + reg;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint32_t word = pack_bf16x2(v[2 * t], v[2 * t + 1]);
@@ -259,228 +302,284 @@ __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0
         }
       }
     }
+  }
 }
 
 // y[r, i]: rows r in columns of the products, outputs i in their rows.  A
-// cluster holds x once, each CTA a range of the inputs.  Most tiles are a
-// warp's own; the last ones, fewer than there are warps, are shared by `split`
-// warps each, a range of the CTA's inputs to a warp.  Partial results meet in
-// shared memory and are added in the order of the inputs.
+// cluster holds x once, each CTA a range of the inputs, and has a run of tiles.
+// The warps of a CTA divide the units of its run evenly: a warp has the end of
+// one tile, some whole ones and the start of another.  What does not end where
+// a tile ends meets in shared memory and is added in the order of the inputs.
 template <typename TX, typename TY, int NT, int GROUP>
 __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
     w4_linear_kernel(const __grid_constant__ W4Args a) {
   constexpr int PARTS = sizeof(TX) == 4 ? 3 : 1;
   constexpr int GRAIN = GROUP > kUnit ? GROUP / kUnit : 1;
+  constexpr int RES = NT * 128;  // results of a tile
   extern __shared__ __align__(16) unsigned char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int cluster = a.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const W4Shape sh = a.sh;
   // Ranges of inputs start at whole groups: pairs of units for groups of 128.
-  auto range = [&](int units, int parts, int i, int& lo, int& hi) {
-    const int per = ((units + GRAIN - 1) / GRAIN + parts - 1) / parts * GRAIN;
-    lo = min(i * per, units);
-    hi = min(lo + per, units);
-  };
-  int u0, u1, none, longest;
-  range(sh.units, cluster, rank, u0, u1);
-  range(sh.units, cluster, 0, none, longest);  // partial results start alike in all CTAs
+  const int longest = ((sh.units + GRAIN - 1) / GRAIN + cluster - 1) / cluster * GRAIN;
+  const int u0 = min(rank * longest, sh.units), units_here = min(longest, sh.units - u0);
   uint32_t* xs = reinterpret_cast<uint32_t*>(smem);
-  float* partial = reinterpret_cast<float*>(
+  // (meeting places start alike in all CTAs)
+  float* heads = reinterpret_cast<float*>(
       smem + static_cast<size_t>(longest) * PARTS * a.rows * (kUnit * 2));
+  float* mains = heads + kW4Warps * RES;  // of warps, or of the cluster's tiles
+  constexpr int AHEAD = W4Tune<NT>::AHEAD, SLOT = w4_slot(GROUP);
+  unsigned char* ring = smem + a.ring + warp * (AHEAD * SLOT);
   grid_dep_wait();
   grid_dep_launch();
-  stage_x<TX, PARTS>(a, xs, u0, u1 - u0);
-  __syncthreads();
-
   const int clusters = gridDim.x / cluster, me = blockIdx.x / cluster;
-  const uint4* codes = static_cast<const uint4*>(a.packed) + lane;
-  const uint32_t* scales =
-      reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.packed) + sh.code_bytes()) +
-      g * (GROUP == 32 ? 2 : 1);
   const uint4* xl = reinterpret_cast<const uint4*>(xs) + t;
   int xrow[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) xrow[nt] = min(nt * 8 + g, a.rows - 1) * 4;
   TY* y = static_cast<TY*>(a.y);
 
-  // a warp's part of a tile: `units` units from v0 of the CTA's range
-  auto product = [&](int tile, int v0, int units, float (&sum)[NT][4]) {
-    constexpr int AHEAD = W4Tune<NT>::AHEAD, WORDS = GROUP == 32 ? 2 : 1;
-    const uint4* src = codes + (static_cast<long long>(tile) * sh.units + u0 + v0) * 32;
-    const uint32_t* sc = scales + (static_cast<long long>(tile) * sh.words * 8 +
-                                   (u0 + v0) * (GROUP == 32 ? 16 : GROUP == 64 ? 8 : 4));
-    const uint4* xu = xl + v0 * (PARTS * 2) * a.rows * 4;
-    uint4 code[AHEAD];
-    uint32_t scale[GROUP == 128 ? AHEAD / 2 : AHEAD][WORDS];
-    // a unit's codes, and scales where it starts a group
-    auto fetch = [&](int i, int ahead) {
-      code[i] = __ldcs(src + (i + ahead) * 32);
-      if constexpr (GROUP == 32) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(sc + (i + ahead) * 16));
-        scale[i][0] = v.x;
-        scale[i][1] = v.y;
-      } else if constexpr (GROUP == 64) {
-        scale[i][0] = __ldcs(sc + (i + ahead) * 8);
-      } else if (i % 2 == 0) {
-        scale[i / 2][0] = __ldcs(sc + (i + ahead) * 4);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (i < units) fetch(i, 0);
-    float acc[NT][4];
-    for (int base = 0; base < units; base += AHEAD) {
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        if (base + i >= units) break;
-        const uint32_t word[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-        const uint32_t sc2[2] = {scale[GROUP == 128 ? i / 2 : i][0],
-                                 scale[GROUP == 128 ? i / 2 : i][WORDS - 1]};
-        if (base + i + AHEAD < units) {
-          if (GROUP == 128 && i % 2 == 0) code[i] = __ldcs(src + (i + AHEAD) * 32);
-          else fetch(i, AHEAD);
-          // a pair's scale is still needed by its second unit
-          if (GROUP == 128 && i % 2 == 1) scale[i / 2][0] = __ldcs(sc + (i - 1 + AHEAD) * 4);
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t a0[4], a1[4];
-          codes_to_bf16(word[2 * half], a0);
-          codes_to_bf16(word[2 * half + 1], a1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (GROUP == 32 || (half == 0 && (GROUP == 64 || i % 2 == 0)))
-              acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-              const uint4 b = xu[(part * 2 + half) * a.rows * 4 + xrow[nt]];
-              mma_bf16(acc[nt], a0, b.x, b.y);
-              mma_bf16(acc[nt], a1, b.z, b.w);
-            }
-          }
-          // the scales of a group whose last product this was
-          if (GROUP == 32 || (half == 1 && (GROUP == 64 || i % 2 == 1))) {
-            const float lo = __uint_as_float(sc2[half] << 16);
-            const float hi = __uint_as_float(sc2[half] & 0xffff0000u);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              sum[nt][0] = fmaf(acc[nt][0], lo, sum[nt][0]);
-              sum[nt][1] = fmaf(acc[nt][1], lo, sum[nt][1]);
-              sum[nt][2] = fmaf(acc[nt][2], hi, sum[nt][2]);
-              sum[nt][3] = fmaf(acc[nt][3], hi, sum[nt][3]);
-            }
-          }
-        }
-        xu += PARTS * 2 * a.rows * 4;
-      }
-      src += AHEAD * 32;
-      sc += AHEAD * (GROUP == 32 ? 16 : GROUP == 64 ? 8 : 4);
-    }
-  };
   auto store = [&](int r, int i, float v) {
     if (r < a.rows && i < sh.n) y[r * a.y_stride + i] = from_f<TY>(v);
   };
-  // where partial results meet: those of `split` warps a tile
-  auto meet = [&](int round, int split, const float (&sum)[NT][4]) {
-    // partial[warp][nt * 8 + column][16 outputs]
-    float* own = partial + warp * (NT * 128);
+  // place[column][16 outputs]
+  auto put = [&](float* place, const float (&sum)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        own[(nt * 8 + 2 * t + (e & 1)) * 16 + g + (e >> 1) * 8] = sum[nt][e];
-    if (cluster > 1) cluster_barrier();
-    else __syncthreads();
-    // this CTA's share of the cluster's results
-    const int results = kW4Warps / split * (NT * 128);
-    for (int z = rank * kW4Threads + static_cast<int>(threadIdx.x); z < results;
-         z += cluster * kW4Threads) {
-      const int w = z / (NT * 128), r = z / 16 % (NT * 8), i = (round + w) * kTileRows + z % 16;
-      if (r >= a.rows) continue;
-      float v = 0.f;
-      for (int c = 0; c < cluster; ++c) {
-        const float* from = partial + w * split * (NT * 128) + z % (NT * 128);
-        if (cluster > 1) from = cluster_pointer(from, c);
-        for (int s = 0; s < split; ++s) v += from[s * (NT * 128)];
-      }
-      store(r, i, v);
-    }
-    if (cluster > 1) cluster_barrier();
-    else __syncthreads();
+        place[(nt * 8 + 2 * t + (e & 1)) * 16 + g + (e >> 1) * 8] = sum[nt][e];
   };
-  // whole tiles first, then the shared ones
-  int split = 1, end = a.whole, round = me * kW4Warps;
-  int v0 = 0, v1 = u1 - u0;
-  while (true) {
-    if (round >= end) {
-      if (end == sh.tiles) break;
-      split = a.split;
-      end = sh.tiles;
-      round = a.whole + me * (kW4Warps / split);
-      range(u1 - u0, split, warp % split, v0, v1);
-      continue;
-    }
-    const int tile = round + warp / split;
-    float sum[NT][4] = {};
-    if (tile < end) product(tile, v0, v1 - v0, sum);
-    if (cluster > 1 || split > 1) {
-      meet(round, split, sum);
-    } else if (tile < end) {
+  const int run0 = static_cast<int>(static_cast<long long>(sh.tiles) * me / clusters);
+  const int run1 = static_cast<int>(static_cast<long long>(sh.tiles) * (me + 1) / clusters);
+  for (int tile0 = run0; tile0 < run1; tile0 += a.chunk) {
+    const int tiles = min(a.chunk, run1 - tile0);
+    // where a warp's units start, counted from the first tile's (fewer than
+    // 2^28: 2^20 tiles of all clusters, 2^12 units)
+    const unsigned all = static_cast<unsigned>(tiles) * units_here;
+    auto start = [&](int w) { return static_cast<int>(all * w / kW4Warps / GRAIN * GRAIN); };
+    const int from = start(warp), mine = start(warp + 1) - from;
+    int j = from / max(units_here, 1);  // tile of the run
+    int v = from - j * units_here;      // its next unit
+    bool begun = v > 0;                 // the tile was begun by an earlier warp
+    // What is fetched next, in pairs that end where a tile ends: a warp's units
+    // come from one run of memory, but for the other CTAs' inputs between tiles.
+    const char* code = static_cast<const char*>(a.packed) + lane * 16 +
+                       (static_cast<long long>(tile0 + j) * sh.units + u0 + v) * kUnitBytes;
+    const char* scale = static_cast<const char*>(a.packed) + sh.code_bytes() + lane * 4 +
+                        (static_cast<long long>(tile0 + j) * sh.words +
+                         (GROUP == 32 ? 2 * (u0 + v) : GROUP == 64 ? u0 + v : (u0 + v) / 2)) * 32;
+    int to_fetch = mine, fv = v;
+    const uint32_t ring_at = smem_u32(ring);
+    uint32_t fill = ring_at;
+    auto fetch = [&]() {
+      if (to_fetch > 0) {
+        const int n = min(min(units_here - fv, to_fetch), 2);
+        copy_async16(fill + lane * 16, code);
+        if (n == 2) copy_async16(fill + kUnitBytes + lane * 16, code + kUnitBytes);
+        constexpr int LANES = GROUP == 32 ? 16 : 8;  // that a unit's scales take
+        if (lane < (GROUP == 128 ? LANES : n * LANES))
+          copy_async4(fill + 2 * kUnitBytes + lane * 4, scale);
+        code += n * kUnitBytes;
+        scale += GROUP == 128 ? 32 : n * LANES * 4;
+        to_fetch -= n;
+        fv += n;
+        if (fv == units_here) {
+          fv = 0;
+          if (cluster > 1) {
+            code += static_cast<long long>(sh.units - units_here) * kUnitBytes;
+            const int words = GROUP == 32 ? 2 * units_here : GROUP == 64 ? units_here : units_here / 2;
+            scale += static_cast<long long>(sh.words - words) * 32;
+          }
+        }
+        fill = fill == ring_at + (AHEAD - 1) * SLOT ? ring_at : fill + SLOT;
+      }
+      copy_commit();
+    };
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          store(nt * 8 + 2 * t + (e & 1), tile * kTileRows + g + (e >> 1) * 8, sum[nt][e]);
+    for (int i = 0; i < AHEAD - 1; ++i) fetch();
+    if (tile0 == run0) {
+      stage_x<TX, PARTS>(a, xs, u0, units_here);
+      __syncthreads();
     }
-    round += clusters * (kW4Warps / split);
+    const unsigned char* slot = ring;
+    const int xhalf = a.rows * 4;  // 16-byte chunks of half a unit and a part
+    const uint4* xu = xl + v * (PARTS * 2) * xhalf;
+    float sum[NT][4] = {}, acc[NT][4];
+    auto product = [&](const uint4& w4, bool odd, uint32_t s0, uint32_t s1) {
+      const uint32_t word[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t a0[4], a1[4];
+        codes_to_bf16(word[2 * half], a0);
+        codes_to_bf16(word[2 * half + 1], a1);
+        const bool first = GROUP == 32 || (half == 0 && (GROUP == 64 || !odd));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint4 b = xu[(part * 2 + half) * xhalf + xrow[nt]];
+            if (first && part == 0) mma_bf16_first(acc[nt], a0, b.x, b.y);
+            else mma_bf16(acc[nt], a0, b.x, b.y);
+            mma_bf16(acc[nt], a1, b.z, b.w);
+          }
+        // the scales of a group whose last product this was
+        if (GROUP == 32 || (half == 1 && (GROUP == 64 || odd))) {
+          const uint32_t s2 = half ? s1 : s0;
+          const float lo = __uint_as_float(s2 << 16), hi = __uint_as_float(s2 & 0xffff0000u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            sum[nt][0] = fmaf(acc[nt][0], lo, sum[nt][0]);
+            sum[nt][1] = fmaf(acc[nt][1], lo, sum[nt][1]);
+            sum[nt][2] = fmaf(acc[nt][2], hi, sum[nt][2]);
+            sum[nt][3] = fmaf(acc[nt][3], hi, sum[nt][3]);
+          }
+        }
+      }
+      xu += PARTS * 2 * xhalf;
+    };
+    // the scale words of a slot's unit
+    auto scale_of = [&](int i, uint32_t& s0, uint32_t& s1) {
+      const unsigned char* p = slot + 2 * kUnitBytes;
+      if constexpr (GROUP == 32) {
+        const uint2 two = reinterpret_cast<const uint2*>(p)[i * 8 + g];
+        s0 = two.x;
+        s1 = two.y;
+      } else {
+        s0 = s1 = reinterpret_cast<const uint32_t*>(p)[(GROUP == 64 ? i * 8 : 0) + g];
+      }
+    };
+    for (int left = mine; left > 0;) {
+      // the warp's units of tile j
+      int units = min(units_here - v, left);
+      left -= units;
+      v += units;
+      for (; units > 0; units -= 2) {
+        copy_wait<AHEAD - 2>();
+        __syncwarp();
+        const uint4 w0 = reinterpret_cast<const uint4*>(slot)[lane];
+        uint32_t s0, s1;
+        scale_of(0, s0, s1);
+        if (GROUP == 128 || units > 1) {
+          const uint4 w1 = reinterpret_cast<const uint4*>(slot + kUnitBytes)[lane];
+          uint32_t s2, s3;
+          scale_of(1, s2, s3);
+          fetch();  // into the slot before this one, which every lane has read
+          product(w0, false, s0, s1);
+          product(w1, true, s2, s3);
+        } else {
+          fetch();
+          product(w0, false, s0, s1);
+        }
+        slot = slot == ring + (AHEAD - 1) * SLOT ? ring : slot + SLOT;
+      }
+      if (begun) {
+        put(heads + warp * RES, sum);
+      } else if (cluster > 1) {
+        put(mains + j * RES, sum);
+      } else if (v < units_here) {
+        put(mains + warp * RES, sum);
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            store(nt * 8 + 2 * t + (e & 1), (tile0 + j) * kTileRows + g + (e >> 1) * 8, sum[nt][e]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = sum[nt][2] = sum[nt][3] = 0.f;
+      ++j;
+      v = 0;
+      begun = false;
+      xu = xl;
+    }
+    copy_wait<0>();
+    __syncthreads();
+    if (cluster == 1) {
+      // a warp's last tile, where other warps go on with it
+      for (int z = threadIdx.x; z < kW4Warps * RES; z += kW4Threads) {
+        const int w = z / RES, e = z % RES, r = e / 16;
+        const int b0 = start(w), b1 = start(w + 1);
+        if (b0 == b1 || r >= a.rows) continue;
+        const int jw = b1 / units_here, begin = jw * units_here;
+        if (b1 == begin || b0 > begin) continue;  // it ends here, or starts with an earlier warp
+        float sumv = mains[z];
+        for (int o = w + 1; o < kW4Warps; ++o) {
+          const int s0 = start(o);
+          if (s0 >= begin + units_here) break;
+          if (s0 < start(o + 1)) sumv += heads[o * RES + e];
+        }
+        store(r, (tile0 + jw) * kTileRows + e % 16, sumv);
+      }
+    } else {
+      // tiles in one piece, then the pieces of all ranges of the inputs
+      if (units_here == 0)
+        for (int z = threadIdx.x; z < tiles * RES; z += kW4Threads) mains[z] = 0.f;
+      for (int o = 1; o < kW4Warps && units_here; ++o) {
+        const int b0 = start(o);
+        if (b0 < start(o + 1) && b0 % units_here)
+          for (int e = threadIdx.x; e < RES; e += kW4Threads)
+            mains[b0 / units_here * RES + e] += heads[o * RES + e];
+      }
+      cluster_barrier();
+      for (int z = rank * kW4Threads + static_cast<int>(threadIdx.x); z < tiles * RES;
+           z += cluster * kW4Threads) {
+        const int e = z % RES, r = e / 16;
+        if (r >= a.rows) continue;
+        float sumv = 0.f;
+        for (int c = 0; c < cluster; ++c) sumv += *cluster_pointer(mains + z, c);
+        store(r, (tile0 + z / RES) * kTileRows + e % 16, sumv);
+      }
+      cluster_barrier();
+    }
+    __syncthreads();
   }
 }
 
 struct W4Plan {
-  int cluster, whole, split, ctas;
+  int cluster, chunk, ctas;
   size_t smem;
 };
 constexpr size_t kW4MostShared = 220 * 1024;
+// tiles that a cluster's CTAs put together at once
+static int w4_chunk(int nt) { return 32 / nt; }
 
-static int w4_grain(const W4Shape& sh) { return sh.group > kUnit ? sh.group / kUnit : 1; }
-static int w4_longest(const W4Shape& sh, int units, int parts) {
-  const int grain = w4_grain(sh);
-  return ((units + grain - 1) / grain + parts - 1) / parts * grain;
+// Shared memory: x, the places where results meet, the warps' rings.
+static size_t w4_ring_at(const W4Shape& sh, int rows, int parts, int nt, int cluster) {
+  const int grain = sh.group > kUnit ? sh.group / kUnit : 1;
+  const int longest = ((sh.units + grain - 1) / grain + cluster - 1) / cluster * grain;
+  return static_cast<size_t>(longest) * parts * rows * (kUnit * 2) +
+         static_cast<size_t>(kW4Warps + (cluster > 1 ? w4_chunk(nt) : kW4Warps)) * nt * 128 * 4;
 }
 static size_t w4_held(const W4Shape& sh, int rows, int parts, int nt, int cluster) {
-  return static_cast<size_t>(w4_longest(sh, sh.units, cluster)) * parts * rows * (kUnit * 2) +
-         static_cast<size_t>(kW4Warps) * nt * 128 * 4;
+  return w4_ring_at(sh, rows, parts, nt, cluster) +
+         static_cast<size_t>(kW4Warps) * w4_slot(sh.group) *
+             (nt == 1 ? W4Tune<1>::AHEAD : nt == 2 ? W4Tune<2>::AHEAD : W4Tune<4>::AHEAD);
 }
 
-// Steps that the slowest warp takes, in units: rounds of whole tiles, then
-// rounds of shared ones, each with what meeting costs; and the time that x
-// takes into shared memory.  The cheapest of the few choices is taken.
+// The time that the busiest CTA takes, by the number of CTAs that share the
+// inputs, in microseconds as measured (0.3 a unit of each of its warps, 64 KB of
+// x into shared memory in one, 1.5 a meeting of a cluster): the cheapest of the
+// four choices is taken.
 static W4Plan w4_plan(const W4Shape& sh, int rows, int parts, int nt, int sms) {
   W4Plan best = {};
   double least = 1e30;
   for (int cluster = 1; cluster <= 8; cluster *= 2) {
     const size_t held = w4_held(sh, rows, parts, nt, cluster);
-    const int per_sm = nt == 1 && held <= kW4MostShared / 2 ? 2 : 1;
     if (held > kW4MostShared) continue;
-    const int most = per_sm * sms / cluster;  // clusters
-    const int units = w4_longest(sh, sh.units, cluster);
-    const long long warps = static_cast<long long>(most) * kW4Warps;
-    const int full = static_cast<int>(sh.tiles / warps);
-    const long long left = sh.tiles - full * warps;
-    for (int split = 1; split <= kW4Warps; split *= 2) {
-      const int at_once = kW4Warps / split;
-      const long long groups = (left + at_once - 1) / at_once;
-      const long long rounds = (groups + most - 1) / most;
-      const double meet = cluster > 1 ? 6.0 : 3.0;
-      const double cost = full * (units + (cluster > 1 ? meet : 0.0)) +
-                          rounds * (w4_longest(sh, units, split) + meet) +
-                          static_cast<double>(held) / 8192.0;
-      if (cost < least) {
-        least = cost;
-        const long long ctas = full ? most : std::min<long long>(groups, most);
-        best = W4Plan{cluster, static_cast<int>(full * warps), split,
-                      static_cast<int>(ctas) * cluster, held};
-      }
+    const int per_sm = nt == 1 && held <= kW4MostShared / 2 ? 2 : 1;
+    const int most = std::max(1, per_sm * sms / cluster);  // clusters
+    const int tiles = (sh.tiles + most - 1) / most;        // of a cluster
+    // few tiles: no more clusters than it takes for every one to have as many
+    const int clusters = tiles > 4 ? std::min(most, sh.tiles) : (sh.tiles + tiles - 1) / tiles;
+    const double units = static_cast<double>(tiles) * ((sh.units + cluster - 1) / cluster);
+    const double share = std::max(1.0, static_cast<double>(clusters) * cluster / sms);
+    const double x = static_cast<double>(sh.k) / cluster * parts * rows * 2;
+    const double cost = std::ceil(units / kW4Warps) * 0.3 * share + x / 65536.0 +
+                        (cluster > 1 ? 1.5 * ((tiles + w4_chunk(nt) - 1) / w4_chunk(nt)) : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = W4Plan{cluster, cluster > 1 ? w4_chunk(nt) : tiles, clusters * cluster, held};
     }
   }
   return best;
@@ -491,8 +590,8 @@ static cudaError_t launch_w4(W4Args a, int sms, cudaStream_t s) {
   const W4Plan p = w4_plan(a.sh, a.rows, sizeof(TX) == 4 ? 3 : 1, NT, sms);
   if (p.ctas == 0) return cudaErrorInvalidValue;  // not reached: w4_rows_at_once
   a.cluster = p.cluster;
-  a.whole = p.whole;
-  a.split = p.split;
+  a.chunk = p.chunk;
+  a.ring = static_cast<int>(w4_ring_at(a.sh, a.rows, sizeof(TX) == 4 ? 3 : 1, NT, p.cluster));
   auto kernel = w4_linear_kernel<TX, TY, NT, GROUP>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(p.smem));
