@@ -54,9 +54,9 @@ pe_status pe_w4_quantize(const void* w, int32_t dtype, int64_t w_stride, int32_t
  * bf16 -> fp32 or fp32 -> fp32; rows x_stride and y_stride elements apart, y
  * not overlapping x.  Products are exact, sums and scales are in fp32, in an
  * order that depends on the sizes and the device only; y is rounded once.
- * fp32 x is taken as three bf16 parts (right to 2^-24 of an element; an
- * element below 2^-110 may lose its last bits, one past 2^127.99 or infinite
- * gives NaN).
+ * An element of x is right to 2^-38 of the largest of its row or better;
+ * fp32 ones also to 2^-24 of themselves.  A row with an infinite or NaN
+ * element gives infinities and NaN, the other rows are as they would be.
  * Made for a few rows: up to 32 cost one pass over the weights, each further
  * 32 another.
  * PE_ERR_INVALID_ARGUMENT: rows < 1, sizes as pe_w4_pack, another

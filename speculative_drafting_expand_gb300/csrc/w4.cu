@@ -6,14 +6,15 @@
 // codes, [tile][unit][lane][16 bytes]: word j of a lane is its part of the left operand of one m16n8k16
 // product (inputs 16 j .. 16 j + 15 of the unit), so a warp reads a unit as
 // one 512-byte line and needs no exchange.  Register i of the operand takes
-// nibbles i (low half) and i + 4 (high half) of the word: one shift and one
-// logic operation make a pair of bf16 numbers 128 + code, one subtraction the
-// exact pair code - 8.  Then the scales, bf16, rows g and g + 8 of a tile side
+// nibbles i (low half) and i + 4 (high half) of the word, from which a logic
+// operation and an addition make a pair of fp16 numbers code - 8, exact.  Then the scales, bf16, rows g and g + 8 of a tile side
 // by side in a word, which is what a lane needs of a group: groups of 32, two
 // words a unit, [tile][unit][g][2]; of 64, [tile][unit][g]; of 128,
 // [tile][pair of units][g].
 #include <algorithm>
 #include <cmath>
+
+#include <cuda_fp16.h>
 
 #include "../../include/peagle_w4.h"
 #include "pe_common.cuh"
@@ -210,28 +211,64 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // The same from zero.
-__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %10, %10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Pairs of codes - 8, exact: 0x4300 is 128 in bf16, whose last bit is 1.
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&a)[4]) {
+// Pairs of codes - 8 in fp16, exact.  0x6400 is 1024, whose last bit is 1: the
+// low nibble of each half gives 1024 + code, the next one 1024 + 16 code.
+// (bf16 has room for one nibble a half and takes two instructions a pair of
+// additions: 115 instructions a unit instead of 93.)
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&a)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w >> (4 * i)));
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(v), "r"(0x43084308u));
+  for (int i = 0; i < 2; ++i) {
+    uint32_t lo, hi;
+    const uint32_t v = i ? w >> 8 : w;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(lo) : "r"(v));
+    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(hi) : "r"(v));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(a[2 * i]) : "r"(lo), "r"(0x64086408u));  // - 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"  // / 16 - 72
+        : "=r"(a[2 * i + 1])
+        : "r"(hi), "r"(0x2c002c00u), "r"(0xd480d480u));
+  }
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight inputs of a row from j on, zeros past the last.
+template <typename TX>
+__device__ __forceinline__ void load_eight(const TX* from, int j, int k, bool wide, float (&v)[8]) {
+  if (wide && j + 8 <= k) {
+#pragma unroll
+    for (int e = 0; e < static_cast<int>(sizeof(TX)) / 2; ++e) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(from) + e);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if constexpr (sizeof(TX) == 4) {
+          v[4 * e + n] = __uint_as_float(w[n]);
+        } else {
+          v[2 * n] = __uint_as_float(w[n] << 16);
+          v[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e < k ? to_f<TX>(from[e]) : 0.f;
   }
 }
 
@@ -239,66 +276,71 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&a)[4]) {
 // bytes], 16 bytes being the four registers of lane (row, t) for the two
 // 16-input steps of half a unit.  A lane whose column is past the last row
 // reads the last row again; its column of the result is not used.
+// fp16 has bf16's bits and more, but not its range: each row (of this CTA's
+// inputs) is multiplied by the power of two, an even one, that brings its
+// largest to 2^13 .. 2^15, and elements below 2^-27 of that lose bits, at most
+// 2^-25, 2^-38 of the largest.  fp32 x is taken as three fp16 parts, 24 bits
+// above that.
 template <typename TX, int PARTS>
-__device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0, int units) {
+__device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0, int units,
+                                        uint32_t* largest, float* unscale) {
   const int eights = units * (kUnit / 8), all = eights * a.rows;  // a thread takes eight inputs
   const TX* x = static_cast<const TX*>(a.x);
   const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                     a.x_stride * static_cast<long long>(sizeof(TX)) % 16 == 0;
-  constexpr int FLY = 2 * sizeof(TX) == 4 ? 4 : 2;  // of a thread on their way
-  constexpr int W = sizeof(TX) / 2;                 // 16-byte loads of eight inputs
-  for (int i0 = threadIdx.x; i0 < all; i0 += FLY * kW4Threads) {
-    uint4 q[FLY][W];
-    int row[FLY], at[FLY];
-#pragma unroll
-    for (int f = 0; f < FLY; ++f) {
-      const int i = i0 + f * kW4Threads;
-      row[f] = i / eights;
-      at[f] = i - row[f] * eights;
-      const int j = unit0 * kUnit + at[f] * 8;
-      if (i < all && wide && j + 8 <= a.sh.k) {
-        const uint4* from = reinterpret_cast<const uint4*>(x + row[f] * a.x_stride + j);
-#pragma unroll
-        for (int e = 0; e < W; ++e) q[f][e] = __ldg(from + e);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < FLY; ++f) {
-      const int i = i0 + f * kW4Threads, j = unit0 * kUnit + at[f] * 8;
-      if (i >= all) break;
+  if (threadIdx.x < 32) largest[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i0 = threadIdx.x - threadIdx.x % 32; i0 < all; i0 += kW4Threads) {
+    const int i = i0 + static_cast<int>(threadIdx.x) % 32;
+    uint32_t top = 0;
+    int r = -1;
+    if (i < all) {
+      r = i / eights;
+      const int j = unit0 * kUnit + (i - r * eights) * 8;
       float v[8];
-      if (wide && j + 8 <= a.sh.k) {
+      load_eight<TX>(x + r * a.x_stride + j, j, a.sh.k, wide, v);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const uint32_t w[4] = {q[f][e].x, q[f][e].y, q[f][e].z, q[f][e].w};
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+    }
+    // mostly a warp's inputs are of one row
+    const int r0 = __shfl_sync(0xffffffffu, r, 0);
+    if (__all_sync(0xffffffffu, r == r0)) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (threadIdx.x % 32 == 0) atomicMax(&largest[r], top);
+    } else if (r >= 0) {
+      atomicMax(&largest[r], top);
+    }
+  }
+  __syncthreads();
+  // half of the power: its square may be past what fp32 has
+  auto half_shift = [&](int r) {
+    const int e = static_cast<int>(largest[r] >> 23);
+    return e == 255 ? 0 : (14 + 127 - e) >> 1;
+  };
+  if (threadIdx.x < a.rows)
+    unscale[threadIdx.x] = __uint_as_float((127 - half_shift(threadIdx.x)) << 23);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < all; i += kW4Threads) {
+    const int r = i / eights, at = i - r * eights, j = unit0 * kUnit + at * 8;
+    float v[8];
+    load_eight<TX>(x + r * a.x_stride + j, j, a.sh.k, wide, v);
+    const float scale = __uint_as_float((127 + half_shift(r)) << 23);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if constexpr (sizeof(TX) == 4) {
-              v[4 * e + n] = __uint_as_float(w[n]);
-            } else {
-              v[2 * n] = __uint_as_float(w[n] << 16);
-              v[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
-            }
-          }
-        }
-      } else {
-        const TX* from = x + row[f] * a.x_stride + j;
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * scale * scale;
+    const int unit = at / 8, in = at % 8 * 8;  // of the unit
+    const int half = in / 32, reg = in / 16 % 2 * 2 + in / 8 % 2;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = j + e < a.sh.k ? to_f<TX>(from[e]) : 0.f;
-      }
-      const int unit = at[f] / 8, in = at[f] % 8 * 8;  // of the unit
-      const int half = in / 32, reg = in / 16 % 2 * 2 + in / 8 % 2;
+    for (int part = 0; part < PARTS; ++part) {
+      uint32_t* to = xs + (((unit * PARTS + part) * 2 + half) * a.rows + r) * 16 + reg;
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        uint32_t* to = xs + (((unit * PARTS + part) * 2 + half) * a.rows + row[f]) * 16 + reg;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t word = pack_bf16x2(v[2 * t], v[2 * t + 1]);
-          to[t * 4] = word;
-          if (part + 1 < PARTS) {
-            v[2 * t] -= __uint_as_float(word << 16);
-            v[2 * t + 1] -= __uint_as_float(word & 0xffff0000u);
-          }
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t word = pack_f16x2(v[2 * t], v[2 * t + 1]);
+        to[t * 4] = word;
+        if (part + 1 < PARTS) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word));
+          v[2 * t] -= f.x;
+          v[2 * t + 1] -= f.y;
         }
       }
     }
@@ -330,6 +372,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
   float* mains = heads + kW4Warps * RES;  // of warps, or of the cluster's tiles
   constexpr int AHEAD = W4Tune<NT>::AHEAD, SLOT = w4_slot(GROUP);
   unsigned char* ring = smem + a.ring + warp * (AHEAD * SLOT);
+  __shared__ uint32_t largest[32];
+  __shared__ __align__(8) float unscale[32];
   grid_dep_wait();
   grid_dep_launch();
   const int clusters = gridDim.x / cluster, me = blockIdx.x / cluster;
@@ -399,7 +443,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
 #pragma unroll
     for (int i = 0; i < AHEAD - 1; ++i) fetch();
     if (tile0 == run0) {
-      stage_x<TX, PARTS>(a, xs, u0, units_here);
+      stage_x<TX, PARTS>(a, xs, u0, units_here, largest, unscale);
       __syncthreads();
     }
     const unsigned char* slot = ring;
@@ -411,17 +455,17 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t a0[4], a1[4];
-        codes_to_bf16(word[2 * half], a0);
-        codes_to_bf16(word[2 * half + 1], a1);
+        codes_to_f16(word[2 * half], a0);
+        codes_to_f16(word[2 * half + 1], a1);
         const bool first = GROUP == 32 || (half == 0 && (GROUP == 64 || !odd));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
             const uint4 b = xu[(part * 2 + half) * xhalf + xrow[nt]];
-            if (first && part == 0) mma_bf16_first(acc[nt], a0, b.x, b.y);
-            else mma_bf16(acc[nt], a0, b.x, b.y);
-            mma_bf16(acc[nt], a1, b.z, b.w);
+            if (first && part == 0) mma_f16_first(acc[nt], a0, b.x, b.y);
+            else mma_f16(acc[nt], a0, b.x, b.y);
+            mma_f16(acc[nt], a1, b.z, b.w);
           }
         // the scales of a group whose last product this was
         if (GROUP == 32 || (half == 1 && (GROUP == 64 || odd))) {
@@ -472,6 +516,15 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
           product(w0, false, s0, s1);
         }
         slot = slot == ring + (AHEAD - 1) * SLOT ? ring : slot + SLOT;
+      }
+      // (columns past the last row have no scale, and no use)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 back = *reinterpret_cast<const float2*>(unscale + nt * 8 + 2 * t);
+        sum[nt][0] = sum[nt][0] * back.x * back.x;
+        sum[nt][1] = sum[nt][1] * back.y * back.y;
+        sum[nt][2] = sum[nt][2] * back.x * back.x;
+        sum[nt][3] = sum[nt][3] * back.y * back.y;
       }
       if (begun) {
         put(heads + warp * RES, sum);

@@ -96,6 +96,35 @@ def test_strides_offsets_and_untouched_columns(xt):
         assert (out[:, :3] == 7).all() and (out[:, 3 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_rows_of_any_magnitude(xt):
+    """A power of two on a row is one on its results, from the smallest normal
+    numbers to the largest; and a row's small elements count beside large
+    ones: right to 2^-38 of the largest (fp32: or 2^-24 of themselves)."""
+    torch, B = _lib()
+    rng = np.random.default_rng(12)
+    n, k = 40, 300
+    w, m = _weight(torch, B, rng, n, k, 32)
+    base = torch.from_numpy(rng.uniform(0.5, 1.0, k).astype(np.float32)).to(_type(torch, xt)).cuda()
+    p = torch.tensor([-119, -101, -60, -14, 0, 1, 15, 16, 61, 100, 118], device="cuda")
+    x = (base.float()[None] * torch.exp2(p.double())[:, None].float()).to(_type(torch, xt))
+    y = B.pe_w4_linear(w, x, out_dtype=torch.float32).double()
+    back = y * torch.exp2(-p.double())[:, None]
+    i0 = int((p == 0).nonzero())
+    # odd powers meet another even one: the same sums, on another grid of fp16
+    assert torch.equal(back[0::1][p % 2 == 0], back[i0].expand(int((p % 2 == 0).sum()), n))
+    for r in range(len(p)):
+        _check(back[r][None], base.double()[None], m, 32, xt, "f32")
+    x = torch.from_numpy((rng.normal(size=(3, k)) * np.exp2(-rng.integers(0, 45, (3, k)))).astype(
+        np.float32)).to(_type(torch, xt)).cuda()
+    y = B.pe_w4_linear(w, x, out_dtype=torch.float32).double().cpu().numpy()
+    xd = x.double().cpu().numpy()
+    s = np.abs(xd) @ np.abs(m).T
+    grid = 2.0 ** -38 * np.abs(xd).max(1)[:, None] * np.abs(m).sum(1)[None]
+    parts = 3 if xt == "f32" else 1
+    assert (np.abs(y - xd @ m.T) <= (2 * parts * 32 + 2 * 10 + 67) * U * s + grid).all()
+
+
 def test_values_of_other_rows_do_not_matter():
     """A row of infinities or NaN leaves the others as they are."""
     torch, B = _lib()
