@@ -12,6 +12,7 @@
 // words a unit, [tile][unit][g][2]; of 64, [tile][unit][g]; of 128,
 // [tile][pair of units][g].
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -190,7 +191,7 @@ constexpr int kW4Warps = kW4Threads / 32;
 template <int NT>
 struct W4Tune {
   static constexpr int CTAS = NT == 1 ? 2 : 1;
-  static constexpr int AHEAD = NT == 1 ? 4 : 6;  // pairs of units in a warp's ring
+  static constexpr int AHEAD = NT == 1 ? 3 : 4;  // pairs of units in a warp's ring
 };
 // A ring's slot: a pair of units and their scales.
 __host__ __device__ constexpr int w4_slot(int group) {
@@ -248,28 +249,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight inputs of a row from j on, zeros past the last.
+// 16 bytes of a row from element j on, zeros past the last.
 template <typename TX>
-__device__ __forceinline__ void load_eight(const TX* from, int j, int k, bool wide, float (&v)[8]) {
-  if (wide && j + 8 <= k) {
+__device__ __forceinline__ uint4 load_inputs(const TX* from, int j, int k, bool wide) {
+  constexpr int E = 16 / static_cast<int>(sizeof(TX));
+  if (wide && j + E <= k) return __ldg(reinterpret_cast<const uint4*>(from));
+  uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < static_cast<int>(sizeof(TX)) / 2; ++e) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(from) + e);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if constexpr (sizeof(TX) == 4) {
-          v[4 * e + n] = __uint_as_float(w[n]);
-        } else {
-          v[2 * n] = __uint_as_float(w[n] << 16);
-          v[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
-        }
-      }
+  for (int n = 0; n < 4; ++n) {
+    if constexpr (sizeof(TX) == 4) {
+      w[n] = j + n < k ? __float_as_uint(from[n]) : 0u;
+    } else {
+      const uint32_t lo = j + 2 * n < k ? __bfloat16_as_ushort(from[2 * n]) : 0u;
+      const uint32_t hi = j + 2 * n + 1 < k ? __bfloat16_as_ushort(from[2 * n + 1]) : 0u;
+      w[n] = lo | hi << 16;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = j + e < k ? to_f<TX>(from[e]) : 0.f;
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // x in shared memory, as the products' right operand: [unit][part][half][row][t][16
@@ -280,36 +276,59 @@ __device__ __forceinline__ void load_eight(const TX* from, int j, int k, bool wi
 // inputs) is multiplied by the power of two, an even one, that brings its
 // largest to 2^13 .. 2^15, and elements below 2^-27 of that lose bits, at most
 // 2^-25, 2^-38 of the largest.  fp32 x is taken as three fp16 parts, 24 bits
-// above that.
-template <typename TX, int PARTS>
+// above that.  16-bit x is put in place as it is while the largest are found,
+// and turned there, FLY loads of a thread at a time; fp32 x is read twice.
+template <typename TX, int PARTS, int FLY>
 __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0, int units,
                                         uint32_t* largest, float* unscale) {
-  const int eights = units * (kUnit / 8), all = eights * a.rows;  // a thread takes eight inputs
+  constexpr int E = 16 / static_cast<int>(sizeof(TX));  // elements a thread takes at a time
+  const int chunks = units * (kUnit / E), all = chunks * a.rows;
   const TX* x = static_cast<const TX*>(a.x);
   const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                     a.x_stride * static_cast<long long>(sizeof(TX)) % 16 == 0;
+  // word of the pair of inputs `in` (of its unit) in part 0
+  auto place = [&](int r, int unit, int in) {
+    return ((unit * PARTS * 2 + in / 32) * a.rows + r) * 16 + in / 2 % 4 * 4 + in / 16 % 2 * 2 +
+           in / 8 % 2;
+  };
+  const int part_words = 2 * a.rows * 16;
   if (threadIdx.x < 32) largest[threadIdx.x] = 0;
   __syncthreads();
-#pragma unroll 4
-  for (int i0 = threadIdx.x - threadIdx.x % 32; i0 < all; i0 += kW4Threads) {
-    const int i = i0 + static_cast<int>(threadIdx.x) % 32;
-    uint32_t top = 0;
-    int r = -1;
-    if (i < all) {
-      r = i / eights;
-      const int j = unit0 * kUnit + (i - r * eights) * 8;
-      float v[8];
-      load_eight<TX>(x + r * a.x_stride + j, j, a.sh.k, wide, v);
+  for (int i0 = threadIdx.x - threadIdx.x % 32; i0 < all; i0 += FLY * kW4Threads) {
+    uint4 q[FLY];
+    int row[FLY], at[FLY];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+    for (int f = 0; f < FLY; ++f) {
+      const int i = i0 + f * kW4Threads + static_cast<int>(threadIdx.x) % 32;
+      row[f] = i < all ? i / chunks : -1;
+      at[f] = (i - row[f] * chunks) * E;
+      if (row[f] >= 0)
+        q[f] = load_inputs<TX>(x + row[f] * a.x_stride + unit0 * kUnit + at[f],
+                               unit0 * kUnit + at[f], a.sh.k, wide);
     }
-    // mostly a warp's inputs are of one row
-    const int r0 = __shfl_sync(0xffffffffu, r, 0);
-    if (__all_sync(0xffffffffu, r == r0)) {
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (threadIdx.x % 32 == 0) atomicMax(&largest[r], top);
-    } else if (r >= 0) {
-      atomicMax(&largest[r], top);
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      if (i0 + f * kW4Threads >= all) break;  // (for the whole warp)
+      uint32_t top = 0;
+      if (row[f] >= 0) {
+        const uint32_t w[4] = {q[f].x, q[f].y, q[f].z, q[f].w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          top = max(top, w[n] & (sizeof(TX) == 4 ? 0x7fffffffu : 0x7fff0000u));
+          if constexpr (sizeof(TX) == 2) {
+            top = max(top, (w[n] & 0x7fffu) << 16);
+            xs[place(row[f], at[f] / kUnit, at[f] % kUnit + 2 * n)] = w[n];
+          }
+        }
+      }
+      // mostly a warp's inputs are of one row
+      const int r0 = __shfl_sync(0xffffffffu, row[f], 0);
+      if (__all_sync(0xffffffffu, row[f] == r0)) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (threadIdx.x % 32 == 0) atomicMax(&largest[r0], top);
+      } else if (row[f] >= 0) {
+        atomicMax(&largest[row[f]], top);
+      }
     }
   }
   __syncthreads();
@@ -318,29 +337,39 @@ __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0
     const int e = static_cast<int>(largest[r] >> 23);
     return e == 255 ? 0 : (14 + 127 - e) >> 1;
   };
+  auto scale_of = [&](int r) { return __uint_as_float((127 + half_shift(r)) << 23); };
   if (threadIdx.x < a.rows)
     unscale[threadIdx.x] = __uint_as_float((127 - half_shift(threadIdx.x)) << 23);
+  if constexpr (sizeof(TX) == 2) {
+    uint4* xq = reinterpret_cast<uint4*>(xs);
+    for (int c = threadIdx.x; c < all; c += kW4Threads) {
+      const float scale = scale_of(c / 4 % a.rows);
+      const uint4 q = xq[c];
+      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        w[n] = pack_f16x2(__uint_as_float(w[n] << 16) * scale * scale,
+                          __uint_as_float(w[n] & 0xffff0000u) * scale * scale);
+      xq[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
 #pragma unroll 2
-  for (int i = threadIdx.x; i < all; i += kW4Threads) {
-    const int r = i / eights, at = i - r * eights, j = unit0 * kUnit + at * 8;
-    float v[8];
-    load_eight<TX>(x + r * a.x_stride + j, j, a.sh.k, wide, v);
-    const float scale = __uint_as_float((127 + half_shift(r)) << 23);
+    for (int i = threadIdx.x; i < all; i += kW4Threads) {
+      const int r = i / chunks, at = (i - r * chunks) * E, j = unit0 * kUnit + at;
+      const float scale = scale_of(r);
+      const uint4 q = load_inputs<TX>(x + r * a.x_stride + j, j, a.sh.k, wide);
+      float v[4] = {__uint_as_float(q.x) * scale * scale, __uint_as_float(q.y) * scale * scale,
+                    __uint_as_float(q.z) * scale * scale, __uint_as_float(q.w) * scale * scale};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * scale * scale;
-    const int unit = at / 8, in = at % 8 * 8;  // of the unit
-    const int half = in / 32, reg = in / 16 % 2 * 2 + in / 8 % 2;
+      for (int n = 0; n < 4; n += 2) {
+        uint32_t* to = xs + place(r, at / kUnit, at % kUnit + n);
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-      uint32_t* to = xs + (((unit * PARTS + part) * 2 + half) * a.rows + r) * 16 + reg;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t word = pack_f16x2(v[2 * t], v[2 * t + 1]);
-        to[t * 4] = word;
-        if (part + 1 < PARTS) {
+        for (int part = 0; part < PARTS; ++part) {
+          const uint32_t word = pack_f16x2(v[n], v[n + 1]);
+          to[part * part_words] = word;
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word));
-          v[2 * t] -= f.x;
-          v[2 * t + 1] -= f.y;
+          v[n] -= f.x;
+          v[n + 1] -= f.y;
         }
       }
     }
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
 #pragma unroll
     for (int i = 0; i < AHEAD - 1; ++i) fetch();
     if (tile0 == run0) {
-      stage_x<TX, PARTS>(a, xs, u0, units_here, largest, unscale);
+      stage_x<TX, PARTS, NT == 1 ? 2 : 8>(a, xs, u0, units_here, largest, unscale);
       __syncthreads();
     }
     const unsigned char* slot = ring;
@@ -610,25 +639,60 @@ static size_t w4_held(const W4Shape& sh, int rows, int parts, int nt, int cluste
              (nt == 1 ? W4Tune<1>::AHEAD : nt == 2 ? W4Tune<2>::AHEAD : W4Tune<4>::AHEAD);
 }
 
+// Clusters of one kernel that are resident at a time: a GPC's SMs need not be a
+// multiple of the cluster.  Asked once a process, device and shape.
+template <typename TX, typename TY, int NT, int GROUP>
+static int resident_clusters(int cluster, int per_sm, size_t smem, int sms) {
+  if (cluster == 1) return per_sm * sms;
+  static std::atomic<int> known[16][2][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const int c = cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+  std::atomic<int>* place = dev < 16 ? &known[dev][per_sm - 1][c] : nullptr;
+  int n = place ? place->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  auto kernel = w4_linear_kernel<TX, TY, NT, GROUP>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kW4Threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+    n = std::max(1, per_sm * sms / cluster / 2);
+  else if (place)
+    place->store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // The time that the busiest CTA takes, by the number of CTAs that share the
-// inputs, in microseconds as measured (0.3 a unit of each of its warps, 64 KB of
+// inputs, in microseconds as measured (0.3 a unit of each of its warps, 32 KB of
 // x into shared memory in one, 1.5 a meeting of a cluster): the cheapest of the
 // four choices is taken.
-static W4Plan w4_plan(const W4Shape& sh, int rows, int parts, int nt, int sms) {
+template <typename TX, typename TY, int NT, int GROUP>
+static W4Plan w4_plan(const W4Shape& sh, int rows, int sms) {
+  constexpr int nt = NT, parts = sizeof(TX) == 4 ? 3 : 1;
   W4Plan best = {};
   double least = 1e30;
   for (int cluster = 1; cluster <= 8; cluster *= 2) {
     const size_t held = w4_held(sh, rows, parts, nt, cluster);
     if (held > kW4MostShared) continue;
     const int per_sm = nt == 1 && held <= kW4MostShared / 2 ? 2 : 1;
-    const int most = std::max(1, per_sm * sms / cluster);  // clusters
+    const int most = resident_clusters<TX, TY, NT, GROUP>(cluster, per_sm, held, sms);
     const int tiles = (sh.tiles + most - 1) / most;        // of a cluster
     // few tiles: no more clusters than it takes for every one to have as many
     const int clusters = tiles > 4 ? std::min(most, sh.tiles) : (sh.tiles + tiles - 1) / tiles;
     const double units = static_cast<double>(tiles) * ((sh.units + cluster - 1) / cluster);
     const double share = std::max(1.0, static_cast<double>(clusters) * cluster / sms);
     const double x = static_cast<double>(sh.k) / cluster * parts * rows * 2;
-    const double cost = std::ceil(units / kW4Warps) * 0.3 * share + x / 65536.0 +
+    const double cost = std::ceil(units / kW4Warps) * 0.3 * share + x / 32768.0 +
                         (cluster > 1 ? 1.5 * ((tiles + w4_chunk(nt) - 1) / w4_chunk(nt)) : 0.0);
     if (cost < least) {
       least = cost;
@@ -640,7 +704,7 @@ static W4Plan w4_plan(const W4Shape& sh, int rows, int parts, int nt, int sms) {
 
 template <typename TX, typename TY, int NT, int GROUP>
 static cudaError_t launch_w4(W4Args a, int sms, cudaStream_t s) {
-  const W4Plan p = w4_plan(a.sh, a.rows, sizeof(TX) == 4 ? 3 : 1, NT, sms);
+  const W4Plan p = w4_plan<TX, TY, NT, GROUP>(a.sh, a.rows, sms);
   if (p.ctas == 0) return cudaErrorInvalidValue;  // not reached: w4_rows_at_once
   a.cluster = p.cluster;
   a.chunk = p.chunk;
