@@ -57,10 +57,21 @@ struct VerifyArgs {
 };
 
 // ------------------------------------------------------------------ numbers
+constexpr float kLargest = 3.402823466e38f;
 // NaN counts as -inf, +inf as the largest finite number, -0 as 0 (which gives
 // equal logits one sort key).
 __device__ __forceinline__ float clean_logit(float x) {
-  return fminf(fmaxf(x, -INFINITY), 3.402823466e38f) + 0.f;
+  return fminf(fmaxf(x, -INFINITY), kLargest) + 0.f;
+}
+// min(x, most); NaN stays NaN.
+__device__ __forceinline__ float at_most(float x, float most) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(most));
+  return r;
+}
+// Tokens in their order are falling keys.
+__device__ __forceinline__ unsigned long long token_key(float x, int id) {
+  return argmax_key(x + 0.f, id);
 }
 template <typename T>
 __device__ __forceinline__ float raw_logit(const T* p) {
@@ -177,16 +188,23 @@ template <typename T>
 __device__ __forceinline__ uint4 load_chunk(const T* row, int V, int id) {
   constexpr int E = Part<T>::E;
   if (id >= 0 && id + E <= V) return __ldcs(reinterpret_cast<const uint4*>(row + id));
-  uint4 v;
-  T* t = reinterpret_cast<T*>(&v);
+  uint32_t w[4];
+  auto bits = [&](int e) -> uint32_t {
+    const bool in = id + e >= 0 && id + e < V;
+    if constexpr (sizeof(T) == 4) return in ? __float_as_uint(row[id + e]) : 0xff800000u;
+    else return in ? __bfloat16_as_ushort(row[id + e]) : 0xff80u;
+  };
 #pragma unroll
-  for (int e = 0; e < E; ++e) t[e] = id + e >= 0 && id + e < V ? row[id + e] : from_f<T>(-INFINITY);
-  return v;
+  for (int i = 0; i < 4; ++i)
+    w[i] = sizeof(T) == 4 ? bits(i) : bits(2 * i) | bits(2 * i + 1) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// The logits of a chunk in shared memory.  fp32 ones were cleaned on their
-// way in; 16-bit ones have no room for the largest fp32 number.
+// The logits of a chunk in shared memory, as they came: NaN has weight 0, is
+// above and equal to nothing, and falls into the last bin without being asked
+// for; a row with +inf is cleaned in place (16-bit logits have no room for the
+// largest fp32 number: `most` is that, or +inf where the row has none).
 template <typename T>
-__device__ __forceinline__ void chunk_logits(const uint4* p, float (&x)[Part<T>::E]) {
+__device__ __forceinline__ void chunk_logits(const uint4* p, float most, float (&x)[Part<T>::E]) {
   const uint4 v = *p;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -194,9 +212,32 @@ __device__ __forceinline__ void chunk_logits(const uint4* p, float (&x)[Part<T>:
     if constexpr (sizeof(T) == 4) {
       x[i] = __uint_as_float(w[i]);
     } else {
-      x[2 * i] = clean_logit(__uint_as_float(w[i] << 16));
-      x[2 * i + 1] = clean_logit(__uint_as_float(w[i] & 0xffff0000u));
+      x[2 * i] = at_most(__uint_as_float(w[i] << 16), most);
+      x[2 * i + 1] = at_most(__uint_as_float(w[i] & 0xffff0000u), most);
     }
+  }
+}
+
+// One of them (read as the words they were written as).
+template <typename T>
+__device__ __forceinline__ float held_logit(const unsigned char* held, int i, float most) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(held);
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+  else return at_most(__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16), most);
+}
+
+// The largest logit of a chunk, whatever NaN there are (a chunk of NaN: NaN).
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmax3(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)),
+                 __uint_as_float(v.w));
+  } else {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
   }
 }
 
@@ -281,7 +322,7 @@ union Scratch {
   Listed list;
 };
 struct Found {
-  unsigned long long before, inside;
+  unsigned long long before, inside, all;
   int bin;
 };
 struct SampleShared {
@@ -339,7 +380,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   uint4* mine = reinterpret_cast<uint4*>(held);
   Scratch& scr = *reinterpret_cast<Scratch*>(held + static_cast<size_t>(part.per) * 16);
   float top = -INFINITY;
-  constexpr int kFly = 4;  // chunks of a thread on their way
+  constexpr int kFly = 6;  // chunks of a thread on their way
   for (int c0 = tid; c0 < part.chunks; c0 += kFly * kSampleThreads) {
     uint4 v[kFly];
 #pragma unroll
@@ -350,29 +391,34 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     for (int i = 0; i < kFly; ++i) {
       const int c = c0 + i * kSampleThreads;
       if (c >= part.chunks) break;
-      if constexpr (sizeof(T) == 4) {
-        const float4 f = make_float4(
-            clean_logit(__uint_as_float(v[i].x)), clean_logit(__uint_as_float(v[i].y)),
-            clean_logit(__uint_as_float(v[i].z)), clean_logit(__uint_as_float(v[i].w)));
-        reinterpret_cast<float4*>(mine)[c] = f;
-        top = fmaxf(fmaxf(top, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
-      } else {
-        mine[c] = v[i];
-        const T* t = reinterpret_cast<const T*>(&v[i]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) top = fmaxf(top, clean_logit(to_f<T>(t[e])));
-      }
+      mine[c] = v[i];
+      top = fmaxf(top, largest_of<T>(v[i]));
     }
   }
-  unsigned long long x = float_order_key(top), y = 0;
+  unsigned long long x = float_order_key(top + 0.f), y = 0;
   cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
-  const RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
+  RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
+  float most = INFINITY;
+  if (sc.max == INFINITY) {
+    sc.max = most = kLargest;
+    if constexpr (sizeof(T) == 4) {
+      for (int c = tid; c < part.chunks; c += kSampleThreads) {
+        const uint4 v = mine[c];
+        mine[c] = make_uint4(__float_as_uint(at_most(__uint_as_float(v.x), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.y), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.z), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.w), most)));
+      }
+      __syncthreads();
+    }
+  }
 
   // Every element of this CTA, in no order: test(logit, id).
   auto each = [&](auto&& test) {
+#pragma unroll 2
     for (int c = tid; c < part.chunks; c += kSampleThreads) {
       float v[E];
-      chunk_logits<T>(mine + c, v);
+      chunk_logits<T>(mine + c, most, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) test(v[e], c * E + e);
     }
@@ -383,12 +429,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   const Segment seg = warp_segment(part.chunks);
   unsigned long long own = 0;      // kept weight of this warp's segment
   bool summed = false;             // ... and is it there yet
+  unsigned long long best = 0;     // a greedy row's token
   if (sc.max > -INFINITY && greedy) {
     // the lowest id of the largest logit, and whether any other logit is finite
-    unsigned long long best = 0, others = 0;
+    unsigned long long others = 0;
     each([&](float v, int i) {
       if (v == sc.max) {
-        const unsigned long long key = argmax_key(v, part.first + i);
+        const unsigned long long key = token_key(v, part.first + i);
         best = key > best ? key : best;
       }
       others += __fsub_rn(v, sc.max) > -INFINITY;
@@ -405,11 +452,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       last = min(last, at + 2);
     }
     unsigned long long floor_key = 0;
+    bool short_of = false;  // some token of W > 0 is kept by no stage so far
     auto able = [&](float v, float z, int bin, int i) {
       if (bin < sure) return true;
       if (bin > last) return false;
       const float e = expf(z);
-      return weight_of(e) > 0 && e >= min_p && argmax_key(v, part.first + i) >= floor_key;
+      return weight_of(e) > 0 && e >= min_p && token_key(v, part.first + i) >= floor_key;
     };
     // The bin, and within it the range of keys, that a limit falls into, and
     // the measure of what comes before.
@@ -420,7 +468,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
         const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
         const int bin = bin_of(z);
         const int at = place(v, bin, i);
-        if (at < 0 || !able(v, z, bin, i)) return;
+        if (at < 0) return;
+        if (!able(v, z, bin, i)) {
+          short_of = short_of || bin < kSure || weight_of(expf(z)) > 0;
+          return;
+        }
         if (count) {
           atomicAdd(&scr.bins[0][at], 1u);
         } else {
@@ -467,14 +519,16 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
             const uint32_t to = cluster_map_shared(smem_u32(&sh.found), c);
             st_cluster_u64(to, before);
             st_cluster_u64(to + 8, v[j]);
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 16),
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 24),
                          "r"(lo + tid * each_bins + j)
                          : "memory");
           }
         before += v[j];
       }
       cluster_barrier();
-      return sh.found;
+      Found f = sh.found;
+      f.all = all;
+      return f;
     };
     // The last token of `listed` ones before which the measure is below the
     // limit: eight bits of the keys at a time.  Every CTA has the whole list.
@@ -558,6 +612,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       };
       histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
       Found f = search(count, 0, limit);
+      // (weights of what passes sum to more than 0 each, so both measures tell)
+      short_of = short_of || f.before + f.inside < f.all;
       unsigned long long low = 0, high = ~0ull;  // keys within the bin
       int lo_bin = f.bin;
       if (count && f.before + f.inside <= kListed) {
@@ -566,42 +622,34 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       }
       const int hi_bin = f.bin;
       int listed;
-      unsigned long long dropped;
+      unsigned long long dropped;  // somewhere in the range's bin, or short_of
       while (true) {
         // weights before the range, by segments; the range's own tokens
         if (tid == 0) sh.listed = 0;
         __syncthreads();
         own = 0;
-        bool drop = false;
-        unsigned long long least = ~0ull, most = 0;
+        bool drop = short_of;
+        unsigned long long first_key = 0, last_key = ~0ull;
         for (int c = seg.lo + lane; c < seg.hi; c += 32) {
           float v[E];
-          chunk_logits<T>(mine + c, v);
+          chunk_logits<T>(mine + c, most, v);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float z = __fmul_rn(__fsub_rn(v[e], sc.max), sc.inv);
             const int bin = bin_of(z);
-            if (bin >= kBins) continue;
-            if (bin > hi_bin) {
-              drop = drop || bin < kSure || weight_of(expf(z)) > 0;
-              continue;
-            }
-            if (!able(v[e], z, bin, c * E + e)) {
-              drop = drop || bin < kSure || weight_of(expf(z)) > 0;
-              continue;
-            }
+            if (bin > hi_bin || !able(v[e], z, bin, c * E + e)) continue;
             if (bin < lo_bin) {
               own += weight_of(expf(z));
               continue;
             }
-            const unsigned long long key = argmax_key(v[e], part.first + c * E + e);
+            const unsigned long long key = token_key(v[e], part.first + c * E + e);
             if (key > high) {
               own += weight_of(expf(z));
             } else if (key < low) {
               drop = true;
             } else {
-              least = key < least ? key : least;
-              most = key > most ? key : most;
+              last_key = key < last_key ? key : last_key;
+              first_key = key > first_key ? key : first_key;
               const int at = atomicAdd(&sh.listed, 1);
               if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(c * E + e);
             }
@@ -619,10 +667,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
           const int here = static_cast<int>(sh.ex.slot[par][0][rank]);
           for (int i = tid; i < here * cluster; i += kSampleThreads) {
             const int to = i / here, j = i % here, el = scr.list.own[j];
-            const float v = to_f<T>(reinterpret_cast<const T*>(held)[el]);
-            const float xv = sizeof(T) == 4 ? v : clean_logit(v);
+            const float xv = held_logit<T>(held, el, most);
             st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), to),
-                           argmax_key(xv, part.first + el));
+                           token_key(xv, part.first + el));
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
                              cluster_map_shared(smem_u32(&scr.list.w[at + j]), to)),
                          "r"(weight_of(exp_of(xv, sc)))
@@ -632,19 +679,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
           break;
         }
         // too many to rank: bins of the range's keys (ties go by their ids)
-        unsigned long long inverse = ~least;
+        unsigned long long inverse = ~last_key;
         cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, dropped);
         low = ~inverse;
         unsigned long long none = 0;
-        cluster_reduce<true>(sh.ex, parity, cluster, rank, most, none);
-        high = most;
+        cluster_reduce<true>(sh.ex, parity, cluster, rank, first_key, none);
+        high = first_key;
         int shift = 0;
         while (((high - low) >> shift) >= kBins) ++shift;
         lo_bin = hi_bin;  // (the range is that bin's: lists of all bins are short)
         const unsigned long long lowest = low, highest = high;
         histogram(count, [&](float v, int bin, int i) {
           if (bin != hi_bin) return -1;
-          const unsigned long long key = argmax_key(v, part.first + i);
+          const unsigned long long key = token_key(v, part.first + i);
           return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
         });
         f = search(count, f.before, [&](unsigned long long) { return stop; });
@@ -703,20 +750,25 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   // Draw.  A greedy draft that this row may reject has no share.
   const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
   auto weight = [&](int c, int e) -> uint32_t {
-    const T t = reinterpret_cast<const T*>(held)[c * E + e];
-    const float v = sizeof(T) == 4 ? to_f<T>(t) : clean_logit(to_f<T>(t));
+    const float v = held_logit<T>(held, c * E + e, most);
     const int id = part.first + c * E + e;
     if (!is_kept(v, id, cut, cut_token) || id == left_out) return 0;
     return weight_of(exp_of(v, sc));
   };
   if (!summed) {
+    // every token, or a greedy row's one
     own = 0;
-    for (int c = seg.lo + lane; c < seg.hi; c += 32) {
-      float v[E];
-      chunk_logits<T>(mine + c, v);
+    if (!greedy) {
+#pragma unroll 2
+      for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+        float v[E];
+        chunk_logits<T>(mine + c, most, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (is_kept(v[e], part.first + c * E + e, cut, cut_token)) own += weight_of(exp_of(v[e], sc));
+        for (int e = 0; e < E; ++e) own += weight_of(exp_of(v[e], sc));
+      }
+    } else if (sc.max > -INFINITY && part.owner(argmax_key_index(best)) == rank) {
+      const int at = (argmax_key_index(best) - part.first) / E;
+      if (at / warp_segment_size(part.chunks) == warp && lane == 0) own = weight_of(1.f);
     }
     own = warp_sum_u64(own);
     if (lane == 0) sh.warp_mass[warp] = own;
