@@ -6,6 +6,7 @@
 // counts and sums of them are exact in 64 bits, whatever order the threads,
 // warps and CTAs add them in.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "../../include/peagle_sample.h"
@@ -126,43 +127,51 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
 }
 
 struct Exchange {
-  unsigned long long warp[2][kSampleWarps];
-  unsigned long long slot[2][2][kMostCluster];  // [parity][value][CTA]
+  unsigned long long warp[3][kSampleWarps];
+  unsigned long long slot[2][3][kMostCluster];  // [parity][value][CTA]
 };
 
-// Two 64-bit sums (or a maximum and a sum) over the cluster; every thread gets
-// them.  The CTAs' own first sums stay in ex.slot[parity][0].  One barrier:
-// the slots of the round before the last are free, because whoever has passed
-// the last barrier has read them.
+// Three 64-bit sums (or a maximum and two sums) over the cluster; every thread
+// gets them.  The CTAs' own values stay in ex.slot[parity].  One barrier: the
+// slots of the round before the last are free, because whoever has passed the
+// last barrier has read them.
 template <bool MAX>
 __device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cluster, int rank,
-                                               unsigned long long& a, unsigned long long& b) {
+                                               unsigned long long& a, unsigned long long& b,
+                                               unsigned long long& c) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   a = MAX ? warp_max_u64(a) : warp_sum_u64(a);
   b = warp_sum_u64(b);
+  c = warp_sum_u64(c);
   if (lane == 0) {
     ex.warp[0][warp] = a;
     ex.warp[1][warp] = b;
+    ex.warp[2][warp] = c;
   }
   __syncthreads();
-  if (warp == 0) {
-    unsigned long long x = lane < kSampleWarps ? ex.warp[0][lane] : 0;
-    unsigned long long y = lane < kSampleWarps ? ex.warp[1][lane] : 0;
-    x = MAX ? warp_max_u64(x) : warp_sum_u64(x);
-    y = warp_sum_u64(y);
-    if (lane < cluster) {
-      st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][0][rank]), lane), x);
-      st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][1][rank]), lane), y);
-    }
+  if (warp < 3) {  // a warp a value
+    unsigned long long x = lane < kSampleWarps ? ex.warp[warp][lane] : 0;
+    x = MAX && warp == 0 ? warp_max_u64(x) : warp_sum_u64(x);
+    if (lane < cluster)
+      st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][warp][rank]), lane), x);
   }
   cluster_barrier();
-  a = b = 0;
-  for (int r = 0; r < cluster; ++r) {
+  a = b = c = 0;
+#pragma unroll
+  for (int r = 0; r < kMostCluster; ++r) {
+    if (r >= cluster) break;
     const unsigned long long x = ex.slot[parity][0][r];
     a = MAX ? (x > a ? x : a) : a + x;
     b += ex.slot[parity][1][r];
+    c += ex.slot[parity][2][r];
   }
   parity ^= 1;
+}
+template <bool MAX>
+__device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cluster, int rank,
+                                               unsigned long long& a, unsigned long long& b) {
+  unsigned long long c = 0;
+  cluster_reduce<MAX>(ex, parity, cluster, rank, a, b, c);
 }
 
 // A CTA's part of a row: 16-byte chunks of the memory that the row lies in;
@@ -304,9 +313,9 @@ constexpr int kPerOctave = 48;
 constexpr int kSure = 32 * kPerOctave - 1;
 constexpr int kBins = 32 * kPerOctave + 4;
 __device__ __forceinline__ int bin_of(float z) {
-  // 8388608 + n has the bits 0x4B000000 + n
+  // 8388608 + n has the bits 0x4B000000 + n, a larger or no number larger ones
   const float f = fmaf(z, -69.24936196f, 8388608.f);  // 48 / ln 2
-  return __float_as_int(fminf(f, 8388608.f + kBins)) - 0x4B000000;
+  return static_cast<int>(min(__float_as_uint(f) - 0x4B000000u, static_cast<uint32_t>(kBins)));
 }
 
 // Tokens that are ranked one by one, from all CTAs of the cluster.
@@ -334,6 +343,125 @@ struct SampleShared {
   int digit, listed;
 };
 
+// Tokens that top-p takes at the first try, and the most for which the threads'
+// largest logits are asked.
+constexpr int kGuess = 128;
+constexpr int kMostGuess = 256;
+
+// A row's result.
+__device__ __forceinline__ void store_row(const SampleArgs& a, bool verify, int r, RowScale sc,
+                                          unsigned long long border, long long all, int token,
+                                          float logprob) {
+  if (!verify) {
+    a.tokens[r] = token;
+    if (a.logprobs) a.logprobs[r] = logprob;
+  }
+  if (a.dist) {
+    const float cut = border ? key_float(static_cast<uint32_t>(border >> 32)) : -INFINITY;
+    const int cut_token = border ? argmax_key_index(border) : a.V - 1;
+    uint4* d = reinterpret_cast<uint4*>(a.dist + r);
+    d[0] = make_uint4(__float_as_uint(sc.max), __float_as_uint(sc.inv), __float_as_uint(cut),
+                      static_cast<uint32_t>(cut_token));
+    d[1] = make_uint4(static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32),
+                      static_cast<uint32_t>(token), 0u);
+  }
+}
+
+// A row whose kept tokens are all listed: `first` of the n listed ones pass
+// top-k, and of their weight top-p takes p (without top-k: of the row's, that
+// is up to `stop`).  By one CTA: every token's place and the weight before it
+// from a comparison with every other, several threads a token where there are
+// few.
+struct ListRow {
+  int n, first;
+  bool by_count, by_mass, rest;  // rest: tokens of W > 0 are not listed
+  double p, stop;
+};
+template <typename T, bool VERIFY>
+__device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& sh, Listed& list,
+                                            const ListRow& lr, RowScale sc, int r, int q,
+                                            const T* row, int left_out, bool no_draw) {
+  constexpr int kEach = (kListed + kSampleThreads - 1) / kSampleThreads;
+  const int tid = threadIdx.x, n = lr.n;
+  __syncwarp();
+  const int per = n <= kSampleThreads / 8   ? 8
+                  : n <= kSampleThreads / 4 ? 4
+                  : n <= kSampleThreads / 2 ? 2
+                                            : 1;  // threads a token
+  const int mine = tid / per, part = tid % per;
+  unsigned long long key[kEach], before[kEach];
+  uint32_t w[kEach], place[kEach];
+#pragma unroll
+  for (int s = 0; s < kEach; ++s) {
+    const int i = mine + s * kSampleThreads;
+    key[s] = i < n ? list.key[i] : 0;
+    w[s] = i < n ? list.w[i] : 0;
+    before[s] = place[s] = 0;
+    if (i < n)
+      for (int j = part; j < n; j += per)
+        if (list.key[j] > key[s]) {
+          ++place[s];
+          before[s] += list.w[j];
+        }
+    for (int m = 1; m < per; m <<= 1) {
+      place[s] += __shfl_xor_sync(0xffffffffu, place[s], m);
+      before[s] += __shfl_xor_sync(0xffffffffu, before[s], m);
+    }
+  }
+  double stop = lr.stop;
+  if (lr.by_count && lr.by_mass) {
+#pragma unroll
+    for (int s = 0; s < kEach; ++s)
+      if (w[s] && place[s] + 1 == lr.first) sh.scan[0] = before[s] + w[s];
+    __syncthreads();
+    stop = __dmul_rn(lr.p, static_cast<double>(sh.scan[0]));
+  }
+  int kept = 0;
+#pragma unroll
+  for (int s = 0; s < kEach; ++s)
+    kept += __syncthreads_count(
+        w[s] && part == 0 && place[s] < lr.first &&
+        (!lr.by_mass || place[s] == 0 || static_cast<double>(before[s]) < stop));
+#pragma unroll
+  for (int s = 0; s < kEach; ++s)
+    if (w[s] && part == 0 && place[s] + 1 == kept) {
+      sh.found.before = key[s];
+      sh.found.inside = before[s] + w[s];
+    }
+  __syncthreads();
+  const unsigned long long last = sh.found.before, border = kept < n || lr.rest ? last : 0;
+  const long long all = static_cast<long long>(sh.found.inside);
+  long long share = all;
+  if (left_out >= 0) {
+    const float x = raw_logit(row + left_out);
+    if (token_key(x, left_out) >= last) share -= weight_of(exp_of(x, sc));
+  }
+  if (share <= 0 || no_draw) {
+    if (tid == 0) store_row(a, VERIFY, r, sc, border, all, -1, -INFINITY);
+    return;
+  }
+  // the kept weight of lower ids (a key's low half falls as the id grows)
+  const unsigned long long at = static_cast<unsigned long long>(place_of(a.u[q], share));
+#pragma unroll
+  for (int s = 0; s < kEach; ++s) {
+    const bool in = w[s] && key[s] >= last && argmax_key_index(key[s]) != left_out;
+    unsigned long long lower = 0;
+    if (in)
+      for (int j = part; j < n; j += per) {
+        const unsigned long long other = list.key[j];
+        if (other >= last && static_cast<uint32_t>(other) > static_cast<uint32_t>(key[s]) &&
+            argmax_key_index(other) != left_out)
+          lower += list.w[j];
+      }
+    for (int m = 1; m < per; m <<= 1) lower += __shfl_xor_sync(0xffffffffu, lower, m);
+    if (in && part == 0 && at >= lower && at - lower < w[s]) {
+      const int token = argmax_key_index(key[s]);
+      store_row(a, VERIFY, r, sc, border, all, token,
+                VERIFY ? 0.f : logprob_of(raw_logit(row + token), sc, all));
+    }
+  }
+}
+
 template <typename T, bool VERIFY>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
@@ -341,11 +469,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   __shared__ SampleShared sh;
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int cluster = a.cluster, rank = cluster_ctarank(), r = blockIdx.x / cluster;
+  const int cluster = a.cluster, rank = cluster_ctarank();
   int parity = 0;
+  cluster_barrier();  // no CTA's shared memory is written to before it has started
   grid_dep_wait();
   grid_dep_launch();
-
+  const int step = gridDim.x / cluster;
+  for (int r = blockIdx.x / cluster; r < a.rows; r += step) {
+  __syncthreads();  // whoever still reads the row before
   // the row's request, its filters, and the draft that it judges
   int q = r, draft = -1;
   bool judges = false;
@@ -358,7 +489,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     }
     q = lo;
     const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
-    if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) return;  // the whole cluster
+    if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) continue;  // the whole cluster
     judges = r + 1 < w1;
     draft = judges ? a.ids[r + 1] : -1;
   }
@@ -394,6 +525,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       mine[c] = v[i];
       top = fmaxf(top, largest_of<T>(v[i]));
     }
+  }
+  // the next row of this cluster on its way to L2
+  if (warp == 0 && r + step < a.rows) {
+    const T* next = row + step * a.stride;
+    const Part<T> np = part_of(next, a.V, cluster, rank);
+    const int skip = np.first < 0 ? 1 : 0;  // chunks that are the row's alone
+    const int whole = np.chunks - skip - (np.first + np.chunks * E > a.V ? 1 : 0);
+    const int lo = skip + whole * lane / 32, hi = skip + whole * (lane + 1) / 32;
+    if (hi > lo && whole > 0) prefetch_l2(next + np.first + lo * E, (hi - lo) * 16u);
   }
   unsigned long long x = float_order_key(top + 0.f), y = 0;
   cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
@@ -459,11 +599,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       const float e = expf(z);
       return weight_of(e) > 0 && e >= min_p && token_key(v, part.first + i) >= floor_key;
     };
+    auto clear_bins = [&]() {
+      for (int i = tid; i < kBins; i += kSampleThreads) scr.bins[0][i] = scr.bins[1][i] = 0;
+      __syncthreads();
+    };
     // The bin, and within it the range of keys, that a limit falls into, and
     // the measure of what comes before.
     auto histogram = [&](bool count, auto&& place) {
-      for (int i = tid; i < kBins; i += kSampleThreads) scr.bins[0][i] = scr.bins[1][i] = 0;
-      __syncthreads();
+      clear_bins();
       each([&](float v, int i) {
         const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
         const int bin = bin_of(z);
@@ -495,10 +638,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
         v[j] = 0;
         const int at = tid * each_bins + j;
         if (j < each_bins && at < share && lo + at < kBins) {
-          for (int c = 0; c < cluster; ++c) {
-            const uint32_t* from = cluster_pointer(&scr.bins[0][lo + at], c);
-            v[j] += from[0] + (static_cast<unsigned long long>(from[kBins]) << 16);
-          }
+          uint32_t l[kMostCluster] = {}, h[kMostCluster] = {};
+#pragma unroll
+          for (int c = 0; c < kMostCluster; ++c)
+            if (c < cluster) {
+              const uint32_t* from = cluster_pointer(&scr.bins[0][lo + at], c);
+              l[c] = from[0];
+              if (!count) h[c] = from[kBins];
+            }
+#pragma unroll
+          for (int c = 0; c < kMostCluster; ++c)
+            v[j] += l[c] + (static_cast<unsigned long long>(h[c]) << 16);
         }
         sum += v[j];
       }
@@ -601,14 +751,115 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       return result;
     };
 
-    // by number (top-k, min-p), by weight (top-p), or one after the other
-    for (int stage = by_count || !by_mass ? 0 : 1; stage < (by_mass ? 2 : 1); ++stage) {
+    // Where the filters keep few tokens, they are all among a few.  Of at
+    // least `guess` threads the largest logit is in the bin that is found, or
+    // before it, so at least as many tokens are.
+    const int guess = by_count ? k : kGuess;
+    bool done = false;
+    if (!by_count && !by_mass) {
+      // min-p alone: a look at each token is enough
+      own = 0;
+      unsigned long long last_key = ~0ull, short_n = 0;
+      for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+        float v[E];
+        chunk_logits<T>(mine + c, most, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float z = __fmul_rn(__fsub_rn(v[e], sc.max), sc.inv);
+          const int bin = bin_of(z);
+          if (bin >= kBins) continue;
+          if (able(v[e], z, bin, c * E + e)) {
+            own += weight_of(expf(z));
+            const unsigned long long key = token_key(v[e], part.first + c * E + e);
+            last_key = key < last_key ? key : last_key;
+          } else {
+            short_n |= bin < kSure || weight_of(expf(z)) > 0;
+          }
+        }
+      }
+      own = warp_sum_u64(own);
+      if (lane == 0) sh.warp_mass[warp] = own;
+      unsigned long long inverse = ~last_key;
+      cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, short_n);
+      border = short_n ? ~inverse : 0;
+      done = summed = true;
+    } else if (guess <= kMostGuess) {
+      clear_bins();
+      if (tid == 0) sh.listed = 0;
+      const float tv = at_most(top, most), tz = __fmul_rn(__fsub_rn(tv, sc.max), sc.inv);
+      const int tb = bin_of(tz);
+      if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[0][tb], 1u);
+      cluster_barrier();
+      const Found f = search(true, 0, [&](unsigned long long all) {
+        return fmin(static_cast<double>(guess), static_cast<double>(all));
+      });
+      const int hi_bin = f.all < guess ? kBins - 1 : f.bin;
+      unsigned long long n = 0, mass = 0, list_mass = 0;
+      bool rest = false;
+      each([&](float v, int i) {
+        const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
+        const int bin = bin_of(z);
+        if (bin > hi_bin && by_count) {
+          rest = rest || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
+          return;
+        }
+        if (bin >= kBins) return;
+        const uint32_t w = weight_of(expf(z));
+        if (!able(v, z, bin, i)) {
+          rest = rest || w > 0;
+          return;
+        }
+        mass += w;
+        if (bin > hi_bin) {
+          rest = rest || w > 0;
+          return;
+        }
+        list_mass += w;
+        const int at = atomicAdd(&sh.listed, 1);
+        if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(i);
+      });
+      __syncthreads();
+      n = (tid == 0 ? static_cast<unsigned>(sh.listed) : 0u) | (rest ? 1ull << 32 : 0ull);
+      const int par = parity;
+      cluster_reduce<false>(sh.ex, parity, cluster, rank, n, mass, list_mass);
+      const int listed = static_cast<int>(n & 0xffffffffu);
+      rest = n >> 32;
+      const double stop = __dmul_rn(static_cast<double>(p), static_cast<double>(mass));
+      if (listed <= kListed && (by_count || !(static_cast<double>(list_mass) < stop))) {
+        // everything that is kept is listed: the first CTA does the rest, and
+        // the others go on
+        int at = 0;
+        for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i] & 0xffffffffu);
+        const int here = static_cast<int>(sh.ex.slot[par][0][rank] & 0xffffffffu);
+        for (int j = tid; j < here; j += kSampleThreads) {
+          const int el = scr.list.own[j];
+          const float xv = held_logit<T>(held, el, most);
+          st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), 0),
+                         token_key(xv, part.first + el));
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                           cluster_map_shared(smem_u32(&scr.list.w[at + j]), 0)),
+                       "r"(weight_of(exp_of(xv, sc)))
+                       : "memory");
+        }
+        cluster_barrier();
+        if (rank == 0) {
+          const ListRow lr = {listed, by_count ? min(k, listed) : listed, by_count, by_mass,
+                              rest,   static_cast<double>(p),            stop};
+          const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
+          draw_from_list<T, VERIFY>(a, sh, scr.list, lr, sc, r, q, row, left_out,
+                                    VERIFY && judges && !a.greedy_drafts);
+        }
+        continue;
+      }
+    }
+
+    // by number (top-k), by weight (top-p), or one after the other
+    for (int stage = by_count ? 0 : 1; stage < (by_mass ? 2 : 1) && !done; ++stage) {
       const bool count = stage == 0;
-      const double want = by_count ? static_cast<double>(k) : 9e15;
       double stop = 0.0;
       auto limit = [&](unsigned long long all) {
         const double n = static_cast<double>(all);
-        return stop = count ? fmin(want, n) : __dmul_rn(static_cast<double>(p), n);
+        return stop = count ? fmin(static_cast<double>(k), n) : __dmul_rn(static_cast<double>(p), n);
       };
       histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
       Found f = search(count, 0, limit);
@@ -623,7 +874,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       const int hi_bin = f.bin;
       int listed;
       unsigned long long dropped;  // somewhere in the range's bin, or short_of
-      while (true) {
+      // (each further level has 2^-10 of the keys of the one before, of 2^64)
+      for (int level = 0; level < 8; ++level) {
         // weights before the range, by segments; the range's own tokens
         if (tid == 0) sh.listed = 0;
         __syncthreads();
@@ -686,7 +938,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
         cluster_reduce<true>(sh.ex, parity, cluster, rank, first_key, none);
         high = first_key;
         int shift = 0;
-        while (((high - low) >> shift) >= kBins) ++shift;
+        while (shift < 54 && ((high - low) >> shift) >= kBins) ++shift;
         lo_bin = hi_bin;  // (the range is that bin's: lists of all bins are short)
         const unsigned long long lowest = low, highest = high;
         histogram(count, [&](float v, int bin, int i) {
@@ -699,6 +951,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
         const unsigned long long end = high - ((1ull << shift) - 1);
         low = end > lowest && end <= high ? end : lowest;
       }
+      listed = min(listed, kListed);
       border = select(listed, count, f.before, stop, 0);
       if (count && by_mass && lo_bin == 0 && listed <= kListed && hi_bin == f.bin && high == ~0ull) {
         // all that is left is in the list: the weights' limit in it
@@ -798,19 +1051,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       if (i >= 0) token = part.first + i;
     }
   }
-  if (token >= 0 || (!draws && rank == 0 && tid == 0)) {
-    if (!VERIFY) {
-      a.tokens[r] = token;
-      if (a.logprobs)
-        a.logprobs[r] = token >= 0 ? logprob_of(raw_logit(row + token), sc, all) : -INFINITY;
-    }
-    if (a.dist) {
-      uint4* d = reinterpret_cast<uint4*>(a.dist + r);
-      d[0] = make_uint4(__float_as_uint(sc.max), __float_as_uint(inv), __float_as_uint(cut),
-                        static_cast<uint32_t>(cut_token));
-      d[1] = make_uint4(static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32),
-                        static_cast<uint32_t>(token), 0u);
-    }
+  if (token >= 0 || (!draws && rank == 0 && tid == 0))
+    store_row(a, VERIFY, r, sc, border, all, token,
+              token >= 0 && !VERIFY ? logprob_of(raw_logit(row + token), sc, all) : -INFINITY);
   }
 }
 
@@ -826,12 +1069,14 @@ __device__ __forceinline__ uint32_t dist_weight(float x, int id, const pe_dist& 
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
     const __grid_constant__ VerifyArgs a) {
+  extern __shared__ __align__(16) unsigned char held_weights[];
   __shared__ Exchange ex;
   __shared__ unsigned long long warp_mass[2][kSampleWarps];
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int cluster = a.cluster, rank = cluster_ctarank(), r = blockIdx.x / cluster;
   int parity = 0;
+  cluster_barrier();  // no CTA's shared memory is written to before it has started
   grid_dep_wait();
   grid_dep_launch();
   const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1], drafts = a.T - a.B;
@@ -891,27 +1136,50 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
     const float aq =
         Q.total > 0 ? static_cast<float>(2147483648.0 / static_cast<double>(Q.total)) : 0.f;
     const Part<T> part = part_of(row, a.V, cluster, rank);
-    auto weights = [&](int c, int e, uint32_t& more, uint32_t& plain) {
-      const int id = part.first + c * E + e;
-      more = plain = 0;
-      if (id < 0 || id >= a.V) return;
-      const float pw = __fmul_rn(
-          static_cast<float>(dist_weight<T>(raw_logit(row + id), id, P)), ap);
-      const float qw = __fmul_rn(
-          static_cast<float>(dist_weight<T>(raw_logit(qrow + id), id, Q)), aq);
-      plain = __float2uint_rn(pw);
-      more = __float2uint_rn(fmaxf(__fsub_rn(pw, qw), 0.f));
+    // the drafter's row beside it: 16 bytes at a time where they lie alike
+    const bool alike = (reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(qrow)) % 16 == 0;
+    uint32_t* held = reinterpret_cast<uint32_t*>(held_weights);
+    const RowScale ps = {P.max, P.inv}, qs = {Q.max, Q.inv};
+    auto weights_of = [&](float x, float y, int id, uint32_t& m, uint32_t& n) {
+      const uint32_t wp = is_kept(x, id, P.cut, P.cut_token) ? weight_of(exp_of(x, ps)) : 0u;
+      const uint32_t wq = is_kept(y, id, Q.cut, Q.cut_token) ? weight_of(exp_of(y, qs)) : 0u;
+      const float pw = __fmul_rn(static_cast<float>(wp), ap);
+      n = __float2uint_rn(pw);
+      m = __float2uint_rn(fmaxf(__fsub_rn(pw, __fmul_rn(static_cast<float>(wq), aq)), 0.f));
     };
     const Segment seg = warp_segment(part.chunks);
     unsigned long long more = 0, plain = 0;
-    for (int c = seg.lo + lane; c < seg.hi; c += 32)
+#pragma unroll 2
+    for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+      const int first = part.first + c * E;
+      const uint4 pv = load_chunk(row, a.V, first);
+      uint4 qv;
+      if (alike) {
+        qv = load_chunk(qrow, a.V, first);
+      } else {
+        uint32_t w[4];
+        auto bits = [&](int e) -> uint32_t {
+          const bool in = first + e >= 0 && first + e < a.V;
+          if constexpr (sizeof(T) == 4) return in ? __float_as_uint(qrow[first + e]) : 0xff800000u;
+          else return in ? __bfloat16_as_ushort(qrow[first + e]) : 0xff80u;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = sizeof(T) == 4 ? bits(i) : bits(2 * i) | bits(2 * i + 1) << 16;
+        qv = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      float px[E], qx[E];
+      chunk_logits<T>(&pv, INFINITY, px);
+      chunk_logits<T>(&qv, INFINITY, qx);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         uint32_t m, n;
-        weights(c, e, m, n);
+        weights_of(clean_logit(px[e]), clean_logit(qx[e]), first + e, m, n);
+        held[c * E + e] = m;
         more += m;
         plain += n;
       }
+    }
     unsigned long long total_more = more, total_plain = plain;
     more = warp_sum_u64(more);
     plain = warp_sum_u64(plain);
@@ -930,9 +1198,11 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
     for (int i = 0; i < warp; ++i) at -= static_cast<long long>(warp_mass[use][i]);
     if (at >= 0 && at < own) {
       const int i = find_in_segment<E>(seg, at, [&](int c, int e) {
-        uint32_t m, n;
-        weights(c, e, m, n);
-        return use ? n : m;
+        if (!use) return held[c * E + e];
+        const int id = part.first + c * E + e;
+        uint32_t m = 0, n = 0;
+        if (id >= 0 && id < a.V) weights_of(raw_logit(row + id), raw_logit(qrow + id), id, m, n);
+        return n;
       });
       if (i >= 0) token = part.first + i;
       writes = token >= 0;
@@ -966,6 +1236,9 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
 }
 
 // -------------------------------------------------------------------- launch
+// Two CTAs an SM, or one.
+constexpr size_t kHalfShared = 112 * 1024 - sizeof(SampleShared);
+constexpr size_t kMostShared = 226 * 1024 - sizeof(SampleShared);
 struct SampleShape {
   int cluster;
   size_t smem;
@@ -973,29 +1246,77 @@ struct SampleShape {
 // Few rows: as many CTAs a row as a cluster has, for the shortest way; more
 // rows than that fills: as few as hold the row.
 static SampleShape sample_shape(int rows, int V, int elem, int sms) {
-  constexpr size_t kHalf = 113 * 1024 - sizeof(SampleShared);
   auto bytes = [&](int c) {
     const int e = 16 / elem, all = (V + 2 * (e - 1)) / e;
     return static_cast<size_t>((all + c - 1) / c) * 16 + sizeof(Scratch);
   };
   int c = 1;
-  while (c < kMostCluster && bytes(c) > kHalf) c *= 2;
+  while (c < kMostCluster && bytes(c) > kHalfShared) c *= 2;
   while (c < kMostCluster && static_cast<long long>(rows) * c * 2 <= 2 * sms &&
          bytes(c) > sizeof(Scratch) + 4096)
     c *= 2;
   return SampleShape{c, bytes(c)};
 }
 
+// Clusters that are resident at a time (a GPC's SMs need not be a multiple of
+// the cluster).  Asked once a process, device and shape.
+template <typename T, bool VERIFY>
+static cudaError_t resident_rows(const SampleShape& sh, int& n) {
+  static std::atomic<int> known[16][4][2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int c = sh.cluster == 1 ? 0 : sh.cluster == 2 ? 1 : sh.cluster == 4 ? 2 : 3;
+  std::atomic<int>* place =
+      dev < 16 ? &known[dev][c][sh.smem > kHalfShared ? 1 : 0] : nullptr;
+  n = place ? place->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return cudaSuccess;
+  auto kernel = sample_rows_kernel<T, VERIFY>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kMostShared));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sh.cluster);
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = sh.smem > kHalfShared ? kMostShared : kHalfShared;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = sh.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && place) place->store(n, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename T, bool VERIFY>
 static cudaError_t launch_rows(SampleArgs a, int sms, cudaStream_t s) {
   const SampleShape sh = sample_shape(a.rows, a.V, sizeof(T), sms);
   a.cluster = sh.cluster;
-  auto kernel = sample_rows_kernel<T, VERIFY>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sh.smem));
+  int resident = 0;
+  cudaError_t e = resident_rows<T, VERIFY>(sh, resident);  // (opts into the shared memory, too)
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.rows) * sh.cluster),
+  return launch_pdl_cluster(sample_rows_kernel<T, VERIFY>,
+                            dim3(static_cast<unsigned>(std::min(a.rows, resident)) * sh.cluster),
                             dim3(kSampleThreads), sh.smem, s, sh.cluster, a);
+}
+
+template <typename T>
+static cudaError_t launch_verify(VerifyArgs v, cudaStream_t s) {
+  // greedy drafts: nothing is left to add up
+  v.cluster = v.draft_logits ? kMostCluster : 1;
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const size_t smem =
+      v.draft_logits ? static_cast<size_t>((v.V + 2 * (E - 1)) / E + v.cluster - 1) / v.cluster * E * 4 : 0;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        verify_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl_cluster(verify_kernel<T>, dim3(static_cast<unsigned>(v.B) * v.cluster),
+                            dim3(kSampleThreads), smem, s, v.cluster, v);
 }
 
 static cudaError_t sm_count(int& sms) {
@@ -1102,11 +1423,7 @@ extern "C" pe_status pe_verify(int32_t B, int32_t T, int32_t vocab, int32_t dtyp
   if (e == cudaSuccess)
     e = f32 ? launch_rows<float, true>(a, sms, s) : launch_rows<bf16, true>(a, sms, s);
   if (e == cudaSuccess) {
-    // greedy drafts: nothing is left to add up
-    v.cluster = draft_logits ? kMostCluster : 1;
-    const dim3 grid(static_cast<unsigned>(B) * v.cluster);
-    e = f32 ? launch_pdl_cluster(verify_kernel<float>, grid, dim3(kSampleThreads), 0, s, v.cluster, v)
-            : launch_pdl_cluster(verify_kernel<bf16>, grid, dim3(kSampleThreads), 0, s, v.cluster, v);
+    e = f32 ? launch_verify<float>(v, s) : launch_verify<bf16>(v, s);
   }
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
