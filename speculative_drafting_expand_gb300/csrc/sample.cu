@@ -228,30 +228,43 @@ __device__ __forceinline__ void chunk_logits(const uint4& v, float most, float (
     }
   }
 }
-// Chunks from, from + step, .. below `to` of a CTA's part, FLY of them on their
-// way at a time, those at the row's ends last: f(chunk's words, chunk).
-template <int FLY, typename T, typename F>
-__device__ __forceinline__ void each_chunk(const T* row, int V, const Part<T>& part, int from,
-                                           int step, int to, F&& f) {
+// Chunks from, from + step, .. below `to` of a CTA's part: f(chunk's words,
+// chunk).  A thread's chunks come through a ring of its own in shared memory,
+// by asynchronous copies, so that many are on their way in a loop that stays
+// short.
+constexpr int kRing = 4;
+constexpr size_t kRingBytes = static_cast<size_t>(kRing) * kSampleThreads * 16;
+template <typename T, typename F>
+__device__ __forceinline__ void each_chunk(uint4* ring, const T* row, int V, const Part<T>& part,
+                                           int from, int step, int to, F&& f) {
   constexpr int E = Part<T>::E;
+  uint4* mine = ring + threadIdx.x;
+  const uint32_t first_slot = smem_u32(mine), last_slot = first_slot + (kRing - 1) * kSampleThreads * 16;
+  uint32_t fill = first_slot;
+  int ahead = from;
   const int hi = min(to, part.hi);
-  for (int c0 = from; c0 < hi; c0 += FLY * step) {
-    uint4 v[FLY];
+  auto fetch = [&]() {
+    if (ahead >= part.lo && ahead < hi)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(fill),
+                   "l"(row + part.first + ahead * E)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += step;
+    fill = fill == last_slot ? first_slot : fill + kSampleThreads * 16;
+  };
 #pragma unroll
-    for (int i = 0; i < FLY; ++i) {
-      const int c = c0 + i * step;
-      if (c >= part.lo && c < hi) v[i] = load_whole(row, part.first + c * E);
-    }
-#pragma unroll
-    for (int i = 0; i < FLY; ++i) {
-      const int c = c0 + i * step;
-      if (c >= part.lo && c < hi) f(v[i], c);
-    }
+  for (int i = 0; i < kRing - 1; ++i) fetch();
+  int slot = 0;
+#pragma unroll 1
+  for (int c = from; c < to; c += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    uint4 v = mine[slot * kSampleThreads];
+    slot = (slot + 1) % kRing;
+    fetch();  // into the place before this one
+    if (c < part.lo || c >= part.hi) v = load_ragged(row, V, part.first + c * E);
+    f(v, c);
   }
-  // at most two a row: the first chunk and the last
-  for (int c = 0; c < part.chunks; c += max(part.chunks - 1, 1))
-    if ((c < part.lo || c >= part.hi) && c >= from && c < to && (c - from) % step == 0)
-      f(load_ragged(row, V, part.first + c * E), c);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The largest logit of a chunk, whatever NaN there are (a chunk of NaN: NaN).
@@ -282,8 +295,8 @@ __device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v
 // A warp's contiguous chunks of a CTA's part, and groups of them: sums over
 // warps and groups are in the order of the ids, and one group is looked at
 // again to find a token.  Rows of few chunks have groups of one round of a
-// warp's loads, others of four.
-constexpr int kRounds = 4;
+// warp's loads, others of eight.
+constexpr int kRounds = 8;
 constexpr int kMostGroups = 64;  // of a warp: 2^17 fp32 logits in all
 struct Segment {
   int lo, hi, rounds, per;
@@ -294,29 +307,33 @@ __device__ __forceinline__ Segment warp_segment(int chunks) {
   const int lo = min(static_cast<int>(threadIdx.x) / 32 * per, chunks);
   return Segment{lo, min(lo + per, chunks), rounds, per};
 }
-// Sums of a warp's groups into groups[], weight(x, id of the chunk's first
-// element, e) of each element; every lane gets the sum of all.
+// Sums of a warp's groups into groups[], weight(x, place of the element) of each
+// element; every lane gets the sum of all.
 template <typename T, typename W>
-__device__ __forceinline__ unsigned long long sum_groups(const T* row, int V, const Part<T>& part,
-                                                         const Segment& seg, float most,
-                                                         unsigned long long* groups, W&& weight) {
+__device__ __forceinline__ unsigned long long sum_groups(uint4* ring, const T* row, int V,
+                                                         const Part<T>& part, const Segment& seg,
+                                                         float most, unsigned long long* groups,
+                                                         W&& weight) {
   constexpr int E = Part<T>::E;
   const int lane = threadIdx.x % 32;
-  unsigned long long all = 0;
-  int n = 0;
-  for (int c0 = seg.lo; c0 < seg.hi; c0 += 32 * seg.rounds, ++n) {
-    unsigned long long own = 0;
-    each_chunk<kRounds>(row, V, part, c0 + lane, 32, min(c0 + 32 * seg.rounds, seg.hi),
-                        [&](const uint4& v, int c) {
-                          float x[E];
-                          chunk_logits<T>(v, most, x);
+  unsigned long long all = 0, own = 0;
+  int round = 0;
+  // (every lane takes part in a group's sum: chunks past the end weigh nothing)
+  const int end = seg.lo + (seg.hi - seg.lo + 31) / 32 * 32;
+  each_chunk(ring, row, V, part, seg.lo + lane, 32, end, [&](const uint4& v, int c) {
+    if (c < seg.hi) {
+      float x[E];
+      chunk_logits<T>(v, most, x);
 #pragma unroll
-                          for (int e = 0; e < E; ++e) own += weight(x[e], c * E + e);
-                        });
-    own = warp_sum_u64(own);
-    if (lane == 0) groups[n] = own;
-    all += own;
-  }
+      for (int e = 0; e < E; ++e) own += weight(x[e], c * E + e);
+    }
+    if (++round % seg.rounds == 0 || c - lane + 32 >= end) {
+      own = warp_sum_u64(own);
+      if (lane == 0) groups[(round - 1) / seg.rounds] = own;
+      all += own;
+      own = 0;
+    }
+  });
   return all;
 }
 // The element at which a warp's weights, in order, first exceed `at`: the group
@@ -345,46 +362,37 @@ __device__ __forceinline__ int find_in_groups(const T* row, int V, const Part<T>
     group = g0 + who;
   }
   if (group < 0) return -1;  // not reached: the sums agree
-  const int c0 = seg.lo + group * 32 * seg.rounds;
-  int found = -1;
-  uint4 v[kRounds];
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i)
-    if (i < seg.rounds && c0 + i * 32 + lane < seg.hi)
-    {
-      const int c = c0 + i * 32 + lane;
-      v[i] = c >= part.lo && c < part.hi ? load_whole(row, part.first + c * E)
-                                         : load_ragged(row, V, part.first + c * E);
-    }
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int c = c0 + i * 32 + lane;
-    uint32_t w[E];
+#pragma unroll 1
+  for (int i = 0; i < seg.rounds; ++i) {
+    const int c = seg.lo + (group * seg.rounds + i) * 32 + lane;
+    uint32_t w[E] = {};
     unsigned long long own = 0;
-    if (i < seg.rounds && c < seg.hi) {
+    if (c < seg.hi) {
       float x[E];
-      chunk_logits<T>(v[i], most, x);
+      chunk_logits<T>(c >= part.lo && c < part.hi ? load_whole(row, part.first + c * E)
+                                                  : load_ragged(row, V, part.first + c * E),
+                      most, x);
 #pragma unroll
       for (int e = 0; e < E; ++e) own += w[e] = weight(x[e], c * E + e);
     }
     const unsigned long long sum = warp_scan_u64(own);
     const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31));
-    if (at >= 0 && at < all) {
-      const int who = __ffs(__ballot_sync(0xffffffffu, static_cast<long long>(sum) > at)) - 1;
-      if (lane == who) {
-        long long left = at - static_cast<long long>(sum - own);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (found < 0 && left < static_cast<long long>(w[e])) found = c * E + e;
-          left -= w[e];
-        }
-      }
-      at = -1;  // (found)
-    } else if (at >= 0) {
+    if (at >= all) {
       at -= all;
+      continue;
     }
+    const int who = __ffs(__ballot_sync(0xffffffffu, static_cast<long long>(sum) > at)) - 1;
+    if (lane != who) return -1;
+    at -= static_cast<long long>(sum - own);
+    int found = -1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (found < 0 && at < static_cast<long long>(w[e])) found = c * E + e;
+      at -= w[e];
+    }
+    return found;
   }
-  return found;
+  return -1;
 }
 
 // ------------------------------------------------------------- sampling rows
@@ -408,8 +416,10 @@ struct Listed {
   uint32_t own[kListed];  // this CTA's: element of its part
   uint32_t digits[3][256];
 };
-union Scratch {
-  uint32_t bins[2][kBins];  // counts, or sums of weights and their carries
+// Bins: counts, or sums of weights and their carries; counts of the threads'
+// largest logits.
+struct Scratch {
+  uint32_t bins[3][kBins];
   Listed list;
 };
 struct Found {
@@ -425,6 +435,7 @@ struct SampleShared {
   unsigned long long scan[kSampleWarps];
   unsigned long long digit_before, digit_inside;
   int digit, listed;
+  uint32_t differ[2];
 };
 
 // Tokens that top-p takes at the first try, and the most for which the threads'
@@ -568,7 +579,7 @@ struct RowState {
 // Returns whether the row is done with altogether.  A function of its own, so
 // that rows without filters do not pay for its registers.
 template <typename T, bool VERIFY>
-__device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, Scratch& scr,
+__device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, Scratch& scr, uint4* ring,
                                         RowState<T>& st) {
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -586,7 +597,7 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
   unsigned long long border = 0, own = 0;
   // Every element of this CTA, in no order: test(logit, id).
   auto each = [&](auto&& test) {
-    each_chunk<4>(row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
+    each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
       float x[E];
       chunk_logits<T>(v, most, x);
 #pragma unroll
@@ -611,8 +622,13 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
     return weight_of(e) > 0 && e >= min_p && token_key(v, part.first + i) >= floor_key;
   };
   auto clear_bins = [&]() {
-    for (int i = tid; i < kBins; i += kSampleThreads) scr.bins[0][i] = scr.bins[1][i] = 0;
+    for (int i = tid; i < kBins; i += kSampleThreads)
+      scr.bins[0][i] = scr.bins[1][i] = scr.bins[2][i] = 0;
     __syncthreads();
+  };
+  auto weigh = [&](int bin, uint32_t w) {
+    const uint32_t was = atomicAdd(&scr.bins[0][bin], w);
+    if (was + w < was) atomicAdd(&scr.bins[1][bin], 1u);
   };
   // The bin, and within it the range of keys, that a limit falls into, and
   // the measure of what comes before.
@@ -631,15 +647,15 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
         atomicAdd(&scr.bins[0][at], 1u);
       } else {
         const uint32_t w = weight_of(expf(z));
-        const uint32_t was = atomicAdd(&scr.bins[0][at], w);
-        if (was + w < was) atomicAdd(&scr.bins[1][at], 1u);
+        weigh(at, w);
       }
     });
     cluster_barrier();
   };
-  // Every CTA adds up its share of the bins over the cluster; whoever finds
+  // Every CTA adds up its share of the bins (`which`: 0 numbers, 1 weights, 2 the
+  // threads' largest) over the cluster; whoever finds
   // the limit tells the others.  `limit` gets the measure of all bins.
-  auto search = [&](bool count, unsigned long long base, auto&& limit) {
+  auto search = [&](int which, unsigned long long base, auto&& limit) {
     constexpr int kMost = (kBins + kSampleThreads - 1) / kSampleThreads;
     const int share = (kBins + cluster - 1) / cluster, lo = rank * share;
     const int each_bins = (share + kSampleThreads - 1) / kSampleThreads;
@@ -653,9 +669,9 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
 #pragma unroll
         for (int c = 0; c < kMostCluster; ++c)
           if (c < cluster) {
-            const uint32_t* from = cluster_pointer(&scr.bins[0][lo + at], c);
+            const uint32_t* from = cluster_pointer(&scr.bins[which & 2][lo + at], c);
             l[c] = from[0];
-            if (!count) h[c] = from[kBins];
+            if (which & 1) h[c] = from[kBins];
           }
 #pragma unroll
         for (int c = 0; c < kMostCluster; ++c)
@@ -707,8 +723,27 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       w[j] = on[j] ? scr.list.w[i] : 0;
       on[j] = on[j] && key[j] >= floor;
     }
-    unsigned long long result = 0;
-    for (int shift = 56; shift >= 0; shift -= 8) {
+    // what all keys have in common is skipped
+    uint32_t hi_differ = 0, lo_differ = 0;
+    const unsigned long long some = scr.list.key[0];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (on[j]) {
+        hi_differ |= static_cast<uint32_t>((key[j] ^ some) >> 32);
+        lo_differ |= static_cast<uint32_t>(key[j] ^ some);
+      }
+    if (tid == 0) sh.differ[0] = sh.differ[1] = 0;
+    __syncthreads();
+    hi_differ = __reduce_or_sync(0xffffffffu, hi_differ);
+    lo_differ = __reduce_or_sync(0xffffffffu, lo_differ);
+    if (lane == 0 && hi_differ) atomicOr(&sh.differ[0], hi_differ);
+    if (lane == 0 && lo_differ) atomicOr(&sh.differ[1], lo_differ);
+    __syncthreads();
+    const int bits = sh.differ[0] ? 64 - __clz(sh.differ[0]) : 32 - __clz(sh.differ[1]);
+    const int first_shift = bits <= 8 ? 0 : (bits + 7) / 8 * 8 - 8;
+    unsigned long long result =
+        first_shift >= 56 ? 0 : some >> (first_shift + 8) << (first_shift + 8);
+    for (int shift = first_shift; shift >= 0; shift -= 8) {
       for (int i = tid; i < 256; i += kSampleThreads)
         scr.list.digits[0][i] = scr.list.digits[1][i] = scr.list.digits[2][i] = 0;
       __syncthreads();
@@ -766,11 +801,11 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
   // least `guess` threads the largest logit is in the bin that is found, or
   // before it, so at least as many tokens are.
   const int guess = by_count ? k : kGuess;
-  bool done = false;
+  bool done = false, weighed = false;
   if (!by_count && !by_mass) {
     // min-p alone: a look at each token is enough
     unsigned long long last_key = ~0ull, short_n = 0;
-    own = sum_groups(row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
+    own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
       const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
       const int bin = bin_of(z);
       if (bin >= kBins) return 0u;
@@ -792,9 +827,9 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
     if (tid == 0) sh.listed = 0;
     const float tv = at_most(top, most), tz = __fmul_rn(__fsub_rn(tv, sc.max), sc.inv);
     const int tb = bin_of(tz);
-    if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[0][tb], 1u);
+    if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[2][tb], 1u);
     cluster_barrier();
-    const Found f = search(true, 0, [&](unsigned long long all) {
+    const Found f = search(2, 0, [&](unsigned long long all) {
       return fmin(static_cast<double>(guess), static_cast<double>(all));
     });
     const int hi_bin = f.all < guess ? kBins - 1 : f.bin;
@@ -811,9 +846,11 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       const uint32_t w = weight_of(expf(z));
       if (!able(v, z, bin, i)) {
         rest = rest || w > 0;
+        short_of = short_of || w > 0;
         return;
       }
       mass += w;
+      if (!by_count) weigh(bin, w);  // (top-p that takes more than the list goes on with them)
       if (bin > hi_bin) {
         rest = rest || w > 0;
         return;
@@ -857,6 +894,7 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
     }
   }
 
+  weighed = !by_count && by_mass;
   // by number (top-k), by weight (top-p), or one after the other
   for (int stage = by_count ? 0 : 1; stage < (by_mass ? 2 : 1) && !done; ++stage) {
     const bool count = stage == 0;
@@ -865,8 +903,8 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       const double n = static_cast<double>(all);
       return stop = count ? fmin(static_cast<double>(k), n) : __dmul_rn(static_cast<double>(p), n);
     };
-    histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
-    Found f = search(count, 0, limit);
+    if (!weighed) histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
+    Found f = search(count ? 0 : 1, 0, limit);
     // (weights of what passes sum to more than 0 each, so both measures tell)
     short_of = short_of || f.before + f.inside < f.all;
     unsigned long long low = 0, high = ~0ull;  // keys within the bin
@@ -885,7 +923,7 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       __syncthreads();
       bool drop = short_of;
       unsigned long long first_key = 0, last_key = ~0ull;
-      own = sum_groups(row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
+      own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
         const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
         const int bin = bin_of(z);
         if (bin > hi_bin || !able(v, z, bin, i)) return 0u;
@@ -941,7 +979,7 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
         const unsigned long long key = token_key(v, part.first + i);
         return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
       });
-      f = search(count, f.before, [&](unsigned long long) { return stop; });
+      f = search(count ? 0 : 1, f.before, [&](unsigned long long) { return stop; });
       high = highest - (static_cast<unsigned long long>(f.bin) << shift);
       const unsigned long long end = high - ((1ull << shift) - 1);
       low = end > lowest && end <= high ? end : lowest;
@@ -1003,6 +1041,7 @@ template <typename T, bool VERIFY, bool FILTERS>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
   __shared__ SampleShared sh;
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ __align__(16) unsigned char scratch[FILTERS ? sizeof(Scratch) : 16];
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -1040,7 +1079,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
     const bool no_draw = VERIFY && judges && !a.greedy_drafts;
     float top = -INFINITY;
-    each_chunk<6>(row, a.V, part, tid, kSampleThreads, part.chunks,
+    each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks,
                   [&](const uint4& v, int) { top = fmaxf(top, largest_of<T>(v)); });
     unsigned long long x = float_order_key(top + 0.f), y = 0;
     cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
@@ -1055,7 +1094,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     if (greedy) {
       // the lowest id of the largest logit, and whether any other logit is finite
       unsigned long long best = 0, others = 0;
-      each_chunk<4>(row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
+      each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
         float l[E];
         chunk_logits<T>(v, most, l);
 #pragma unroll
@@ -1092,7 +1131,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       if (by_count || by_mass || by_share) {
         RowState<T> st = {row,      r,       q,        draft, judges, k,    p,   min_p,
                           by_count, by_mass, by_share, part,  sc,     most, top, parity, 0, 0};
-        const bool done = filter_row<T, VERIFY>(a, sh, *reinterpret_cast<Scratch*>(scratch), st);
+        const bool done = filter_row<T, VERIFY>(a, sh, *reinterpret_cast<Scratch*>(scratch), ring, st);
         parity = st.parity;
         if (done) continue;
         border = st.border;
@@ -1103,7 +1142,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const float cut = border ? key_float(static_cast<uint32_t>(border >> 32)) : -INFINITY;
     const int cut_token = border ? argmax_key_index(border) : a.V - 1;
     if (!summed)
-      own = sum_groups(row, a.V, part, seg, most, sh.groups[warp],
+      own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp],
                        [&](float v, int) { return weight_of(exp_of(v, sc)); });
     if (lane == 0) sh.warp_mass[warp] = own;
     unsigned long long total = lane == 0 ? own : 0, none = 0;
@@ -1389,9 +1428,13 @@ static cudaError_t resident_rows(int cluster, int& n) {
   std::atomic<int>* place = dev < 16 ? &known[dev][c] : nullptr;
   n = place ? place->load(std::memory_order_relaxed) : 0;
   if (n > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(sample_rows_kernel<T, VERIFY, FILTERS>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
@@ -1413,7 +1456,7 @@ static cudaError_t launch_rows(SampleArgs a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(sample_rows_kernel<T, VERIFY, FILTERS>,
                             dim3(static_cast<unsigned>(std::min(a.rows, resident)) * a.cluster),
-                            dim3(kSampleThreads), 0, s, a.cluster, a);
+                            dim3(kSampleThreads), kRingBytes, s, a.cluster, a);
 }
 // A call without top-k, top-p and min-p has a kernel without them: what they
 // need of registers costs every row, whether it has filters or not.
