@@ -221,13 +221,17 @@ __device__ __forceinline__ void chunk_logits(const uint4& v, float most, float (
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 4) {
-      x[i] = at_most(__uint_as_float(w[i]), most);
+      x[i] = __uint_as_float(w[i]);
     } else {
-      x[2 * i] = at_most(__uint_as_float(w[i] << 16), most);
-      x[2 * i + 1] = at_most(__uint_as_float(w[i] & 0xffff0000u), most);
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  if (most != INFINITY)
+#pragma unroll
+    for (int e = 0; e < Part<T>::E; ++e) x[e] = at_most(x[e], most);
 }
+
 // Chunks from, from + step, .. below `to` of a CTA's part: f(chunk's words,
 // chunk).  A thread's chunks come through a ring of its own in shared memory,
 // by asynchronous copies, so that many are on their way in a loop that stays
@@ -440,7 +444,7 @@ struct SampleShared {
 
 // Tokens that top-p takes at the first try, and the most for which the threads'
 // largest logits are asked.
-constexpr int kGuess = 128;
+constexpr int kGuess = 256;
 constexpr int kMostGuess = 256;
 
 // A row's result.
@@ -632,11 +636,15 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
   };
   // The bin, and within it the range of keys, that a limit falls into, and
   // the measure of what comes before.
-  auto histogram = [&](bool count, auto&& place) {
+  auto histogram = [&](bool count, auto&& place, int within) {
     clear_bins();
     each([&](float v, int i) {
       const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
       const int bin = bin_of(z);
+      if (bin > within) {
+      short_of = short_of || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
+      return;
+      }
       const int at = place(v, bin, i);
       if (at < 0) return;
       if (!able(v, z, bin, i)) {
@@ -801,19 +809,18 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
   // least `guess` threads the largest logit is in the bin that is found, or
   // before it, so at least as many tokens are.
   const int guess = by_count ? k : kGuess;
-  bool done = false, weighed = false;
+  bool done = false;
   if (!by_count && !by_mass) {
     // min-p alone: a look at each token is enough
     unsigned long long last_key = ~0ull, short_n = 0;
     own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
       const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
       const int bin = bin_of(z);
-      if (bin >= kBins) return 0u;
-      const uint32_t w = weight_of(expf(z));
       if (!able(v, z, bin, i)) {
-        short_n |= w > 0;
+        short_n |= bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
         return 0u;
       }
+      const uint32_t w = weight_of(expf(z));
       const unsigned long long key = token_key(v, part.first + i);
       last_key = key < last_key ? key : last_key;
       return w;
@@ -846,11 +853,9 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       const uint32_t w = weight_of(expf(z));
       if (!able(v, z, bin, i)) {
         rest = rest || w > 0;
-        short_of = short_of || w > 0;
         return;
       }
       mass += w;
-      if (!by_count) weigh(bin, w);  // (top-p that takes more than the list goes on with them)
       if (bin > hi_bin) {
         rest = rest || w > 0;
         return;
@@ -894,7 +899,6 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
     }
   }
 
-  weighed = !by_count && by_mass;
   // by number (top-k), by weight (top-p), or one after the other
   for (int stage = by_count ? 0 : 1; stage < (by_mass ? 2 : 1) && !done; ++stage) {
     const bool count = stage == 0;
@@ -903,7 +907,26 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
       const double n = static_cast<double>(all);
       return stop = count ? fmin(static_cast<double>(k), n) : __dmul_rn(static_cast<double>(p), n);
     };
-    if (!weighed) histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
+    // Large k: of at least k chunks the largest logit is in the bin that is found,
+      // or before it, so no others need be counted (an addition to a bin costs
+      // what twenty other instructions do).
+      int within = kBins - 1;
+      if (count) {
+        clear_bins();
+        each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks,
+                   [&](const uint4& v, int) {
+                     const float l = at_most(largest_of<T>(v), most);
+                     const float z = __fmul_rn(__fsub_rn(l, sc.max), sc.inv);
+                     const int bin = bin_of(z);
+                     if (bin < kBins && able(l, z, bin, 0)) atomicAdd(&scr.bins[2][bin], 1u);
+                   });
+        cluster_barrier();
+        const Found b = search(2, 0, [&](unsigned long long all) {
+          return fmin(static_cast<double>(k), static_cast<double>(all));
+        });
+        if (b.all >= k) within = b.bin;
+      }
+      histogram(count, [&](float, int bin, int) { return bin <= within ? bin : -1; }, within);
     Found f = search(count ? 0 : 1, 0, limit);
     // (weights of what passes sum to more than 0 each, so both measures tell)
     short_of = short_of || f.before + f.inside < f.all;
@@ -978,7 +1001,7 @@ __device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, S
         if (bin != hi_bin) return -1;
         const unsigned long long key = token_key(v, part.first + i);
         return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
-      });
+      }, kBins - 1);
       f = search(count ? 0 : 1, f.before, [&](unsigned long long) { return stop; });
       high = highest - (static_cast<unsigned long long>(f.bin) << shift);
       const unsigned long long end = high - ((1ull << shift) - 1);
