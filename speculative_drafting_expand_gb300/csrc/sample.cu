@@ -15,10 +15,10 @@
 
 namespace pe {
 
-constexpr int kSampleThreads = 512;
+constexpr int kSampleThreads = 384;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kMostCluster = 8;
-constexpr int kMostVocab = 393216;  // what verify_kernel's eight CTAs hold of weights
+constexpr int kMostVocab = 393216;  // fp32: 192 KB of each of eight CTAs' shared memory
 
 struct SampleArgs {
   int rows, V, cluster;
@@ -183,7 +183,6 @@ struct Part {
   int per;     // chunks of a CTA (the last ones may have fewer)
   int first;   // id of this CTA's first element (may be negative)
   int chunks;  // of this CTA
-  int lo, hi;  // those of them that are the row's alone
   __device__ __forceinline__ int owner(int id) const { return (id + mis) / E / per; }
 };
 template <typename T>
@@ -191,16 +190,13 @@ __device__ __forceinline__ Part<T> part_of(const T* row, int V, int cluster, int
   constexpr int E = Part<T>::E;
   const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % E);
   const int all = (mis + V + E - 1) / E, per = (all + cluster - 1) / cluster;
-  const int lo = min(rank * per, all), chunks = min(lo + per, all) - lo, first = lo * E - mis;
-  return Part<T>{mis, per, first, chunks, first < 0 ? 1 : 0, first + chunks * E > V ? chunks - 1 : chunks};
+  const int lo = min(rank * per, all);
+  return Part<T>{mis, per, lo * E - mis, min(lo + per, all) - lo};
 }
 template <typename T>
-__device__ __forceinline__ uint4 load_whole(const T* row, int id) {
-  return __ldg(reinterpret_cast<const uint4*>(row + id));
-}
-// A chunk at an end of the row: element by element.
-template <typename T>
-__device__ __forceinline__ uint4 load_ragged(const T* row, int V, int id) {
+__device__ __forceinline__ uint4 load_chunk(const T* row, int V, int id) {
+  constexpr int E = Part<T>::E;
+  if (id >= 0 && id + E <= V) return __ldcs(reinterpret_cast<const uint4*>(row + id));
   uint32_t w[4];
   auto bits = [&](int e) -> uint32_t {
     const bool in = id + e >= 0 && id + e < V;
@@ -212,63 +208,31 @@ __device__ __forceinline__ uint4 load_ragged(const T* row, int V, int id) {
     w[i] = sizeof(T) == 4 ? bits(i) : bits(2 * i) | bits(2 * i + 1) << 16;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// The logits of a chunk, as they came: NaN has weight 0, is above and equal to
-// nothing, and falls into the last bin without being asked for.  `most` is +inf,
-// or in a row with +inf the largest finite number.
+// The logits of a chunk in shared memory, as they came: NaN has weight 0, is
+// above and equal to nothing, and falls into the last bin without being asked
+// for; a row with +inf is cleaned in place (16-bit logits have no room for the
+// largest fp32 number: `most` is that, or +inf where the row has none).
 template <typename T>
-__device__ __forceinline__ void chunk_logits(const uint4& v, float most, float (&x)[Part<T>::E]) {
+__device__ __forceinline__ void chunk_logits(const uint4* p, float most, float (&x)[Part<T>::E]) {
+  const uint4 v = *p;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 4) {
       x[i] = __uint_as_float(w[i]);
     } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      x[2 * i] = at_most(__uint_as_float(w[i] << 16), most);
+      x[2 * i + 1] = at_most(__uint_as_float(w[i] & 0xffff0000u), most);
     }
   }
-  if (most != INFINITY)
-#pragma unroll
-    for (int e = 0; e < Part<T>::E; ++e) x[e] = at_most(x[e], most);
 }
 
-// Chunks from, from + step, .. below `to` of a CTA's part: f(chunk's words,
-// chunk).  A thread's chunks come through a ring of its own in shared memory,
-// by asynchronous copies, so that many are on their way in a loop that stays
-// short.
-constexpr int kRing = 4;
-constexpr size_t kRingBytes = static_cast<size_t>(kRing) * kSampleThreads * 16;
-template <typename T, typename F>
-__device__ __forceinline__ void each_chunk(uint4* ring, const T* row, int V, const Part<T>& part,
-                                           int from, int step, int to, F&& f) {
-  constexpr int E = Part<T>::E;
-  uint4* mine = ring + threadIdx.x;
-  const uint32_t first_slot = smem_u32(mine), last_slot = first_slot + (kRing - 1) * kSampleThreads * 16;
-  uint32_t fill = first_slot;
-  int ahead = from;
-  const int hi = min(to, part.hi);
-  auto fetch = [&]() {
-    if (ahead >= part.lo && ahead < hi)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(fill),
-                   "l"(row + part.first + ahead * E)
-                   : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    ahead += step;
-    fill = fill == last_slot ? first_slot : fill + kSampleThreads * 16;
-  };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) fetch();
-  int slot = 0;
-#pragma unroll 1
-  for (int c = from; c < to; c += step) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-    uint4 v = mine[slot * kSampleThreads];
-    slot = (slot + 1) % kRing;
-    fetch();  // into the place before this one
-    if (c < part.lo || c >= part.hi) v = load_ragged(row, V, part.first + c * E);
-    f(v, c);
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+// One of them (read as the words they were written as).
+template <typename T>
+__device__ __forceinline__ float held_logit(const unsigned char* held, int i, float most) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(held);
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+  else return at_most(__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16), most);
 }
 
 // The largest logit of a chunk, whatever NaN there are (a chunk of NaN: NaN).
@@ -286,6 +250,19 @@ __device__ __forceinline__ float largest_of(const uint4& v) {
   }
 }
 
+// Contiguous chunks of a warp, and of a lane within them, so that sums over
+// warps and lanes are in the order of the ids.
+struct Segment {
+  int lo, hi;
+};
+__device__ __forceinline__ int warp_segment_size(int chunks) {
+  return (chunks + kSampleWarps - 1) / kSampleWarps;
+}
+__device__ __forceinline__ Segment warp_segment(int chunks) {
+  const int per = warp_segment_size(chunks);
+  const int lo = min(static_cast<int>(threadIdx.x) / 32 * per, chunks);
+  return Segment{lo, min(lo + per, chunks)};
+}
 __device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v) {
   const int lane = threadIdx.x % 32;
 #pragma unroll
@@ -295,106 +272,35 @@ __device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v
   }
   return v;
 }
-
-// A warp's contiguous chunks of a CTA's part, and groups of them: sums over
-// warps and groups are in the order of the ids, and one group is looked at
-// again to find a token.  Rows of few chunks have groups of one round of a
-// warp's loads, others of eight.
-constexpr int kRounds = 8;
-constexpr int kMostGroups = 64;  // of a warp: 2^17 fp32 logits in all
-struct Segment {
-  int lo, hi, rounds, per;
-};
-__device__ __forceinline__ Segment warp_segment(int chunks) {
-  const int rounds = chunks > kSampleWarps * 32 * kRounds ? kRounds : 1, group = 32 * rounds;
-  const int per = ((chunks + kSampleWarps - 1) / kSampleWarps + group - 1) / group * group;
-  const int lo = min(static_cast<int>(threadIdx.x) / 32 * per, chunks);
-  return Segment{lo, min(lo + per, chunks), rounds, per};
-}
-// Sums of a warp's groups into groups[], weight(x, place of the element) of each
-// element; every lane gets the sum of all.
-template <typename T, typename W>
-__device__ __forceinline__ unsigned long long sum_groups(uint4* ring, const T* row, int V,
-                                                         const Part<T>& part, const Segment& seg,
-                                                         float most, unsigned long long* groups,
-                                                         W&& weight) {
-  constexpr int E = Part<T>::E;
+// The element of a warp's segment at which the weights, in order, first
+// exceed `at`: the lane's part that holds it, then the element.  Returns chunk
+// * E + element on one lane, -1 on the others.
+template <int E, typename W>
+__device__ __forceinline__ int find_in_segment(Segment seg, long long at, W&& weight) {
   const int lane = threadIdx.x % 32;
-  unsigned long long all = 0, own = 0;
-  int round = 0;
-  // (every lane takes part in a group's sum: chunks past the end weigh nothing)
-  const int end = seg.lo + (seg.hi - seg.lo + 31) / 32 * 32;
-  each_chunk(ring, row, V, part, seg.lo + lane, 32, end, [&](const uint4& v, int c) {
-    if (c < seg.hi) {
-      float x[E];
-      chunk_logits<T>(v, most, x);
+  const int per = (seg.hi - seg.lo + 31) / 32;
+  const int lo = min(seg.lo + lane * per, seg.hi), hi = min(lo + per, seg.hi);
+  unsigned long long own = 0;
+  for (int c = lo; c < hi; ++c)
 #pragma unroll
-      for (int e = 0; e < E; ++e) own += weight(x[e], c * E + e);
-    }
-    if (++round % seg.rounds == 0 || c - lane + 32 >= end) {
-      own = warp_sum_u64(own);
-      if (lane == 0) groups[(round - 1) / seg.rounds] = own;
-      all += own;
-      own = 0;
-    }
-  });
-  return all;
-}
-// The element at which a warp's weights, in order, first exceed `at`: the group
-// that holds it (less[g] of its sum is left out), then the element.  Returns
-// chunk * E + element on one lane, -1 on the others.
-template <typename T, typename W, typename L>
-__device__ __forceinline__ int find_in_groups(const T* row, int V, const Part<T>& part,
-                                              const Segment& seg, float most,
-                                              const unsigned long long* groups, long long at,
-                                              L&& less, W&& weight) {
-  constexpr int E = Part<T>::E;
-  const int lane = threadIdx.x % 32;
-  const int n = (seg.hi - seg.lo + 32 * seg.rounds - 1) / (32 * seg.rounds);
-  int group = -1;
-  for (int g0 = 0; g0 < n && group < 0; g0 += 32) {
-    const int g = g0 + lane;
-    const unsigned long long w = g < n ? groups[g] - less(g) : 0ull;
+    for (int e = 0; e < E; ++e) own += weight(c, e);
+  const unsigned long long run = warp_scan_u64(own);
+  const unsigned hit = __ballot_sync(0xffffffffu, static_cast<long long>(run) > at);
+  if (hit == 0) return -1;  // not reached: the sums agree
+  const int who = __ffs(hit) - 1;
+  at -= static_cast<long long>(__shfl_sync(0xffffffffu, run - own, who));
+  const int from = __shfl_sync(0xffffffffu, lo, who) * E, to = __shfl_sync(0xffffffffu, hi, who) * E;
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned long long w = i < to ? weight(i / E, i % E) : 0u;
     const unsigned long long sum = warp_scan_u64(w);
     const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31));
     if (at >= all) {
       at -= all;
       continue;
     }
-    const int who = __ffs(__ballot_sync(0xffffffffu, static_cast<long long>(sum) > at)) - 1;
-    at -= static_cast<long long>(__shfl_sync(0xffffffffu, sum - w, who));
-    group = g0 + who;
-  }
-  if (group < 0) return -1;  // not reached: the sums agree
-#pragma unroll 1
-  for (int i = 0; i < seg.rounds; ++i) {
-    const int c = seg.lo + (group * seg.rounds + i) * 32 + lane;
-    uint32_t w[E] = {};
-    unsigned long long own = 0;
-    if (c < seg.hi) {
-      float x[E];
-      chunk_logits<T>(c >= part.lo && c < part.hi ? load_whole(row, part.first + c * E)
-                                                  : load_ragged(row, V, part.first + c * E),
-                      most, x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) own += w[e] = weight(x[e], c * E + e);
-    }
-    const unsigned long long sum = warp_scan_u64(own);
-    const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31));
-    if (at >= all) {
-      at -= all;
-      continue;
-    }
-    const int who = __ffs(__ballot_sync(0xffffffffu, static_cast<long long>(sum) > at)) - 1;
-    if (lane != who) return -1;
-    at -= static_cast<long long>(sum - own);
-    int found = -1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (found < 0 && at < static_cast<long long>(w[e])) found = c * E + e;
-      at -= w[e];
-    }
-    return found;
+    const unsigned h = __ballot_sync(0xffffffffu, static_cast<long long>(sum) > at);
+    return lane == __ffs(h) - 1 ? i : -1;
   }
   return -1;
 }
@@ -417,13 +323,11 @@ constexpr int kListed = 640;
 struct Listed {
   unsigned long long key[kListed];
   uint32_t w[kListed];
-  uint32_t own[kListed];  // this CTA's: element of its part
+  uint16_t own[kListed];  // this CTA's: element of its part
   uint32_t digits[3][256];
 };
-// Bins: counts, or sums of weights and their carries; counts of the threads'
-// largest logits.
-struct Scratch {
-  uint32_t bins[3][kBins];
+union Scratch {
+  uint32_t bins[2][kBins];  // counts, or sums of the weights' low and high halves
   Listed list;
 };
 struct Found {
@@ -434,8 +338,6 @@ struct SampleShared {
   Exchange ex;
   Found found;
   unsigned long long warp_mass[kSampleWarps];
-  unsigned long long groups[kSampleWarps][kMostGroups];
-  unsigned long long joined[kSampleWarps];
   unsigned long long scan[kSampleWarps];
   unsigned long long digit_before, digit_inside;
   int digit, listed;
@@ -444,7 +346,7 @@ struct SampleShared {
 
 // Tokens that top-p takes at the first try, and the most for which the threads'
 // largest logits are asked.
-constexpr int kGuess = 256;
+constexpr int kGuess = 128;
 constexpr int kMostGuess = 256;
 
 // A row's result.
@@ -561,652 +463,606 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
   }
 }
 
-// What the steps of a row hand on.
-template <typename T>
-struct RowState {
-  const T* row;
-  int r, q, draft;  // row, request, the draft that it judges
-  bool judges;
-  int k;            // filters
-  float p, min_p;
-  bool by_count, by_mass, by_share;
-  Part<T> part;
-  RowScale sc;
-  float most;  // see chunk_logits
-  float top;   // the thread's largest logit
-  int parity;
-  unsigned long long border, own;  // results
-};
-
-// The filters of a row: finds the last kept token's key (0: every token of W >
-// 0 is kept) and this warp's share of the kept weight, by groups in sh.groups.
-// Returns whether the row is done with altogether.  A function of its own, so
-// that rows without filters do not pay for its registers.
-template <typename T, bool VERIFY>
-__device__ __noinline__ bool filter_row(const SampleArgs& a, SampleShared& sh, Scratch& scr, uint4* ring,
-                                        RowState<T>& st) {
-  constexpr int E = Part<T>::E;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int cluster = a.cluster, rank = cluster_ctarank();
-  const T* row = st.row;
-  const int r = st.r, q = st.q, draft = st.draft, k = st.k;
-  const bool judges = st.judges;
-  const float p = st.p, min_p = st.min_p;
-  const bool by_count = st.by_count, by_mass = st.by_mass, by_share = st.by_share;
-  const Part<T> part = st.part;
-  const RowScale sc = st.sc;
-  const float most = st.most, top = st.top;
-  int& parity = st.parity;
-  const Segment seg = warp_segment(part.chunks);
-  unsigned long long border = 0, own = 0;
-  // Every element of this CTA, in no order: test(logit, id).
-  auto each = [&](auto&& test) {
-    each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
-      float x[E];
-      chunk_logits<T>(v, most, x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) test(x[e], c * E + e);
-    });
-  };
-
-  // Which tokens pass the filters other than the one that is being applied:
-  // bins below `sure` do, bins above `last` do not, the rest are looked at.
-  int sure = kSure, last = kBins - 1;
-  if (by_share) {
-    const int at = bin_of(logf(min_p));
-    sure = min(sure, at - 2);
-    last = min(last, at + 2);
-  }
-  unsigned long long floor_key = 0;
-  bool short_of = false;  // some token of W > 0 is kept by no stage so far
-  auto able = [&](float v, float z, int bin, int i) {
-    if (bin < sure) return true;
-    if (bin > last) return false;
-    const float e = expf(z);
-    return weight_of(e) > 0 && e >= min_p && token_key(v, part.first + i) >= floor_key;
-  };
-  auto clear_bins = [&]() {
-    for (int i = tid; i < kBins; i += kSampleThreads)
-      scr.bins[0][i] = scr.bins[1][i] = scr.bins[2][i] = 0;
-    __syncthreads();
-  };
-  auto weigh = [&](int bin, uint32_t w) {
-    const uint32_t was = atomicAdd(&scr.bins[0][bin], w);
-    if (was + w < was) atomicAdd(&scr.bins[1][bin], 1u);
-  };
-  // The bin, and within it the range of keys, that a limit falls into, and
-  // the measure of what comes before.
-  auto histogram = [&](bool count, auto&& place, int within) {
-    clear_bins();
-    each([&](float v, int i) {
-      const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
-      const int bin = bin_of(z);
-      if (bin > within) {
-      short_of = short_of || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
-      return;
-      }
-      const int at = place(v, bin, i);
-      if (at < 0) return;
-      if (!able(v, z, bin, i)) {
-        short_of = short_of || bin < kSure || weight_of(expf(z)) > 0;
-        return;
-      }
-      if (count) {
-        atomicAdd(&scr.bins[0][at], 1u);
-      } else {
-        const uint32_t w = weight_of(expf(z));
-        weigh(at, w);
-      }
-    });
-    cluster_barrier();
-  };
-  // Every CTA adds up its share of the bins (`which`: 0 numbers, 1 weights, 2 the
-  // threads' largest) over the cluster; whoever finds
-  // the limit tells the others.  `limit` gets the measure of all bins.
-  auto search = [&](int which, unsigned long long base, auto&& limit) {
-    constexpr int kMost = (kBins + kSampleThreads - 1) / kSampleThreads;
-    const int share = (kBins + cluster - 1) / cluster, lo = rank * share;
-    const int each_bins = (share + kSampleThreads - 1) / kSampleThreads;
-    unsigned long long v[kMost], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      v[j] = 0;
-      const int at = tid * each_bins + j;
-      if (j < each_bins && at < share && lo + at < kBins) {
-        uint32_t l[kMostCluster] = {}, h[kMostCluster] = {};
-#pragma unroll
-        for (int c = 0; c < kMostCluster; ++c)
-          if (c < cluster) {
-            const uint32_t* from = cluster_pointer(&scr.bins[which & 2][lo + at], c);
-            l[c] = from[0];
-            if (which & 1) h[c] = from[kBins];
-          }
-#pragma unroll
-        for (int c = 0; c < kMostCluster; ++c)
-          v[j] += l[c] + (static_cast<unsigned long long>(h[c]) << 32);
-      }
-      sum += v[j];
-    }
-    const unsigned long long run = warp_scan_u64(sum);
-    if (lane == 31) sh.scan[warp] = run;
-    unsigned long long all = sum, none = 0;
-    const int par = parity;
-    cluster_reduce<false>(sh.ex, parity, cluster, rank, all, none);
-    unsigned long long before = base + run - sum;
-    for (int i = 0; i < rank; ++i) before += sh.ex.slot[par][0][i];
-    for (int i = 0; i < warp; ++i) before += sh.scan[i];
-    const double stop = limit(all);
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      if (v[j] && static_cast<double>(before) < stop &&
-          !(static_cast<double>(before + v[j]) < stop))
-        for (int c = 0; c < cluster; ++c) {
-          const uint32_t to = cluster_map_shared(smem_u32(&sh.found), c);
-          st_cluster_u64(to, before);
-          st_cluster_u64(to + 8, v[j]);
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 24),
-                       "r"(lo + tid * each_bins + j)
-                       : "memory");
-        }
-      before += v[j];
-    }
-    cluster_barrier();
-    Found f = sh.found;
-    f.all = all;
-    return f;
-  };
-  // The last token of `listed` ones before which the measure is below the
-  // limit: eight bits of the keys at a time.  Every CTA has the whole list.
-  auto select = [&](int listed, bool count, unsigned long long base, double stop,
-                    unsigned long long floor) {
-    constexpr int kEach = (kListed + kSampleThreads - 1) / kSampleThreads;
-    unsigned long long key[kEach];
-    uint32_t w[kEach];
-    bool on[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int i = tid + j * kSampleThreads;
-      on[j] = i < listed;
-      key[j] = on[j] ? scr.list.key[i] : 0;
-      w[j] = on[j] ? scr.list.w[i] : 0;
-      on[j] = on[j] && key[j] >= floor;
-    }
-    // what all keys have in common is skipped
-    uint32_t hi_differ = 0, lo_differ = 0;
-    const unsigned long long some = scr.list.key[0];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j)
-      if (on[j]) {
-        hi_differ |= static_cast<uint32_t>((key[j] ^ some) >> 32);
-        lo_differ |= static_cast<uint32_t>(key[j] ^ some);
-      }
-    if (tid == 0) sh.differ[0] = sh.differ[1] = 0;
-    __syncthreads();
-    hi_differ = __reduce_or_sync(0xffffffffu, hi_differ);
-    lo_differ = __reduce_or_sync(0xffffffffu, lo_differ);
-    if (lane == 0 && hi_differ) atomicOr(&sh.differ[0], hi_differ);
-    if (lane == 0 && lo_differ) atomicOr(&sh.differ[1], lo_differ);
-    __syncthreads();
-    const int bits = sh.differ[0] ? 64 - __clz(sh.differ[0]) : 32 - __clz(sh.differ[1]);
-    const int first_shift = bits <= 8 ? 0 : (bits + 7) / 8 * 8 - 8;
-    unsigned long long result =
-        first_shift >= 56 ? 0 : some >> (first_shift + 8) << (first_shift + 8);
-    for (int shift = first_shift; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSampleThreads)
-        scr.list.digits[0][i] = scr.list.digits[1][i] = scr.list.digits[2][i] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kEach; ++j)
-        if (on[j]) {
-          const int d = static_cast<int>(key[j] >> shift) & 255;
-          atomicAdd(&scr.list.digits[0][d], 1u);
-          atomicAdd(&scr.list.digits[1][d], w[j] & 0xffffu);
-          atomicAdd(&scr.list.digits[2][d], w[j] >> 16);
-        }
-      __syncthreads();
-      if (warp == 0) {
-        // lane 0 has the largest digits
-        unsigned long long v[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int d = 255 - lane * 8 - i;
-          v[i] = count ? scr.list.digits[0][d]
-                       : scr.list.digits[1][d] + (static_cast<unsigned long long>(scr.list.digits[2][d]) << 16);
-          sum += v[i];
-        }
-        unsigned long long before = base + warp_scan_u64(sum) - sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (v[i] && static_cast<double>(before) < stop &&
-              !(static_cast<double>(before + v[i]) < stop)) {
-            sh.digit = 255 - lane * 8 - i;
-            sh.digit_before = before;
-            sh.digit_inside = scr.list.digits[0][255 - lane * 8 - i];
-          }
-          before += v[i];
-        }
-      }
-      __syncthreads();
-      const unsigned long long d = static_cast<unsigned long long>(sh.digit);
-      base = sh.digit_before;
-      result |= d << shift;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) on[j] = on[j] && ((key[j] >> shift) & 255) == d;
-      if (sh.digit_inside == 1) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j)
-          if (on[j]) sh.found.before = key[j];
-        __syncthreads();
-        result = sh.found.before;
-        break;
-      }
-      __syncthreads();
-    }
-    return result;
-  };
-
-  // Where the filters keep few tokens, they are all among a few.  Of at
-  // least `guess` threads the largest logit is in the bin that is found, or
-  // before it, so at least as many tokens are.
-  const int guess = by_count ? k : kGuess;
-  bool done = false;
-  if (!by_count && !by_mass) {
-    // min-p alone: a look at each token is enough
-    unsigned long long last_key = ~0ull, short_n = 0;
-    own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
-      const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
-      const int bin = bin_of(z);
-      if (!able(v, z, bin, i)) {
-        short_n |= bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
-        return 0u;
-      }
-      const uint32_t w = weight_of(expf(z));
-      const unsigned long long key = token_key(v, part.first + i);
-      last_key = key < last_key ? key : last_key;
-      return w;
-    });
-    unsigned long long inverse = ~last_key;
-    cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, short_n);
-    border = short_n ? ~inverse : 0;
-    done = true;
-  } else if (guess <= kMostGuess) {
-    clear_bins();
-    if (tid == 0) sh.listed = 0;
-    const float tv = at_most(top, most), tz = __fmul_rn(__fsub_rn(tv, sc.max), sc.inv);
-    const int tb = bin_of(tz);
-    if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[2][tb], 1u);
-    cluster_barrier();
-    const Found f = search(2, 0, [&](unsigned long long all) {
-      return fmin(static_cast<double>(guess), static_cast<double>(all));
-    });
-    const int hi_bin = f.all < guess ? kBins - 1 : f.bin;
-    unsigned long long n = 0, mass = 0, list_mass = 0;
-    bool rest = false;
-    each([&](float v, int i) {
-      const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
-      const int bin = bin_of(z);
-      if (bin > hi_bin && by_count) {
-        rest = rest || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
-        return;
-      }
-      if (bin >= kBins) return;
-      const uint32_t w = weight_of(expf(z));
-      if (!able(v, z, bin, i)) {
-        rest = rest || w > 0;
-        return;
-      }
-      mass += w;
-      if (bin > hi_bin) {
-        rest = rest || w > 0;
-        return;
-      }
-      list_mass += w;
-      const int at = atomicAdd(&sh.listed, 1);
-      if (at < kListed) scr.list.own[at] = i;
-    });
-    __syncthreads();
-    n = (tid == 0 ? static_cast<unsigned>(sh.listed) : 0u) | (rest ? 1ull << 32 : 0ull);
-    const int par = parity;
-    cluster_reduce<false>(sh.ex, parity, cluster, rank, n, mass, list_mass);
-    const int listed = static_cast<int>(n & 0xffffffffu);
-    rest = n >> 32;
-    const double stop = __dmul_rn(static_cast<double>(p), static_cast<double>(mass));
-    if (listed <= kListed && (by_count || !(static_cast<double>(list_mass) < stop))) {
-      // everything that is kept is listed: the first CTA does the rest, and
-      // the others go on
-      int at = 0;
-      for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i] & 0xffffffffu);
-      const int here = static_cast<int>(sh.ex.slot[par][0][rank] & 0xffffffffu);
-      for (int j = tid; j < here; j += kSampleThreads) {
-        const int el = scr.list.own[j];
-        const float xv = raw_logit(row + part.first + el);
-        st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), 0),
-                       token_key(xv, part.first + el));
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                         cluster_map_shared(smem_u32(&scr.list.w[at + j]), 0)),
-                     "r"(weight_of(exp_of(xv, sc)))
-                     : "memory");
-      }
-      cluster_barrier();
-      if (rank == 0) {
-        const ListRow lr = {listed, by_count ? min(k, listed) : listed, by_count, by_mass,
-                            rest,   static_cast<double>(p),            stop};
-        const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
-        draw_from_list<T, VERIFY>(a, sh, scr.list, lr, sc, r, q, row, left_out,
-                                  VERIFY && judges && !a.greedy_drafts);
-      }
-      return true;
-    }
-  }
-
-  // by number (top-k), by weight (top-p), or one after the other
-  for (int stage = by_count ? 0 : 1; stage < (by_mass ? 2 : 1) && !done; ++stage) {
-    const bool count = stage == 0;
-    double stop = 0.0;
-    auto limit = [&](unsigned long long all) {
-      const double n = static_cast<double>(all);
-      return stop = count ? fmin(static_cast<double>(k), n) : __dmul_rn(static_cast<double>(p), n);
-    };
-    // Large k: of at least k chunks the largest logit is in the bin that is found,
-      // or before it, so no others need be counted (an addition to a bin costs
-      // what twenty other instructions do).
-      int within = kBins - 1;
-      if (count) {
-        clear_bins();
-        each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks,
-                   [&](const uint4& v, int) {
-                     const float l = at_most(largest_of<T>(v), most);
-                     const float z = __fmul_rn(__fsub_rn(l, sc.max), sc.inv);
-                     const int bin = bin_of(z);
-                     if (bin < kBins && able(l, z, bin, 0)) atomicAdd(&scr.bins[2][bin], 1u);
-                   });
-        cluster_barrier();
-        const Found b = search(2, 0, [&](unsigned long long all) {
-          return fmin(static_cast<double>(k), static_cast<double>(all));
-        });
-        if (b.all >= k) within = b.bin;
-      }
-      histogram(count, [&](float, int bin, int) { return bin <= within ? bin : -1; }, within);
-    Found f = search(count ? 0 : 1, 0, limit);
-    // (weights of what passes sum to more than 0 each, so both measures tell)
-    short_of = short_of || f.before + f.inside < f.all;
-    unsigned long long low = 0, high = ~0ull;  // keys within the bin
-    int lo_bin = f.bin;
-    if (count && f.before + f.inside <= kListed) {
-      lo_bin = 0;  // few tokens in all: rank every one
-      f.before = 0;
-    }
-    const int hi_bin = f.bin;
-    int listed;
-    unsigned long long dropped;  // somewhere in the range's bin, or short_of
-    // (each further level has 2^-10 of the keys of the one before, of 2^64)
-    for (int level = 0; level < 8; ++level) {
-      // weights before the range, by segments; the range's own tokens
-      if (tid == 0) sh.listed = 0;
-      __syncthreads();
-      bool drop = short_of;
-      unsigned long long first_key = 0, last_key = ~0ull;
-      own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp], [&](float v, int i) {
-        const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
-        const int bin = bin_of(z);
-        if (bin > hi_bin || !able(v, z, bin, i)) return 0u;
-        if (bin < lo_bin) return weight_of(expf(z));
-        const unsigned long long key = token_key(v, part.first + i);
-        if (key > high) return weight_of(expf(z));
-        if (key < low) {
-          drop = true;
-          return 0u;
-        }
-        last_key = key < last_key ? key : last_key;
-        first_key = key > first_key ? key : first_key;
-        const int at = atomicAdd(&sh.listed, 1);
-        if (at < kListed) scr.list.own[at] = i;
-        return 0u;
-      });
-      __syncthreads();
-      unsigned long long n = static_cast<unsigned long long>(tid == 0 ? sh.listed : 0);
-      dropped = drop;
-      const int par = parity;
-      cluster_reduce<false>(sh.ex, parity, cluster, rank, n, dropped);
-      listed = static_cast<int>(n);
-      if (listed <= kListed) {
-        int at = 0;
-        for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i]);
-        const int here = static_cast<int>(sh.ex.slot[par][0][rank]);
-        for (int i = tid; i < here * cluster; i += kSampleThreads) {
-          const int to = i / here, j = i % here, el = scr.list.own[j];
-          const float xv = raw_logit(row + part.first + el);
-          st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), to),
-                         token_key(xv, part.first + el));
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                           cluster_map_shared(smem_u32(&scr.list.w[at + j]), to)),
-                       "r"(weight_of(exp_of(xv, sc)))
-                       : "memory");
-        }
-        cluster_barrier();
-        break;
-      }
-      // too many to rank: bins of the range's keys (ties go by their ids)
-      unsigned long long inverse = ~last_key;
-      cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, dropped);
-      low = ~inverse;
-      unsigned long long none = 0;
-      cluster_reduce<true>(sh.ex, parity, cluster, rank, first_key, none);
-      high = first_key;
-      int shift = 0;
-      while (shift < 54 && ((high - low) >> shift) >= kBins) ++shift;
-      lo_bin = hi_bin;  // (the range is that bin's: lists of all bins are short)
-      const unsigned long long lowest = low, highest = high;
-      histogram(count, [&](float v, int bin, int i) {
-        if (bin != hi_bin) return -1;
-        const unsigned long long key = token_key(v, part.first + i);
-        return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
-      }, kBins - 1);
-      f = search(count ? 0 : 1, f.before, [&](unsigned long long) { return stop; });
-      high = highest - (static_cast<unsigned long long>(f.bin) << shift);
-      const unsigned long long end = high - ((1ull << shift) - 1);
-      low = end > lowest && end <= high ? end : lowest;
-    }
-    listed = min(listed, kListed);
-    border = select(listed, count, f.before, stop, 0);
-    if (count && by_mass && lo_bin == 0 && listed <= kListed && hi_bin == f.bin && high == ~0ull) {
-      // all that is left is in the list: the weights' limit in it
-      unsigned long long mass = 0, none = 0;
-      for (int i = tid; i < listed; i += kSampleThreads)
-        if (scr.list.key[i] >= border) mass += scr.list.w[i];
-      mass = warp_sum_u64(mass);
-      if (lane == 0) sh.scan[warp] = mass;
-      __syncthreads();
-      for (int i = 0; i < kSampleWarps; ++i) none += sh.scan[i];
-      __syncthreads();
-      border = select(listed, false, 0, __dmul_rn(static_cast<double>(p), static_cast<double>(none)),
-                      border);
-      stage = 2;
-    } else if (count && by_mass) {
-      // the second stage's tokens: at or above this border
-      floor_key = border;
-      const float v = key_float(static_cast<uint32_t>(border >> 32));
-      const int at = bin_of(__fmul_rn(__fsub_rn(v, sc.max), sc.inv));
-      sure = min(sure, at);
-      last = min(last, at);
-      cluster_barrier();  // the list is read: its memory may be bins again
-      continue;
-    }
-    // the list's kept tokens join their groups
-    if (tid < kSampleWarps) sh.joined[tid] = 0;
-    __syncthreads();
-    bool left = false;
-    for (int i = tid; i < listed; i += kSampleThreads) {
-      const unsigned long long key = scr.list.key[i], w = scr.list.w[i];
-      if (key < border) {
-        left = true;
-        continue;
-      }
-      const int id = argmax_key_index(key);
-      if (part.owner(id) == rank) {
-        const int c = (id - part.first) / E, of = c / seg.per;
-        atomicAdd(&sh.groups[of][(c - of * seg.per) / (32 * seg.rounds)], w);
-        atomicAdd(&sh.joined[of], w);
-      }
-    }
-    if (!__syncthreads_or(left) && !dropped) border = 0;
-    own += sh.joined[warp];
-  }
-  st.border = border;
-  st.own = own;
-  return false;
-}
-
-// A cluster takes a row at a time.  Its logits are read twice or a few times
-// more, once from HBM: no more rows are under way than L2 holds.  Measured
-// (GB300) ...
 template <typename T, bool VERIFY, bool FILTERS>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
+  extern __shared__ __align__(16) unsigned char held[];
   __shared__ SampleShared sh;
-  extern __shared__ __align__(16) uint4 ring[];
-  __shared__ __align__(16) unsigned char scratch[FILTERS ? sizeof(Scratch) : 16];
   constexpr int E = Part<T>::E;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int cluster = a.cluster, rank = cluster_ctarank();
   int parity = 0;
   cluster_barrier();  // no CTA's shared memory is written to before it has started
   grid_dep_wait();
-  const int step = gridDim.x / cluster;
-  for (int r = blockIdx.x / cluster; r < a.rows; r += step) {
-    __syncthreads();  // whoever is still at the row before
-    // the row's request, its filters, and the draft that it judges
-    int q = r, draft = -1;
-    bool judges = false;
-    if (VERIFY) {
-      int lo = 0, hi = a.B;  // the last request whose window starts at or before r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.cu_in[mid] <= r) lo = mid;
-        else hi = mid;
-      }
-      q = lo;
-      const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
-      if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) continue;  // the whole cluster
-      judges = r + 1 < w1;
-      draft = judges ? a.ids[r + 1] : -1;
+  grid_dep_launch();
+  const int r = blockIdx.x / cluster;
+  // the row's request, its filters, and the draft that it judges
+  int q = r, draft = -1;
+  bool judges = false;
+  if (VERIFY) {
+    int lo = 0, hi = a.B;  // the last request whose window starts at or before r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.cu_in[mid] <= r) lo = mid;
+      else hi = mid;
     }
-    const float temp = a.temperature ? a.temperature[q] : 1.f;
-    float inv = __fdiv_rn(1.f, temp);
-    const bool greedy = !(temp > 0.f) || isinf(inv);
-    if (greedy) inv = 0.f;
+    q = lo;
+    const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
+    if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) return;  // the whole cluster
+    judges = r + 1 < w1;
+    draft = judges ? a.ids[r + 1] : -1;
+  }
+  const float temp = a.temperature ? a.temperature[q] : 1.f;
+  float inv = __fdiv_rn(1.f, temp);
+  const bool greedy = !(temp > 0.f) || isinf(inv);
+  if (greedy) inv = 0.f;
+  const float p = a.top_p ? a.top_p[q] : 1.f;
+  int k = a.top_k ? a.top_k[q] : 0;
+  if (p <= 0.f) k = 1;  // top-p of nothing: the first token alone
+  const bool by_count = k > 0 && k < a.V;
+  const bool by_mass = p < 1.f && p > 0.f;
+  float min_p = a.min_p ? a.min_p[q] : 0.f;
+  min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;  // NaN: 0
+  const bool by_share = min_p > 2.328306436538696e-10f;  // 2^-32: W > 0 implies e >= 2^-32
 
-    const T* row = static_cast<const T*>(a.logits) + r * a.stride;
-    const Part<T> part = part_of(row, a.V, cluster, rank);
-    // a greedy draft that this row may reject has no share
-    const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
-    const bool no_draw = VERIFY && judges && !a.greedy_drafts;
-    float top = -INFINITY;
-    each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks,
-                  [&](const uint4& v, int) { top = fmaxf(top, largest_of<T>(v)); });
-    unsigned long long x = float_order_key(top + 0.f), y = 0;
-    cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
-    RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
-    float most = INFINITY;
-    if (sc.max == INFINITY) sc.max = most = kLargest;
-
-    if (sc.max == -INFINITY) {
-      if (rank == 0 && tid == 0) store_row(a, VERIFY, r, sc, 0, 0, -1, -INFINITY);
-      continue;
-    }
-    if (greedy) {
-      // the lowest id of the largest logit, and whether any other logit is finite
-      unsigned long long best = 0, others = 0;
-      each_chunk(ring, row, a.V, part, tid, kSampleThreads, part.chunks, [&](const uint4& v, int c) {
-        float l[E];
-        chunk_logits<T>(v, most, l);
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  const Part<T> part = part_of(row, a.V, cluster, rank);
+  uint4* mine = reinterpret_cast<uint4*>(held);
+  Scratch& scr = *reinterpret_cast<Scratch*>(held + static_cast<size_t>(part.per) * 16);
+  float top = -INFINITY;
+  constexpr int kFly = 6;  // chunks of a thread on their way
+  for (int c0 = tid; c0 < part.chunks; c0 += kFly * kSampleThreads) {
+    uint4 v[kFly];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (l[e] == sc.max) {
-            const unsigned long long key = token_key(l[e], part.first + c * E + e);
-            best = key > best ? key : best;
-          }
-          others += __fsub_rn(l[e], sc.max) > -INFINITY;
-        }
-      });
-      cluster_reduce<true>(sh.ex, parity, cluster, rank, best, others);
-      if (rank == 0 && tid == 0) {
-        const int id = argmax_key_index(best);
-        const bool drawn = id != left_out && !no_draw;
-        store_row(a, VERIFY, r, sc, others > 1 ? best : 0, weight_of(1.f), drawn ? id : -1,
-                  drawn ? 0.f : -INFINITY);
-      }
-      continue;
-    }
-    // The last kept token's key; 0: every token of W > 0 is kept.
-    unsigned long long border = 0;
-    const Segment seg = warp_segment(part.chunks);
-    unsigned long long own = 0;  // kept weight of this warp's segment
-    bool summed = false;
-    if constexpr (FILTERS) {
-      const float p = a.top_p ? a.top_p[q] : 1.f;
-      int k = a.top_k ? a.top_k[q] : 0;
-      if (p <= 0.f) k = 1;  // top-p of nothing: the first token alone
-      const bool by_count = k > 0 && k < a.V, by_mass = p < 1.f && p > 0.f;
-      float min_p = a.min_p ? a.min_p[q] : 0.f;
-      min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;         // NaN: 0
-      const bool by_share = min_p > 2.328306436538696e-10f;  // 2^-32: W > 0 implies e >= 2^-32
-      if (by_count || by_mass || by_share) {
-        RowState<T> st = {row,      r,       q,        draft, judges, k,    p,   min_p,
-                          by_count, by_mass, by_share, part,  sc,     most, top, parity, 0, 0};
-        const bool done = filter_row<T, VERIFY>(a, sh, *reinterpret_cast<Scratch*>(scratch), ring, st);
-        parity = st.parity;
-        if (done) continue;
-        border = st.border;
-        own = st.own;
-        summed = true;
-      }
-    }
-    const float cut = border ? key_float(static_cast<uint32_t>(border >> 32)) : -INFINITY;
-    const int cut_token = border ? argmax_key_index(border) : a.V - 1;
-    if (!summed)
-      own = sum_groups(ring, row, a.V, part, seg, most, sh.groups[warp],
-                       [&](float v, int) { return weight_of(exp_of(v, sc)); });
-    if (lane == 0) sh.warp_mass[warp] = own;
-    unsigned long long total = lane == 0 ? own : 0, none = 0;
-    const int par = parity;
-    cluster_reduce<false>(sh.ex, parity, cluster, rank, total, none);
-    const long long all = static_cast<long long>(total);
-    long long share = all, out = 0;  // what is drawn from, and what is left out of it
-    if (left_out >= 0) {
-      const float v = raw_logit(row + left_out);
-      if (is_kept(v, left_out, cut, cut_token)) out = weight_of(exp_of(v, sc));
-      share -= out;
-    }
-    if (share <= 0 || no_draw) {
-      if (rank == 0 && tid == 0) store_row(a, VERIFY, r, sc, border, all, -1, -INFINITY);
-      continue;
-    }
-    long long at = place_of(a.u[q], share);
-    // where the left out weight is: CTA, warp, group
-    const int of = out ? part.owner(left_out) : -1;
-    const int oc = of == rank ? (left_out - part.first) / E : 0, ow = of == rank ? oc / seg.per : -1;
-    const int og = ow == warp ? (oc - ow * seg.per) / (32 * seg.rounds) : -1;
-    for (int i = 0; i < rank; ++i)
-      at -= static_cast<long long>(sh.ex.slot[par][0][i]) - (i == of ? out : 0);
-    for (int i = 0; i < warp; ++i)
-      at -= static_cast<long long>(sh.warp_mass[i]) - (i == ow ? out : 0);
-    if (at >= 0 && at < static_cast<long long>(own) - (warp == ow ? out : 0)) {
-      const int i = find_in_groups(
-          row, a.V, part, seg, most, sh.groups[warp], at,
-          [&](int g) { return g == og ? static_cast<unsigned long long>(out) : 0ull; },
-          [&](float v, int i) -> uint32_t {
-            const int id = part.first + i;
-            return is_kept(v, id, cut, cut_token) && id != left_out ? weight_of(exp_of(v, sc)) : 0u;
-          });
-      if (i >= 0) {
-        const int token = part.first + i;
-        store_row(a, VERIFY, r, sc, border, all, token,
-                  VERIFY ? 0.f : logprob_of(raw_logit(row + token), sc, all));
-      }
+    for (int i = 0; i < kFly; ++i)
+      if (c0 + i * kSampleThreads < part.chunks)
+        v[i] = load_chunk(row, a.V, part.first + (c0 + i * kSampleThreads) * E);
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int c = c0 + i * kSampleThreads;
+      if (c >= part.chunks) break;
+      mine[c] = v[i];
+      top = fmaxf(top, largest_of<T>(v[i]));
     }
   }
-  grid_dep_launch();
+  unsigned long long x = float_order_key(top + 0.f), y = 0;
+  cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
+  RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
+  float most = INFINITY;
+  if (sc.max == INFINITY) {
+    sc.max = most = kLargest;
+    if constexpr (sizeof(T) == 4) {
+      for (int c = tid; c < part.chunks; c += kSampleThreads) {
+        const uint4 v = mine[c];
+        mine[c] = make_uint4(__float_as_uint(at_most(__uint_as_float(v.x), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.y), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.z), most)),
+                             __float_as_uint(at_most(__uint_as_float(v.w), most)));
+      }
+      __syncthreads();
+    }
+  }
+
+  // Every element of this CTA, in no order: test(logit, id).
+  auto each = [&](auto&& test) {
+#pragma unroll 2
+    for (int c = tid; c < part.chunks; c += kSampleThreads) {
+      float v[E];
+      chunk_logits<T>(mine + c, most, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) test(v[e], c * E + e);
+    }
+  };
+
+  // The last kept token's key; 0: every token of W > 0 is kept.
+  unsigned long long border = 0;
+  const Segment seg = warp_segment(part.chunks);
+  unsigned long long own = 0;      // kept weight of this warp's segment
+  bool summed = false;             // ... and is it there yet
+  unsigned long long best = 0;     // a greedy row's token
+  if (sc.max > -INFINITY && greedy) {
+    // the lowest id of the largest logit, and whether any other logit is finite
+    unsigned long long others = 0;
+    each([&](float v, int i) {
+      if (v == sc.max) {
+        const unsigned long long key = token_key(v, part.first + i);
+        best = key > best ? key : best;
+      }
+      others += __fsub_rn(v, sc.max) > -INFINITY;
+    });
+    cluster_reduce<true>(sh.ex, parity, cluster, rank, best, others);
+    border = others > 1 ? best : 0;
+  } else if (FILTERS && sc.max > -INFINITY && (by_count || by_mass || by_share)) {
+    // Which tokens pass the filters other than the one that is being applied:
+    // bins below `sure` do, bins above `last` do not, the rest are looked at.
+    int sure = kSure, last = kBins - 1;
+    if (by_share) {
+      const int at = bin_of(logf(min_p));
+      sure = min(sure, at - 2);
+      last = min(last, at + 2);
+    }
+    unsigned long long floor_key = 0;
+    bool short_of = false;  // some token of W > 0 is kept by no stage so far
+    auto able = [&](float v, float z, int bin, int i) {
+      if (bin < sure) return true;
+      if (bin > last) return false;
+      const float e = expf(z);
+      return weight_of(e) > 0 && e >= min_p && token_key(v, part.first + i) >= floor_key;
+    };
+    auto clear_bins = [&]() {
+      for (int i = tid; i < kBins; i += kSampleThreads) scr.bins[0][i] = scr.bins[1][i] = 0;
+      __syncthreads();
+    };
+    // The bin, and within it the range of keys, that a limit falls into, and
+    // the measure of what comes before.
+    auto histogram = [&](bool count, auto&& place) {
+      clear_bins();
+      each([&](float v, int i) {
+        const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
+        const int bin = bin_of(z);
+        const int at = place(v, bin, i);
+        if (at < 0) return;
+        if (!able(v, z, bin, i)) {
+          short_of = short_of || bin < kSure || weight_of(expf(z)) > 0;
+          return;
+        }
+        if (count) {
+          atomicAdd(&scr.bins[0][at], 1u);
+        } else {
+          const uint32_t w = weight_of(expf(z));
+          atomicAdd(&scr.bins[0][at], w & 0xffffu);  // at most 2^16 elements a CTA
+          atomicAdd(&scr.bins[1][at], w >> 16);
+        }
+      });
+      cluster_barrier();
+    };
+    // Every CTA adds up its share of the bins over the cluster; whoever finds
+    // the limit tells the others.  `limit` gets the measure of all bins.
+    auto search = [&](bool count, unsigned long long base, auto&& limit) {
+      constexpr int kMost = (kBins + kSampleThreads - 1) / kSampleThreads;
+      const int share = (kBins + cluster - 1) / cluster, lo = rank * share;
+      const int each_bins = (share + kSampleThreads - 1) / kSampleThreads;
+      unsigned long long v[kMost], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        v[j] = 0;
+        const int at = tid * each_bins + j;
+        if (j < each_bins && at < share && lo + at < kBins) {
+          uint32_t l[kMostCluster] = {}, h[kMostCluster] = {};
+#pragma unroll
+          for (int c = 0; c < kMostCluster; ++c)
+            if (c < cluster) {
+              const uint32_t* from = cluster_pointer(&scr.bins[0][lo + at], c);
+              l[c] = from[0];
+              if (!count) h[c] = from[kBins];
+            }
+#pragma unroll
+          for (int c = 0; c < kMostCluster; ++c)
+            v[j] += l[c] + (static_cast<unsigned long long>(h[c]) << 16);
+        }
+        sum += v[j];
+      }
+      const unsigned long long run = warp_scan_u64(sum);
+      if (lane == 31) sh.scan[warp] = run;
+      unsigned long long all = sum, none = 0;
+      const int par = parity;
+      cluster_reduce<false>(sh.ex, parity, cluster, rank, all, none);
+      unsigned long long before = base + run - sum;
+      for (int i = 0; i < rank; ++i) before += sh.ex.slot[par][0][i];
+      for (int i = 0; i < warp; ++i) before += sh.scan[i];
+      const double stop = limit(all);
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        if (v[j] && static_cast<double>(before) < stop &&
+            !(static_cast<double>(before + v[j]) < stop))
+          for (int c = 0; c < cluster; ++c) {
+            const uint32_t to = cluster_map_shared(smem_u32(&sh.found), c);
+            st_cluster_u64(to, before);
+            st_cluster_u64(to + 8, v[j]);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 24),
+                         "r"(lo + tid * each_bins + j)
+                         : "memory");
+          }
+        before += v[j];
+      }
+      cluster_barrier();
+      Found f = sh.found;
+      f.all = all;
+      return f;
+    };
+    // The last token of `listed` ones before which the measure is below the
+    // limit: eight bits of the keys at a time.  Every CTA has the whole list.
+    auto select = [&](int listed, bool count, unsigned long long base, double stop,
+                      unsigned long long floor) {
+      constexpr int kEach = (kListed + kSampleThreads - 1) / kSampleThreads;
+      unsigned long long key[kEach];
+      uint32_t w[kEach];
+      bool on[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = tid + j * kSampleThreads;
+        on[j] = i < listed;
+        key[j] = on[j] ? scr.list.key[i] : 0;
+        w[j] = on[j] ? scr.list.w[i] : 0;
+        on[j] = on[j] && key[j] >= floor;
+      }
+      // what all keys have in common is skipped
+      uint32_t hi_differ = 0, lo_differ = 0;
+      const unsigned long long some = scr.list.key[0];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (on[j]) {
+          hi_differ |= static_cast<uint32_t>((key[j] ^ some) >> 32);
+          lo_differ |= static_cast<uint32_t>(key[j] ^ some);
+        }
+      if (tid == 0) sh.differ[0] = sh.differ[1] = 0;
+      __syncthreads();
+      hi_differ = __reduce_or_sync(0xffffffffu, hi_differ);
+      lo_differ = __reduce_or_sync(0xffffffffu, lo_differ);
+      if (lane == 0 && hi_differ) atomicOr(&sh.differ[0], hi_differ);
+      if (lane == 0 && lo_differ) atomicOr(&sh.differ[1], lo_differ);
+      __syncthreads();
+      const int bits = sh.differ[0] ? 64 - __clz(sh.differ[0]) : 32 - __clz(sh.differ[1]);
+      const int first_shift = bits <= 8 ? 0 : (bits + 7) / 8 * 8 - 8;
+      unsigned long long result =
+          first_shift >= 56 ? 0 : some >> (first_shift + 8) << (first_shift + 8);
+      for (int shift = first_shift; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kSampleThreads)
+          scr.list.digits[0][i] = scr.list.digits[1][i] = scr.list.digits[2][i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (on[j]) {
+            const int d = static_cast<int>(key[j] >> shift) & 255;
+            atomicAdd(&scr.list.digits[0][d], 1u);
+            atomicAdd(&scr.list.digits[1][d], w[j] & 0xffffu);
+            atomicAdd(&scr.list.digits[2][d], w[j] >> 16);
+          }
+        __syncthreads();
+        if (warp == 0) {
+          // lane 0 has the largest digits
+          unsigned long long v[8], sum = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = 255 - lane * 8 - i;
+            v[i] = count ? scr.list.digits[0][d]
+                         : scr.list.digits[1][d] + (static_cast<unsigned long long>(scr.list.digits[2][d]) << 16);
+            sum += v[i];
+          }
+          unsigned long long before = base + warp_scan_u64(sum) - sum;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (v[i] && static_cast<double>(before) < stop &&
+                !(static_cast<double>(before + v[i]) < stop)) {
+              sh.digit = 255 - lane * 8 - i;
+              sh.digit_before = before;
+              sh.digit_inside = scr.list.digits[0][255 - lane * 8 - i];
+            }
+            before += v[i];
+          }
+        }
+        __syncthreads();
+        const unsigned long long d = static_cast<unsigned long long>(sh.digit);
+        base = sh.digit_before;
+        result |= d << shift;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) on[j] = on[j] && ((key[j] >> shift) & 255) == d;
+        if (sh.digit_inside == 1) {
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            if (on[j]) sh.found.before = key[j];
+          __syncthreads();
+          result = sh.found.before;
+          break;
+        }
+        __syncthreads();
+      }
+      return result;
+    };
+
+    // Where the filters keep few tokens, they are all among a few.  Of at
+    // least `guess` threads the largest logit is in the bin that is found, or
+    // before it, so at least as many tokens are.
+    const int guess = by_count ? k : kGuess;
+    bool done = false;
+    if (!by_count && !by_mass) {
+      // min-p alone: a look at each token is enough
+      own = 0;
+      unsigned long long last_key = ~0ull, short_n = 0;
+      for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+        float v[E];
+        chunk_logits<T>(mine + c, most, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float z = __fmul_rn(__fsub_rn(v[e], sc.max), sc.inv);
+          const int bin = bin_of(z);
+          if (bin >= kBins) continue;
+          if (able(v[e], z, bin, c * E + e)) {
+            own += weight_of(expf(z));
+            const unsigned long long key = token_key(v[e], part.first + c * E + e);
+            last_key = key < last_key ? key : last_key;
+          } else {
+            short_n |= bin < kSure || weight_of(expf(z)) > 0;
+          }
+        }
+      }
+      own = warp_sum_u64(own);
+      if (lane == 0) sh.warp_mass[warp] = own;
+      unsigned long long inverse = ~last_key;
+      cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, short_n);
+      border = short_n ? ~inverse : 0;
+      done = summed = true;
+    } else if (by_count && guess <= kMostGuess) {
+      clear_bins();
+      if (tid == 0) sh.listed = 0;
+      const float tv = at_most(top, most), tz = __fmul_rn(__fsub_rn(tv, sc.max), sc.inv);
+      const int tb = bin_of(tz);
+      if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[0][tb], 1u);
+      cluster_barrier();
+      const Found f = search(true, 0, [&](unsigned long long all) {
+        return fmin(static_cast<double>(guess), static_cast<double>(all));
+      });
+      const int hi_bin = f.all < guess ? kBins - 1 : f.bin;
+      unsigned long long n = 0, mass = 0, list_mass = 0;
+      bool rest = false;
+      each([&](float v, int i) {
+        const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
+        const int bin = bin_of(z);
+        if (bin > hi_bin && by_count) {
+          rest = rest || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
+          return;
+        }
+        if (bin >= kBins) return;
+        const uint32_t w = weight_of(expf(z));
+        if (!able(v, z, bin, i)) {
+          rest = rest || w > 0;
+          return;
+        }
+        mass += w;
+        if (bin > hi_bin) {
+          rest = rest || w > 0;
+          return;
+        }
+        list_mass += w;
+        const int at = atomicAdd(&sh.listed, 1);
+        if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(i);
+      });
+      __syncthreads();
+      n = (tid == 0 ? static_cast<unsigned>(sh.listed) : 0u) | (rest ? 1ull << 32 : 0ull);
+      const int par = parity;
+      cluster_reduce<false>(sh.ex, parity, cluster, rank, n, mass, list_mass);
+      const int listed = static_cast<int>(n & 0xffffffffu);
+      rest = n >> 32;
+      const double stop = __dmul_rn(static_cast<double>(p), static_cast<double>(mass));
+      if (listed <= kListed && (by_count || !(static_cast<double>(list_mass) < stop))) {
+        // everything that is kept is listed: the first CTA does the rest, and
+        // the others go on
+        int at = 0;
+        for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i] & 0xffffffffu);
+        const int here = static_cast<int>(sh.ex.slot[par][0][rank] & 0xffffffffu);
+        for (int j = tid; j < here; j += kSampleThreads) {
+          const int el = scr.list.own[j];
+          const float xv = held_logit<T>(held, el, most);
+          st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), 0),
+                         token_key(xv, part.first + el));
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                           cluster_map_shared(smem_u32(&scr.list.w[at + j]), 0)),
+                       "r"(weight_of(exp_of(xv, sc)))
+                       : "memory");
+        }
+        cluster_barrier();
+        if (rank == 0) {
+          const ListRow lr = {listed, by_count ? min(k, listed) : listed, by_count, by_mass,
+                              rest,   static_cast<double>(p),            stop};
+          const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
+          draw_from_list<T, VERIFY>(a, sh, scr.list, lr, sc, r, q, row, left_out,
+                                    VERIFY && judges && !a.greedy_drafts);
+        }
+        return;
+      }
+    }
+
+    // by number (top-k), by weight (top-p), or one after the other
+    for (int stage = by_count ? 0 : 1; stage < (by_mass ? 2 : 1) && !done; ++stage) {
+      const bool count = stage == 0;
+      double stop = 0.0;
+      auto limit = [&](unsigned long long all) {
+        const double n = static_cast<double>(all);
+        return stop = count ? fmin(static_cast<double>(k), n) : __dmul_rn(static_cast<double>(p), n);
+      };
+      histogram(count, [&](float, int bin, int) { return bin < kBins ? bin : -1; });
+      Found f = search(count, 0, limit);
+      // (weights of what passes sum to more than 0 each, so both measures tell)
+      short_of = short_of || f.before + f.inside < f.all;
+      unsigned long long low = 0, high = ~0ull;  // keys within the bin
+      int lo_bin = f.bin;
+      if (count && f.before + f.inside <= kListed) {
+        lo_bin = 0;  // few tokens in all: rank every one
+        f.before = 0;
+      }
+      const int hi_bin = f.bin;
+      int listed;
+      unsigned long long dropped;  // somewhere in the range's bin, or short_of
+      // (each further level has 2^-10 of the keys of the one before, of 2^64)
+      for (int level = 0; level < 8; ++level) {
+        // weights before the range, by segments; the range's own tokens
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        own = 0;
+        bool drop = short_of;
+        unsigned long long first_key = 0, last_key = ~0ull;
+        for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+          float v[E];
+          chunk_logits<T>(mine + c, most, v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float z = __fmul_rn(__fsub_rn(v[e], sc.max), sc.inv);
+            const int bin = bin_of(z);
+            if (bin > hi_bin || !able(v[e], z, bin, c * E + e)) continue;
+            if (bin < lo_bin) {
+              own += weight_of(expf(z));
+              continue;
+            }
+            const unsigned long long key = token_key(v[e], part.first + c * E + e);
+            if (key > high) {
+              own += weight_of(expf(z));
+            } else if (key < low) {
+              drop = true;
+            } else {
+              last_key = key < last_key ? key : last_key;
+              first_key = key > first_key ? key : first_key;
+              const int at = atomicAdd(&sh.listed, 1);
+              if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(c * E + e);
+            }
+          }
+        }
+        __syncthreads();
+        unsigned long long n = static_cast<unsigned long long>(tid == 0 ? sh.listed : 0);
+        dropped = drop;
+        const int par = parity;
+        cluster_reduce<false>(sh.ex, parity, cluster, rank, n, dropped);
+        listed = static_cast<int>(n);
+        if (listed <= kListed) {
+          int at = 0;
+          for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i]);
+          const int here = static_cast<int>(sh.ex.slot[par][0][rank]);
+          for (int i = tid; i < here * cluster; i += kSampleThreads) {
+            const int to = i / here, j = i % here, el = scr.list.own[j];
+            const float xv = held_logit<T>(held, el, most);
+            st_cluster_u64(cluster_map_shared(smem_u32(&scr.list.key[at + j]), to),
+                           token_key(xv, part.first + el));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                             cluster_map_shared(smem_u32(&scr.list.w[at + j]), to)),
+                         "r"(weight_of(exp_of(xv, sc)))
+                         : "memory");
+          }
+          cluster_barrier();
+          break;
+        }
+        // too many to rank: bins of the range's keys (ties go by their ids)
+        unsigned long long inverse = ~last_key;
+        cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, dropped);
+        low = ~inverse;
+        unsigned long long none = 0;
+        cluster_reduce<true>(sh.ex, parity, cluster, rank, first_key, none);
+        high = first_key;
+        int shift = 0;
+        while (shift < 54 && ((high - low) >> shift) >= kBins) ++shift;
+        lo_bin = hi_bin;  // (the range is that bin's: lists of all bins are short)
+        const unsigned long long lowest = low, highest = high;
+        histogram(count, [&](float v, int bin, int i) {
+          if (bin != hi_bin) return -1;
+          const unsigned long long key = token_key(v, part.first + i);
+          return key < lowest || key > highest ? -1 : static_cast<int>((highest - key) >> shift);
+        });
+        f = search(count, f.before, [&](unsigned long long) { return stop; });
+        high = highest - (static_cast<unsigned long long>(f.bin) << shift);
+        const unsigned long long end = high - ((1ull << shift) - 1);
+        low = end > lowest && end <= high ? end : lowest;
+      }
+      listed = min(listed, kListed);
+      border = select(listed, count, f.before, stop, 0);
+      if (count && by_mass && lo_bin == 0 && listed <= kListed && hi_bin == f.bin && high == ~0ull) {
+        // all that is left is in the list: the weights' limit in it
+        unsigned long long mass = 0, none = 0;
+        for (int i = tid; i < listed; i += kSampleThreads)
+          if (scr.list.key[i] >= border) mass += scr.list.w[i];
+        mass = warp_sum_u64(mass);
+        if (lane == 0) sh.scan[warp] = mass;
+        __syncthreads();
+        for (int i = 0; i < kSampleWarps; ++i) none += sh.scan[i];
+        __syncthreads();
+        border = select(listed, false, 0, __dmul_rn(static_cast<double>(p), static_cast<double>(none)),
+                        border);
+        stage = 2;
+      } else if (count && by_mass) {
+        // the second stage's tokens: at or above this border
+        floor_key = border;
+        const float v = key_float(static_cast<uint32_t>(border >> 32));
+        const int at = bin_of(__fmul_rn(__fsub_rn(v, sc.max), sc.inv));
+        sure = min(sure, at);
+        last = min(last, at);
+        cluster_barrier();  // the list is read: its memory may be bins again
+        continue;
+      }
+      // the list's kept tokens join their segments
+      __syncthreads();
+      own = warp_sum_u64(own);
+      if (lane == 0) sh.warp_mass[warp] = own;
+      __syncthreads();
+      const int per = warp_segment_size(part.chunks);
+      bool left = false;
+      for (int i = tid; i < listed; i += kSampleThreads) {
+        const unsigned long long key = scr.list.key[i], w = scr.list.w[i];
+        if (key < border) {
+          left = true;
+          continue;
+        }
+        const int id = argmax_key_index(key);
+        if (part.owner(id) == rank) atomicAdd(&sh.warp_mass[(id - part.first) / E / per], w);
+      }
+      if (!__syncthreads_or(left) && !dropped) border = 0;
+      own = sh.warp_mass[warp];
+      summed = true;
+    }
+  }
+  const float cut = border ? key_float(static_cast<uint32_t>(border >> 32)) : -INFINITY;
+  const int cut_token = border ? argmax_key_index(border) : a.V - 1;
+
+  // Draw.  A greedy draft that this row may reject has no share.
+  const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
+  auto weight = [&](int c, int e) -> uint32_t {
+    const float v = held_logit<T>(held, c * E + e, most);
+    const int id = part.first + c * E + e;
+    if (!is_kept(v, id, cut, cut_token) || id == left_out) return 0;
+    return weight_of(exp_of(v, sc));
+  };
+  if (!summed) {
+    // every token, or a greedy row's one
+    own = 0;
+    if (!greedy) {
+#pragma unroll 2
+      for (int c = seg.lo + lane; c < seg.hi; c += 32) {
+        float v[E];
+        chunk_logits<T>(mine + c, most, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) own += weight_of(exp_of(v[e], sc));
+      }
+    } else if (sc.max > -INFINITY && part.owner(argmax_key_index(best)) == rank) {
+      const int at = (argmax_key_index(best) - part.first) / E;
+      if (at / warp_segment_size(part.chunks) == warp && lane == 0) own = weight_of(1.f);
+    }
+    own = warp_sum_u64(own);
+    if (lane == 0) sh.warp_mass[warp] = own;
+  }
+  unsigned long long total = lane == 0 ? own : 0, none = 0;
+  const int par = parity;
+  cluster_reduce<false>(sh.ex, parity, cluster, rank, total, none);
+  const long long all = static_cast<long long>(total);
+  long long share = all, out = 0;  // what is drawn from, and what is left out of it
+  if (left_out >= 0) {
+    const float v = raw_logit(row + left_out);
+    if (is_kept(v, left_out, cut, cut_token)) out = weight_of(exp_of(v, sc));
+    share -= out;
+  }
+  const bool draws = share > 0 && !(VERIFY && judges && !a.greedy_drafts);
+  int token = -1;
+  if (draws) {
+    long long at = place_of(a.u[q], share);
+    const int of = out ? part.owner(left_out) : -1;
+    for (int i = 0; i < rank; ++i)
+      at -= static_cast<long long>(sh.ex.slot[par][0][i]) - (i == of ? out : 0);
+    const int in = of == rank ? (left_out - part.first) / E / warp_segment_size(part.chunks) : -1;
+    for (int i = 0; i < warp; ++i)
+      at -= static_cast<long long>(sh.warp_mass[i]) - (i == in ? out : 0);
+    if (at >= 0 && at < static_cast<long long>(own) - (warp == in ? out : 0)) {
+      const int i = find_in_segment<E>(seg, at, weight);
+      if (i >= 0) token = part.first + i;
+    }
+  }
+  if (token >= 0 || (!draws && rank == 0 && tid == 0))
+    store_row(a, VERIFY, r, sc, border, all, token,
+              token >= 0 && !VERIFY ? logprob_of(raw_logit(row + token), sc, all) : -INFINITY);
 }
 
 // -------------------------------------------------------------- verification
@@ -1215,43 +1071,6 @@ template <typename T>
 __device__ __forceinline__ uint32_t dist_weight(float x, int id, const pe_dist& d) {
   if (!is_kept(x, id, d.cut, d.cut_token)) return 0;
   return weight_of(exp_of(x, RowScale{d.max, d.inv}));
-}
-
-// Contiguous chunks of a warp, and the element at which weights in shared memory
-// first exceed `at`: the lane's part that holds it, then the element.
-__device__ __forceinline__ Segment held_segment(int chunks) {
-  const int per = (chunks + kSampleWarps - 1) / kSampleWarps;
-  const int lo = min(static_cast<int>(threadIdx.x) / 32 * per, chunks);
-  return Segment{lo, min(lo + per, chunks), 1, per};
-}
-template <int E, typename W>
-__device__ __forceinline__ int find_in_segment(Segment seg, long long at, W&& weight) {
-  const int lane = threadIdx.x % 32;
-  const int per = (seg.hi - seg.lo + 31) / 32;
-  const int lo = min(seg.lo + lane * per, seg.hi), hi = min(lo + per, seg.hi);
-  unsigned long long own = 0;
-  for (int c = lo; c < hi; ++c)
-#pragma unroll
-    for (int e = 0; e < E; ++e) own += weight(c, e);
-  const unsigned long long run = warp_scan_u64(own);
-  const unsigned hit = __ballot_sync(0xffffffffu, static_cast<long long>(run) > at);
-  if (hit == 0) return -1;  // not reached: the sums agree
-  const int who = __ffs(hit) - 1;
-  at -= static_cast<long long>(__shfl_sync(0xffffffffu, run - own, who));
-  const int from = __shfl_sync(0xffffffffu, lo, who) * E, to = __shfl_sync(0xffffffffu, hi, who) * E;
-  for (int i0 = from; i0 < to; i0 += 32) {
-    const int i = i0 + lane;
-    const unsigned long long w = i < to ? weight(i / E, i % E) : 0u;
-    const unsigned long long sum = warp_scan_u64(w);
-    const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31));
-    if (at >= all) {
-      at -= all;
-      continue;
-    }
-    const unsigned h = __ballot_sync(0xffffffffu, static_cast<long long>(sum) > at);
-    return lane == __ffs(h) - 1 ? i : -1;
-  }
-  return -1;
 }
 
 // A cluster a request: its first rejected draft, and the token drawn there.
@@ -1336,16 +1155,15 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
       n = __float2uint_rn(pw);
       m = __float2uint_rn(fmaxf(__fsub_rn(pw, __fmul_rn(static_cast<float>(wq), aq)), 0.f));
     };
-    const Segment seg = held_segment(part.chunks);
+    const Segment seg = warp_segment(part.chunks);
     unsigned long long more = 0, plain = 0;
 #pragma unroll 2
     for (int c = seg.lo + lane; c < seg.hi; c += 32) {
       const int first = part.first + c * E;
-      const bool whole = c >= part.lo && c < part.hi;
-      const uint4 pv = whole ? load_whole(row, first) : load_ragged(row, a.V, first);
+      const uint4 pv = load_chunk(row, a.V, first);
       uint4 qv;
-      if (alike && whole) {
-        qv = load_whole(qrow, first);
+      if (alike) {
+        qv = load_chunk(qrow, a.V, first);
       } else {
         uint32_t w[4];
         auto bits = [&](int e) -> uint32_t {
@@ -1359,8 +1177,8 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
         qv = make_uint4(w[0], w[1], w[2], w[3]);
       }
       float px[E], qx[E];
-      chunk_logits<T>(pv, INFINITY, px);
-      chunk_logits<T>(qv, INFINITY, qx);
+      chunk_logits<T>(&pv, INFINITY, px);
+      chunk_logits<T>(&qv, INFINITY, qx);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         uint32_t m, n;
@@ -1426,60 +1244,38 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
 }
 
 // -------------------------------------------------------------------- launch
-// CTAs a row.  Few rows: as many as a cluster has, for the shortest way.  Many:
-// so many that the rows under way at a time, by two CTAs an SM, take half of
-// L2, or all rows do.
-static int sample_cluster(int rows, int V, int elem, int sms) {
-  constexpr double kL2 = 64e6;
-  const double row = static_cast<double>(V) * elem;
-  const long long ctas = 2LL * sms;
+// Two CTAs an SM, or one.
+constexpr size_t kHalfShared = 112 * 1024 - sizeof(SampleShared);
+constexpr size_t kMostShared = 226 * 1024 - sizeof(SampleShared);
+struct SampleShape {
+  int cluster;
+  size_t smem;
+};
+// Few rows: as many CTAs a row as a cluster has, for the shortest way; more
+// rows than that fills: as few as hold the row.
+static SampleShape sample_shape(int rows, int V, int elem, int sms) {
+  auto bytes = [&](int c) {
+    const int e = 16 / elem, all = (V + 2 * (e - 1)) / e;
+    return static_cast<size_t>((all + c - 1) / c) * 16 + sizeof(Scratch);
+  };
   int c = 1;
-  while (c < kMostCluster && std::min<double>(rows, static_cast<double>(ctas) / c) * row > kL2) c *= 2;
-  while (c < kMostCluster && static_cast<long long>(rows) * c * 2 <= ctas && row / c > 4096) c *= 2;
-  return c;
-}
-
-// Clusters that are resident at a time (a GPC's SMs need not be a multiple of
-// the cluster).  Asked once a process, device and kernel.
-template <typename T, bool VERIFY, bool FILTERS>
-static cudaError_t resident_rows(int cluster, int& n) {
-  static std::atomic<int> known[16][4];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const int c = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
-  std::atomic<int>* place = dev < 16 ? &known[dev][c] : nullptr;
-  n = place ? place->load(std::memory_order_relaxed) : 0;
-  if (n > 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(sample_rows_kernel<T, VERIFY, FILTERS>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
-  cfg.blockDim = dim3(kSampleThreads);
-  cfg.dynamicSmemBytes = kRingBytes;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(&n, sample_rows_kernel<T, VERIFY, FILTERS>, &cfg);
-  if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess && place) place->store(n, std::memory_order_relaxed);
-  return e;
+  while (c < kMostCluster && bytes(c) > kHalfShared) c *= 2;
+  while (c < kMostCluster && static_cast<long long>(rows) * c * 2 <= 2 * sms &&
+         bytes(c) > sizeof(Scratch) + 4096)
+    c *= 2;
+  return SampleShape{c, bytes(c)};
 }
 
 template <typename T, bool VERIFY, bool FILTERS>
 static cudaError_t launch_rows(SampleArgs a, int sms, cudaStream_t s) {
-  a.cluster = sample_cluster(a.rows, a.V, sizeof(T), sms);
-  int resident = 0;
-  const cudaError_t e = resident_rows<T, VERIFY, FILTERS>(a.cluster, resident);
+  const SampleShape sh = sample_shape(a.rows, a.V, sizeof(T), sms);
+  a.cluster = sh.cluster;
+  auto kernel = sample_rows_kernel<T, VERIFY, FILTERS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sh.smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(sample_rows_kernel<T, VERIFY, FILTERS>,
-                            dim3(static_cast<unsigned>(std::min(a.rows, resident)) * a.cluster),
-                            dim3(kSampleThreads), kRingBytes, s, a.cluster, a);
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.rows) * sh.cluster),
+                            dim3(kSampleThreads), sh.smem, s, sh.cluster, a);
 }
 // A call without top-k, top-p and min-p has a kernel without them: what they
 // need of registers costs every row, whether it has filters or not.
