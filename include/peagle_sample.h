@@ -69,7 +69,8 @@ typedef struct {
  * drafter's rows.
  * PE_ERR_INVALID_ARGUMENT: rows or vocab < 1, another dtype, a stride
  * shorter than a row, a null pointer, logits not aligned to their elements,
- * dist not 16-byte aligned.  PE_ERR_UNSUPPORTED: vocab past 393216. */
+ * dist not 16-byte aligned.  PE_ERR_UNSUPPORTED: vocab past 393216, rows past
+ * 2^27. */
 pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logits,
                     int64_t stride, const float* temperature, const int32_t* top_k,
                     const float* top_p, const float* min_p, const float* u, int32_t* tokens,
@@ -116,7 +117,7 @@ pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logi
  * Q = 0).
  * PE_ERR_INVALID_ARGUMENT: B < 1, T < B, vocab < 1, another dtype, a stride
  * shorter than a row, a null or misaligned pointer, draft_logits without
- * draft_dist.  PE_ERR_UNSUPPORTED: vocab past 393216. */
+ * draft_dist.  PE_ERR_UNSUPPORTED: vocab past 393216, T past 2^27. */
 pe_status pe_verify(int32_t B, int32_t T, int32_t vocab, int32_t dtype, const void* logits,
                     int64_t stride, const int32_t* ids, const int32_t* cu_in,
                     const float* temperature, const int32_t* top_k, const float* top_p,

@@ -58,7 +58,8 @@ pe_status pe_w4_quantize(const void* w, int32_t dtype, int64_t w_stride, int32_t
  * fp32 ones also to 2^-24 of themselves.  A row with an infinite or NaN
  * element gives infinities and NaN, the other rows are as they would be.
  * Made for a few rows: up to 32 cost one pass over the weights, each further
- * 32 another.
+ * 32 another (fewer where 32 rows of x do not fit into the shared memory of
+ * eight SMs).
  * PE_ERR_INVALID_ARGUMENT: rows < 1, sizes as pe_w4_pack, another
  * combination of types, a stride shorter than a row, a null pointer, packed
  * not 16-byte aligned, x or y not aligned to its elements. */

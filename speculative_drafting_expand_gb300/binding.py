@@ -851,6 +851,15 @@ def _op_call(index: int, stream, name, fn, *args) -> None:
         raise PeError(name, status)
 
 
+def _op_used(stream, *tensors) -> None:
+    """Memory that is freed after a call on `stream` is not handed out again
+    before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 class W4Weight:
     """A matrix [n, k] of 4-bit codes with a bfloat16 scale for each `group`
     (32, 64 or 128) inputs of a row, laid out for pe_w4_linear.  Entry (i, j)
@@ -873,6 +882,7 @@ class W4Weight:
                              "on the codes' device")
         _op_call(index, stream, "pe_w4_pack", lib().pe_w4_pack, ptr(codes), ptr(scales), n, k,
                  group, ptr(self.packed))
+        _op_used(stream, codes, scales)
 
     def _prepare(self, n, k, group, device, stream):
         torch = _torch()
@@ -898,6 +908,7 @@ class W4Weight:
         stride = _op_rows("weight", weight, n, k, self.index)
         _op_call(self.index, stream, "pe_w4_quantize", lib().pe_w4_quantize, ptr(weight), kind,
                  stride, n, k, group, ptr(self.packed))
+        _op_used(stream, weight)
         return self
 
 
@@ -918,6 +929,7 @@ def pe_w4_linear(w: W4Weight, x, out=None, out_dtype=None, stream=None):
     ys = _op_rows("out", out, rows, w.n, w.index)
     _op_call(w.index, stream, "pe_w4_linear", lib().pe_w4_linear, w.packed.data_ptr(), w.n, w.k,
              w.group, rows, kind, x.data_ptr(), xs, ok, out.data_ptr(), ys)
+    _op_used(stream, w.packed, x, out)
     return out
 
 
@@ -965,6 +977,7 @@ def pe_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
              stride, *filters, pu, _op_vector("tokens", tokens, rows, torch.int32, index),
              _op_vector("logprobs", logprobs, rows, torch.float32, index),
              _op_dist("dist", dist, rows, index))
+    _op_used(stream, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, dist)
     return tokens, logprobs, dist
 
 
@@ -1019,4 +1032,6 @@ def pe_verify(logits, ids, cu_in, accept_u, u, temperature=None, top_k=None, top
              _op_vector("sampled_ids", sampled_ids, B, i32, index),
              _op_vector("logprobs", logprobs, T, f32, index), _op_dist("dist", dist, T, index),
              None if err is None else _op_vector("err", err, 1, i32, index))
+    _op_used(stream, logits, ids, cu_in, accept_u, u, temperature, top_k, top_p, min_p,
+             draft_logits, draft_dist, num_accepted, sampled_ids, logprobs, dist, err)
     return num_accepted, sampled_ids, logprobs, dist

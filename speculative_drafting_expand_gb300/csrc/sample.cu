@@ -6,7 +6,6 @@
 // counts and sums of them are exact in 64 bits, whatever order the threads,
 // warps and CTAs add them in.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "../../include/peagle_sample.h"
@@ -127,51 +126,41 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
 }
 
 struct Exchange {
-  unsigned long long warp[3][kSampleWarps];
-  unsigned long long slot[2][3][kMostCluster];  // [parity][value][CTA]
+  unsigned long long warp[2][kSampleWarps];
+  unsigned long long slot[2][2][kMostCluster];  // [parity][value][CTA]
 };
 
-// Three 64-bit sums (or a maximum and two sums) over the cluster; every thread
-// gets them.  The CTAs' own values stay in ex.slot[parity].  One barrier: the
-// slots of the round before the last are free, because whoever has passed the
-// last barrier has read them.
+// Two 64-bit sums (or a maximum and a sum) over the cluster; every thread gets
+// them.  The CTAs' own values stay in ex.slot[parity].  One barrier: the slots
+// of the round before the last are free, because whoever has passed the last
+// barrier has read them.
 template <bool MAX>
 __device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cluster, int rank,
-                                               unsigned long long& a, unsigned long long& b,
-                                               unsigned long long& c) {
+                                               unsigned long long& a, unsigned long long& b) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   a = MAX ? warp_max_u64(a) : warp_sum_u64(a);
   b = warp_sum_u64(b);
-  c = warp_sum_u64(c);
   if (lane == 0) {
     ex.warp[0][warp] = a;
     ex.warp[1][warp] = b;
-    ex.warp[2][warp] = c;
   }
   __syncthreads();
-  if (warp < 3) {  // a warp a value
+  if (warp < 2) {  // a warp a value
     unsigned long long x = lane < kSampleWarps ? ex.warp[warp][lane] : 0;
     x = MAX && warp == 0 ? warp_max_u64(x) : warp_sum_u64(x);
     if (lane < cluster)
       st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][warp][rank]), lane), x);
   }
   cluster_barrier();
-  a = b = c = 0;
+  a = b = 0;
 #pragma unroll
   for (int r = 0; r < kMostCluster; ++r) {
     if (r >= cluster) break;
     const unsigned long long x = ex.slot[parity][0][r];
     a = MAX ? (x > a ? x : a) : a + x;
     b += ex.slot[parity][1][r];
-    c += ex.slot[parity][2][r];
   }
   parity ^= 1;
-}
-template <bool MAX>
-__device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cluster, int rank,
-                                               unsigned long long& a, unsigned long long& b) {
-  unsigned long long c = 0;
-  cluster_reduce<MAX>(ex, parity, cluster, rank, a, b, c);
 }
 
 // A CTA's part of a row: 16-byte chunks of the memory that the row lies in;
@@ -344,9 +333,10 @@ struct SampleShared {
   uint32_t differ[2];
 };
 
-// Tokens that top-p takes at the first try, and the most for which the threads'
-// largest logits are asked.
-constexpr int kGuess = 128;
+// The largest k for which the threads' largest logits are asked: past it the
+// threads of a row are too few for the k-th of theirs to be near the row's k-th.
+// (33 rows of 50,257 bf16 logits with mixed filters: 30 us, and 37 with 64 as
+// the limit.)
 constexpr int kMostGuess = 256;
 
 // A row's result.
@@ -368,15 +358,14 @@ __device__ __forceinline__ void store_row(const SampleArgs& a, bool verify, int 
   }
 }
 
-// A row whose kept tokens are all listed: `first` of the n listed ones pass
-// top-k, and of their weight top-p takes p (without top-k: of the row's, that
-// is up to `stop`).  By one CTA: every token's place and the weight before it
-// from a comparison with every other, several threads a token where there are
-// few.
+// A row whose tokens that pass top-k and min-p are the `first` first of the n
+// listed ones; of their weight top-p takes p.  By one CTA: every token's place
+// and the weight before it from a comparison with every other, several threads
+// a token where there are few.
 struct ListRow {
   int n, first;
-  bool by_count, by_mass, rest;  // rest: tokens of W > 0 are not listed
-  double p, stop;
+  bool by_mass, rest;  // rest: tokens of W > 0 are not listed
+  double p;
 };
 template <typename T, bool VERIFY>
 __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& sh, Listed& list,
@@ -409,8 +398,8 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
       before[s] += __shfl_xor_sync(0xffffffffu, before[s], m);
     }
   }
-  double stop = lr.stop;
-  if (lr.by_count && lr.by_mass) {
+  double stop = 0.0;
+  if (lr.by_mass) {
 #pragma unroll
     for (int s = 0; s < kEach; ++s)
       if (w[s] && place[s] + 1 == lr.first) sh.scan[0] = before[s] + w[s];
@@ -463,6 +452,25 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
   }
 }
 
+// A cluster a row.  W needs the row's largest logit before the first sum, and
+// each filter a look at every token more, so the row is read from HBM once and
+// stays in the cluster's shared memory: reading it again from L2 instead, in
+// smaller CTAs or through rings of asynchronous copies, took 192 us where this
+// takes 179 (448 rows of 201,088 fp32 logits by temperature, 2.0 TB/s).  What
+// bounds a row is the way through its steps, which wait on each other: the
+// copy, the largest, the sum, the draw, each behind a meeting of the cluster
+// (about 1.5 us), against which two CTAs of different rows share an SM.
+//
+// Filters look for the last kept token.  Weights and logits fall together, so
+// a histogram over falling logits has the sums "of the tokens before" at its
+// bins' borders; the limit's own bin (a 48th of a factor of two, a few tokens
+// of a usual row) is listed, and the limit found in it by the digits of the
+// keys; a bin with more than a list takes is cut by a further histogram of its
+// keys.  Additions to bins in shared memory bound that (15 cycles a warp's 32
+// where they are spread, two of them a token for sums of weights): 128 rows of
+// 151,936 fp32 logits with mixed filters take 106 us.  For top-k to kMostGuess
+// the histogram is of one logit a thread, and one CTA ranks what it lists: one
+// row 36 -> 22 us, the 128 mixed ones 131 -> 106 us.
 template <typename T, bool VERIFY, bool FILTERS>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
@@ -760,10 +768,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       return result;
     };
 
-    // Where the filters keep few tokens, they are all among a few.  Of at
-    // least `guess` threads the largest logit is in the bin that is found, or
-    // before it, so at least as many tokens are.
-    const int guess = by_count ? k : kGuess;
     bool done = false;
     if (!by_count && !by_mass) {
       // min-p alone: a look at each token is enough
@@ -792,7 +796,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       cluster_reduce<true>(sh.ex, parity, cluster, rank, inverse, short_n);
       border = short_n ? ~inverse : 0;
       done = summed = true;
-    } else if (by_count && guess <= kMostGuess) {
+    } else if (by_count && k <= kMostGuess) {
+      // Few tokens are kept, and they are among a few: of at least k threads the
+      // largest logit is in the bin that is found, or before it, so at least k
+      // tokens are.
       clear_bins();
       if (tid == 0) sh.listed = 0;
       const float tv = at_most(top, most), tz = __fmul_rn(__fsub_rn(tv, sc.max), sc.inv);
@@ -800,46 +807,30 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       if (tb < kBins && able(tv, tz, tb, 0)) atomicAdd(&scr.bins[0][tb], 1u);
       cluster_barrier();
       const Found f = search(true, 0, [&](unsigned long long all) {
-        return fmin(static_cast<double>(guess), static_cast<double>(all));
+        return fmin(static_cast<double>(k), static_cast<double>(all));
       });
-      const int hi_bin = f.all < guess ? kBins - 1 : f.bin;
-      unsigned long long n = 0, mass = 0, list_mass = 0;
+      const int hi_bin = f.all < k ? kBins - 1 : f.bin;
       bool rest = false;
       each([&](float v, int i) {
         const float z = __fmul_rn(__fsub_rn(v, sc.max), sc.inv);
         const int bin = bin_of(z);
-        if (bin > hi_bin && by_count) {
+        if (bin > hi_bin || !able(v, z, bin, i)) {
           rest = rest || bin < kSure || (bin < kBins && weight_of(expf(z)) > 0);
           return;
         }
-        if (bin >= kBins) return;
-        const uint32_t w = weight_of(expf(z));
-        if (!able(v, z, bin, i)) {
-          rest = rest || w > 0;
-          return;
-        }
-        mass += w;
-        if (bin > hi_bin) {
-          rest = rest || w > 0;
-          return;
-        }
-        list_mass += w;
         const int at = atomicAdd(&sh.listed, 1);
         if (at < kListed) scr.list.own[at] = static_cast<uint16_t>(i);
       });
       __syncthreads();
-      n = (tid == 0 ? static_cast<unsigned>(sh.listed) : 0u) | (rest ? 1ull << 32 : 0ull);
+      unsigned long long n = tid == 0 ? static_cast<unsigned>(sh.listed) : 0u, others = rest;
       const int par = parity;
-      cluster_reduce<false>(sh.ex, parity, cluster, rank, n, mass, list_mass);
-      const int listed = static_cast<int>(n & 0xffffffffu);
-      rest = n >> 32;
-      const double stop = __dmul_rn(static_cast<double>(p), static_cast<double>(mass));
-      if (listed <= kListed && (by_count || !(static_cast<double>(list_mass) < stop))) {
-        // everything that is kept is listed: the first CTA does the rest, and
-        // the others go on
+      cluster_reduce<false>(sh.ex, parity, cluster, rank, n, others);
+      const int listed = static_cast<int>(n);
+      if (listed <= kListed) {
+        // the first CTA does the rest, and the others leave
         int at = 0;
-        for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i] & 0xffffffffu);
-        const int here = static_cast<int>(sh.ex.slot[par][0][rank] & 0xffffffffu);
+        for (int i = 0; i < rank; ++i) at += static_cast<int>(sh.ex.slot[par][0][i]);
+        const int here = static_cast<int>(sh.ex.slot[par][0][rank]);
         for (int j = tid; j < here; j += kSampleThreads) {
           const int el = scr.list.own[j];
           const float xv = held_logit<T>(held, el, most);
@@ -852,8 +843,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
         }
         cluster_barrier();
         if (rank == 0) {
-          const ListRow lr = {listed, by_count ? min(k, listed) : listed, by_count, by_mass,
-                              rest,   static_cast<double>(p),            stop};
+          const ListRow lr = {listed, min(k, listed), by_mass, others > 0, static_cast<double>(p)};
           const int left_out = VERIFY && a.greedy_drafts && draft >= 0 && draft < a.V ? draft : -1;
           draw_from_list<T, VERIFY>(a, sh, scr.list, lr, sc, r, q, row, left_out,
                                     VERIFY && judges && !a.greedy_drafts);
@@ -1074,6 +1064,12 @@ __device__ __forceinline__ uint32_t dist_weight(float x, int id, const pe_dist& 
 }
 
 // A cluster a request: its first rejected draft, and the token drawn there.
+// A request's window takes a few reads; with sampled drafts the two rows of the
+// first rejected one are read once, 16 bytes at a time, and the weights of what
+// the target has more of are held in shared memory for the draw, which goes by
+// the order of ids.  Two exponentials a token and the wait for the rows bound
+// that: 64 requests, 201,088 fp32 logits, take 72 us here (1.4 TB/s) after 394
+// in the kernel above, which has their 512 rows.
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
     const __grid_constant__ VerifyArgs a) {
@@ -1244,15 +1240,19 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
 }
 
 // -------------------------------------------------------------------- launch
-// Two CTAs an SM, or one.
+// Shared memory of one of two CTAs on an SM.
 constexpr size_t kHalfShared = 112 * 1024 - sizeof(SampleShared);
-constexpr size_t kMostShared = 226 * 1024 - sizeof(SampleShared);
+// The most that a CTA takes, of rows or of weights.  (A kernel's limit is always
+// set to the same, never to what one call needs: another thread's call may lie
+// between setting and launching.)
+constexpr size_t kMostShared = static_cast<size_t>(kMostVocab / kMostCluster) * 4 + 64 + sizeof(Scratch);
 struct SampleShape {
   int cluster;
   size_t smem;
 };
-// Few rows: as many CTAs a row as a cluster has, for the shortest way; more
-// rows than that fills: as few as hold the row.
+// Few rows: as many CTAs a row as a cluster has, for the shortest way (33 rows
+// of 50,257 bf16 logits: 30 us by eight CTAs each, 59 by one); more rows than
+// that fills: as few as hold the row, two to an SM.
 static SampleShape sample_shape(int rows, int V, int elem, int sms) {
   auto bytes = [&](int c) {
     const int e = 16 / elem, all = (V + 2 * (e - 1)) / e;
@@ -1272,7 +1272,7 @@ static cudaError_t launch_rows(SampleArgs a, int sms, cudaStream_t s) {
   a.cluster = sh.cluster;
   auto kernel = sample_rows_kernel<T, VERIFY, FILTERS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(sh.smem));
+                                             static_cast<int>(kMostShared));
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.rows) * sh.cluster),
                             dim3(kSampleThreads), sh.smem, s, sh.cluster, a);
@@ -1294,7 +1294,7 @@ static cudaError_t launch_verify(VerifyArgs v, cudaStream_t s) {
       v.draft_logits ? static_cast<size_t>((v.V + 2 * (E - 1)) / E + v.cluster - 1) / v.cluster * E * 4 : 0;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        verify_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        verify_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostShared));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl_cluster(verify_kernel<T>, dim3(static_cast<unsigned>(v.B) * v.cluster),

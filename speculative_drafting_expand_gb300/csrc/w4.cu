@@ -3,14 +3,14 @@
 //
 // Packed layout.  The matrix is cut into tiles of 16 rows and units of 64
 // inputs (groups of 128: an even number), filled up with zeros.  First the
-// codes, [tile][unit][lane][16 bytes]: word j of a lane is its part of the left operand of one m16n8k16
-// product (inputs 16 j .. 16 j + 15 of the unit), so a warp reads a unit as
-// one 512-byte line and needs no exchange.  Register i of the operand takes
-// nibbles i (low half) and i + 4 (high half) of the word, from which a logic
-// operation and an addition make a pair of fp16 numbers code - 8, exact.  Then the scales, bf16, rows g and g + 8 of a tile side
-// by side in a word, which is what a lane needs of a group: groups of 32, two
-// words a unit, [tile][unit][g][2]; of 64, [tile][unit][g]; of 128,
-// [tile][pair of units][g].
+// codes, [tile][unit][lane][16 bytes]: word j of a lane is its part of the left
+// operand of one m16n8k16 product (inputs 16 j .. 16 j + 15 of the unit), so a
+// warp reads a unit as one 512-byte line and needs no exchange.  Register i of
+// the operand takes nibbles i (low half) and i + 4 (high half) of the word, from
+// which a logic operation and an addition make a pair of fp16 numbers code - 8,
+// exact.  Then the scales, bf16, rows g and g + 8 of a tile side by side in a
+// word, which is what a lane needs of a group: groups of 32, two words a unit,
+// [tile][unit][g][2]; of 64, [tile][unit][g]; of 128, [tile][pair of units][g].
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -381,6 +381,15 @@ __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0
 // The warps of a CTA divide the units of its run evenly: a warp has the end of
 // one tile, some whole ones and the start of another.  What does not end where
 // a tile ends meets in shared memory and is added in the order of the inputs.
+// Products of 8 columns and not tcgen05 tiles: codes would have to be written to
+// shared memory as 16-bit operands of 128 rows, four times their bytes, for one
+// to eight columns of use.  The codes go from the ring into registers and from
+// there into the product; what bounds that is the issue of instructions, 93 a
+// unit for the codes, the products and the scales (201,088 x 2880 in groups of
+// 32, one row: 66 us, 4.95 TB/s, three quarters of the issue slots in use;
+// 151,936 x 2048 in groups of 128, eight rows: 40 us, 4.2 TB/s).  Small matrices
+// are bound by the way from the launch through x and the ring's first pairs to
+// the meeting (5120 x 2880, one row: 9.4 us).
 template <typename TX, typename TY, int NT, int GROUP>
 __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
     w4_linear_kernel(const __grid_constant__ W4Args a) {
@@ -664,7 +673,7 @@ static int resident_clusters(int cluster, int per_sm, size_t smem, int sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess ||
+                           static_cast<int>(kW4MostShared)) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
     n = std::max(1, per_sm * sms / cluster / 2);
   else if (place)
@@ -710,8 +719,9 @@ static cudaError_t launch_w4(W4Args a, int sms, cudaStream_t s) {
   a.chunk = p.chunk;
   a.ring = static_cast<int>(w4_ring_at(a.sh, a.rows, sizeof(TX) == 4 ? 3 : 1, NT, p.cluster));
   auto kernel = w4_linear_kernel<TX, TY, NT, GROUP>;
+  // (always the same limit: another thread's call may lie between this and the launch)
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(p.smem));
+                                       static_cast<int>(kW4MostShared));
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kernel, dim3(p.ctas), dim3(kW4Threads), p.smem, s, p.cluster, a);
 }

@@ -404,3 +404,48 @@ def test_a_drafting_step_goes_on_from_what_verification_returns():
     ref = O.expand_batch(K, ids.view(-1).cpu().numpy(), inp.target_pos, cu.cpu().numpy(), a_host,
                          s_host, inp.block_table, shape.page_size, shape.mask_token_id)
     G.check_expand(ex, ref, wl.T)
+
+
+def test_memory_freed_before_another_stream_has_read_it():
+    torch, B = _lib()
+    V = 5000
+    x, u, k = torch.randn(6, V, device="cuda") * 3, torch.rand(6, device="cuda"), \
+        torch.full((6,), 30, dtype=torch.int32, device="cuda")
+    want = B.pe_sample(x, u, top_k=k)
+    copies = [t.clone() for t in (x, u, k)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # 50 ms in which the copies are freed
+    got = B.pe_sample(copies[0], copies[1], top_k=copies[2], stream=side)
+    del copies
+    other = [torch.full_like(t, 7) for t in (x, u, k) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 7).all()) for t in other)
+
+
+def test_two_host_threads_with_vocabularies_of_different_sizes():
+    torch, B = _lib()
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(V):
+        x, u = torch.randn(5, V, device="cuda") * 3, torch.rand(5, device="cuda")
+        cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+        ids = torch.randint(V, (5,), dtype=torch.int32, device="cuda")
+        y = torch.randn(4, V, device="cuda")
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+
+        def both():
+            d = B.pe_sample(y, u[1:].contiguous(), stream=stream)
+            return d + B.pe_verify(x, ids, cu, u, u[:1].contiguous(), draft_logits=y,
+                                   draft_dist=d[2], stream=stream)
+
+        first = both()
+        rest = [both() for _ in range(100)]
+        stream.synchronize()
+        return all(torch.equal(a, b) for r in rest for a, b in zip(r, first))
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, (400, 200000)))

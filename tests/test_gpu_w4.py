@@ -190,3 +190,48 @@ def test_large_offsets():
                        out_dtype=torch.float32)[0]
     assert y[0] == k and y[-1] == 2 * k and y[n // 2 + 5] == -k
     assert int((y != 0).sum()) == 3
+
+
+def test_memory_freed_before_another_stream_has_read_it():
+    torch, B = _lib()
+    rng = np.random.default_rng(9)
+    n, k = 512, 1024
+    codes = torch.from_numpy(rng.integers(0, 256, (n, k // 2), dtype=np.uint8)).cuda()
+    scales = torch.rand(n, k // 32, device="cuda").bfloat16()
+    weight = torch.randn(n, k, device="cuda")
+    x = torch.randn(3, k, device="cuda")
+    want = B.pe_w4_linear(B.W4Weight(codes, scales, k, 32), x)
+    want_q = B.pe_w4_linear(B.W4Weight.quantize(weight), x)
+    copies = [t.clone() for t in (codes, scales, weight, x, x)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # 50 ms in which the copies are freed
+    w = B.W4Weight(copies[0], copies[1], k, 32, stream=side)
+    q = B.W4Weight.quantize(copies[2], stream=side)
+    y = B.pe_w4_linear(w, copies[3], stream=side)
+    yq = B.pe_w4_linear(q, copies[4], stream=side)
+    del copies, w, q
+    other = [torch.full_like(t, 7) for t in (codes, scales, weight, x, x) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(yq, want_q)
+    assert all(bool((t == 7).all()) for t in other)
+
+
+def test_two_host_threads_with_matrices_of_different_sizes():
+    torch, B = _lib()
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(seed):
+        rng = np.random.default_rng(seed)
+        w, _ = _weight(torch, B, rng, 256, 4096 if seed else 320, 32)
+        x = torch.from_numpy(rng.normal(size=(8, w.k)).astype(np.float32)).cuda()
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        first = B.pe_w4_linear(w, x, stream=stream)
+        rest = [B.pe_w4_linear(w, x, stream=stream) for _ in range(300)]
+        stream.synchronize()
+        return all(torch.equal(first, y) for y in rest)
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, (0, 1)))
