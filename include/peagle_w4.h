@@ -36,7 +36,8 @@ int64_t pe_w4_bytes(int32_t n, int32_t k, int32_t group);
  * [n, ceil(k / group)] bf16.  packed: pe_w4_bytes bytes, 16-byte aligned, not
  * overlapping the inputs.
  * PE_ERR_INVALID_ARGUMENT: n or k < 1, a group other than 32, 64 and 128, a
- * null or misaligned pointer.  PE_ERR_UNSUPPORTED: k past 2^18, n past 2^24. */
+ * null or misaligned pointer.  PE_ERR_UNSUPPORTED: k past 2^17 (one
+ * row of x in fp32 has to fit into the shared memory of eight SMs), n past 2^24. */
 pe_status pe_w4_pack(const uint8_t* codes, const void* scales, int32_t n, int32_t k,
                      int32_t group, void* packed, void* stream);
 

@@ -889,7 +889,7 @@ class W4Weight:
         _cache_ints(n=n, k=k, group=group)
         nbytes = lib().pe_w4_bytes(n, k, group)
         if nbytes <= 0:
-            raise ValueError("a 4-bit matrix has n, k >= 1 (k up to 2**18, n up to 2**24) and a "
+            raise ValueError("a 4-bit matrix has n, k >= 1 (k up to 2**17, n up to 2**24) and a "
                              "group of 32, 64 or 128")
         self.n, self.k, self.group, self.device = n, k, group, device
         self.packed = _op_empty(nbytes, torch.uint8, device, stream)

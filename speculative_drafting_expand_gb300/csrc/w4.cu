@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
   for (int tile0 = run0; tile0 < run1; tile0 += a.chunk) {
     const int tiles = min(a.chunk, run1 - tile0);
     // where a warp's units start, counted from the first tile's (fewer than
-    // 2^28: 2^20 tiles of all clusters, 2^12 units)
+    // 2^28: 2^20 tiles of all clusters, 2^11 units)
     const unsigned all = static_cast<unsigned>(tiles) * units_here;
     auto start = [&](int w) { return static_cast<int>(all * w / kW4Warps / GRAIN * GRAIN); };
     const int from = start(warp), mine = start(warp + 1) - from;
@@ -761,7 +761,7 @@ static cudaError_t run_w4(W4Args a, int sms, cudaStream_t s) {
 static pe_status w4_sizes(int32_t n, int32_t k, int32_t group) {
   if (n < 1 || k < 1 || (group != 32 && group != 64 && group != 128))
     return PE_ERR_INVALID_ARGUMENT;
-  if (k > (1 << 18) || n > (1 << 24)) return PE_ERR_UNSUPPORTED;
+  if (k > (1 << 17) || n > (1 << 24)) return PE_ERR_UNSUPPORTED;
   return PE_OK;
 }
 static bool w4_aligned(const void* p, size_t to) {

@@ -235,3 +235,14 @@ def test_two_host_threads_with_matrices_of_different_sizes():
 
     with ThreadPoolExecutor(2) as pool:
         assert all(pool.map(work, (0, 1)))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 7, 33])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("k,group", [(1 << 17, 32), (1 << 17, 128), ((1 << 17) - 77, 64)])
+def test_longest_rows(rows, xt, k, group):
+    torch, B = _lib()
+    rng = np.random.default_rng([rows, k, group])
+    w, m = _weight(torch, B, rng, 35, k, group)
+    x = torch.from_numpy(rng.normal(size=(rows, k)).astype(np.float32)).to(_type(torch, xt)).cuda()
+    _check(B.pe_w4_linear(w, x, out_dtype=torch.float32), x, m, group, xt, "f32")

@@ -93,6 +93,12 @@ def test_w4_sizes_are_refused_by_every_call(B, change, status):
     assert B.lib().pe_w4_bytes(s["n"], s["k"], s["group"]) == 0
 
 
+def test_w4_longest_row(B):
+    k = (1 << 17) + 1
+    assert B.lib().pe_w4_bytes(17, k - 1, 32) > 0 and B.lib().pe_w4_bytes(17, k, 32) == 0
+    assert _pack(B, k=k) == _quantize(B, k=k, stride=k) == _linear(B, k=k, xs=k, ys=17) == 2
+
+
 def test_w4_bytes_is_16_rows_by_64_inputs_and_scales(B):
     f = B.lib().pe_w4_bytes
     assert f(1, 1, 32) == 512 + 64
