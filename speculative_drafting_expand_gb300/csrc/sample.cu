@@ -125,6 +125,13 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
   return v;
 }
 
+// No CTA's shared memory is written to by a peer before it has started: there
+// is nothing to publish yet.
+__device__ __forceinline__ void start_barrier() {
+  cluster_arrive_relaxed();
+  cluster_wait_acquire();
+}
+
 struct Exchange {
   unsigned long long warp[2][kSampleWarps];
   unsigned long long slot[2][2][kMostCluster];  // [parity][value][CTA]
@@ -151,7 +158,12 @@ __device__ __forceinline__ void cluster_reduce(Exchange& ex, int& parity, int cl
     if (lane < cluster)
       st_cluster_u64(cluster_map_shared(smem_u32(&ex.slot[parity][warp][rank]), lane), x);
   }
-  cluster_barrier();
+  // the two warps publish what they wrote, and with it what the CTA's other
+  // warps wrote before they met above (with a release by every warp 448 rows by
+  // temperature take 178 us for 174)
+  if (warp < 2) cluster_arrive_release();
+  else cluster_arrive_relaxed();
+  cluster_wait_acquire();
   a = b = 0;
 #pragma unroll
   for (int r = 0; r < kMostCluster; ++r) {
@@ -456,7 +468,7 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
 // each filter a look at every token more, so the row is read from HBM once and
 // stays in the cluster's shared memory: reading it again from L2 instead, in
 // smaller CTAs or through rings of asynchronous copies, took 192 us where this
-// takes 179 (448 rows of 201,088 fp32 logits by temperature, 2.0 TB/s).  What
+// takes 174 (448 rows of 201,088 fp32 logits by temperature, 2.1 TB/s).  What
 // bounds a row is the way through its steps, which wait on each other: the
 // copy, the largest, the sum, the draw, each behind a meeting of the cluster
 // (about 1.5 us), against which two CTAs of different rows share an SM.
@@ -468,9 +480,9 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
 // keys; a bin with more than a list takes is cut by a further histogram of its
 // keys.  Additions to bins in shared memory bound that (15 cycles a warp's 32
 // where they are spread, two of them a token for sums of weights): 128 rows of
-// 151,936 fp32 logits with mixed filters take 106 us.  For top-k to kMostGuess
+// 151,936 fp32 logits with mixed filters take 101 to 110 us.  For top-k to kMostGuess
 // the histogram is of one logit a thread, and one CTA ranks what it lists: one
-// row 36 -> 22 us, the 128 mixed ones 131 -> 106 us.
+// row 36 -> 21 us, the 128 mixed ones 131 -> 106 us.
 template <typename T, bool VERIFY, bool FILTERS>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     const __grid_constant__ SampleArgs a) {
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int cluster = a.cluster, rank = cluster_ctarank();
   int parity = 0;
-  cluster_barrier();  // no CTA's shared memory is written to before it has started
+  start_barrier();
   grid_dep_wait();
   grid_dep_launch();
   const int r = blockIdx.x / cluster;
@@ -1080,7 +1092,7 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int cluster = a.cluster, rank = cluster_ctarank(), r = blockIdx.x / cluster;
   int parity = 0;
-  cluster_barrier();  // no CTA's shared memory is written to before it has started
+  start_barrier();
   grid_dep_wait();
   grid_dep_launch();
   const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1], drafts = a.T - a.B;
