@@ -5,8 +5,9 @@ Tolerance, from the arithmetic (u = 2^-24, S = sum_j |x_j w_j|): products of
 bf16 numbers are exact in fp32; a group's products are summed in fp32 in any
 order, each addition rounded or truncated (2 u at most): 2 group u S; each
 group's sum is scaled and added (2 roundings), partial results of at most 64
-warps are added: (2 groups + 64) u S.  fp32 x: three bf16 parts leave u |x|,
-and three times the additions.  y: half a step of its type."""
+warps are added: (2 groups + 64) u S.  fp32 x: three fp16 parts leave less
+than u |x| of what is within 2^-14 of its row's largest (less, 2^-38 of that,
+vanishes beside the 64 u S), and three times the additions.  y: half a step of its type."""
 
 import numpy as np
 import pytest
