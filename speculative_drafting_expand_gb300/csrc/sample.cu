@@ -307,15 +307,18 @@ __device__ __forceinline__ int find_in_segment(Segment seg, long long at, W&& we
 }
 
 // ------------------------------------------------------------- sampling rows
-// Bins of falling logits, 48 an octave of e = 2^(-bin / 48): rounding is
+// Bins of falling logits, 40 an octave of e = 2^(-bin / 40): rounding is
 // monotonic, so a larger logit never has a larger bin.  Bins below kSure hold
 // W > 0 alone, bins from kBins on (and NaN, which -inf gives) W = 0 alone.
-constexpr int kPerOctave = 48;
+// (64 requests of sampled drafts with mixed filters: 448 us with 48 an octave,
+// 441 with 40, 444 with 32: fewer bins to clear and to add up, longer lists.)
+constexpr int kPerOctave = 40;
 constexpr int kSure = 32 * kPerOctave - 1;
 constexpr int kBins = 32 * kPerOctave + 4;
+static_assert(kBins >= 1024, "a further level cuts 2^64 keys into at most 2^10");
 __device__ __forceinline__ int bin_of(float z) {
   // 8388608 + n has the bits 0x4B000000 + n, a larger or no number larger ones
-  const float f = fmaf(z, -69.24936196f, 8388608.f);  // 48 / ln 2
+  const float f = fmaf(z, -57.70780164f, 8388608.f);  // 40 / ln 2
   return static_cast<int>(min(__float_as_uint(f) - 0x4B000000u, static_cast<uint32_t>(kBins)));
 }
 
@@ -475,12 +478,12 @@ __device__ __noinline__ void draw_from_list(const SampleArgs& a, SampleShared& s
 //
 // Filters look for the last kept token.  Weights and logits fall together, so
 // a histogram over falling logits has the sums "of the tokens before" at its
-// bins' borders; the limit's own bin (a 48th of a factor of two, a few tokens
+// bins' borders; the limit's own bin (a 40th of a factor of two, a few tokens
 // of a usual row) is listed, and the limit found in it by the digits of the
 // keys; a bin with more than a list takes is cut by a further histogram of its
 // keys.  Additions to bins in shared memory bound that (15 cycles a warp's 32
 // where they are spread, two of them a token for sums of weights): 128 rows of
-// 151,936 fp32 logits with mixed filters take 101 to 110 us.  For top-k to kMostGuess
+// 151,936 fp32 logits with mixed filters take 101 to 105 us.  For top-k to kMostGuess
 // the histogram is of one logit a thread, and one CTA ranks what it lists: one
 // row 36 -> 21 us, the 128 mixed ones 131 -> 106 us.
 template <typename T, bool VERIFY, bool FILTERS>
