@@ -348,6 +348,19 @@ struct SampleShared {
   uint32_t differ[2];
 };
 
+// Whether nothing in cu_in contradicts request r's window [w0, w1): the entries
+// before it lie at or before its start, those after it at or behind its end.
+// Then a bisection finds the window for each of its rows, and no other such
+// window has any of them.  By all threads of a CTA.
+__device__ __forceinline__ bool window_in_order(const int32_t* cu_in, int B, int r, int w0, int w1) {
+  bool bad = false;
+  for (int i = threadIdx.x; i <= B; i += kSampleThreads) {
+    const int at = cu_in[i];
+    bad = bad || (i < r && at > w0) || (i > r && at < w1);
+  }
+  return !__syncthreads_or(bad);
+}
+
 // The largest k for which the threads' largest logits are asked: past it the
 // threads of a row are too few for the k-th of theirs to be near the row's k-th.
 // (33 rows of 50,257 bf16 logits with mixed filters: 30 us, and 37 with 64 as
@@ -512,6 +525,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     q = lo;
     const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
     if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) return;  // the whole cluster
+    if (!window_in_order(a.cu_in, a.B, q, w0, w1)) return;
     judges = r + 1 < w1;
     draft = judges ? a.ids[r + 1] : -1;
   }
@@ -1099,7 +1113,7 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   grid_dep_wait();
   grid_dep_launch();
   const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1], drafts = a.T - a.B;
-  if (w0 < 0 || w1 <= w0 || w1 > a.T) {
+  if (w0 < 0 || w1 <= w0 || w1 > a.T || !window_in_order(a.cu_in, a.B, r, w0, w1)) {
     if (rank == 0 && tid == 0) {
       record_error(a.err, PE_DEV_BAD_ROW);
       a.num_accepted[r] = 0;
