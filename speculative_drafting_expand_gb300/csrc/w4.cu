@@ -376,6 +376,35 @@ __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0
   }
 }
 
+// y[r, i] in 64 bits and from the numbers as they came, by one thread.  For a
+// row of finite x whose sum left fp32's range: it is taken of x brought to 2^13
+// .. 2^15 and times scales of up to 2^128, so it can where the result itself has
+// room (x of 1 with scales above 2^100, smaller x with smaller ones).  No model
+// has such scales; what the others pay is a comparison a result when it is stored
+// (taking the row's power back before the scale instead costs a multiplication a
+// result and group).
+template <typename TX, typename TY>
+__device__ __noinline__ void store_by_64_bits(const W4Args& a, int r, int i) {
+  const W4Shape sh = a.sh;
+  const int tile = i / kTileRows, row = i % kTileRows;
+  const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
+  const uint32_t* codes = static_cast<const uint32_t*>(a.packed);
+  const bf16* scales =
+      reinterpret_cast<const bf16*>(static_cast<const char*>(a.packed) + sh.code_bytes());
+  double sum = 0.0;
+  for (int j = 0; j < sh.k; ++j) {
+    // (nibble_place, the other way round)
+    const int in = j % 16, nibble = (in & 1) * 4 + in / 8 * 2 + (row >> 3);
+    const int lane = (row & 7) * 4 + in % 8 / 2;
+    const long long word =
+        ((static_cast<long long>(tile) * sh.units + j / kUnit) * 32 + lane) * 4 + j % kUnit / 16;
+    const int code = static_cast<int>(codes[word] >> (4 * nibble) & 15) - 8;
+    const float scale = __bfloat162float(scales[sh.scale_at(tile, row, j / sh.group)]);
+    sum += static_cast<double>(to_f<TX>(x[j])) * code * scale;
+  }
+  static_cast<TY*>(a.y)[r * a.y_stride + i] = from_f<TY>(static_cast<float>(sum));
+}
+
 // y[r, i]: rows r in columns of the products, outputs i in their rows.  A
 // cluster holds x once, each CTA a range of the inputs, and has a run of tiles.
 // The warps of a CTA divide the units of its run evenly: a warp has the end of
@@ -419,8 +448,19 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
   for (int nt = 0; nt < NT; ++nt) xrow[nt] = min(nt * 8 + g, a.rows - 1) * 4;
   TY* y = static_cast<TY*>(a.y);
 
+  bool over = false;  // a result is infinite or NaN
   auto store = [&](int r, int i, float v) {
-    if (r < a.rows && i < sh.n) y[r * a.y_stride + i] = from_f<TY>(v);
+    if (r < a.rows && i < sh.n) {
+      y[r * a.y_stride + i] = from_f<TY>(v);
+      over = over || !(fabsf(v) < INFINITY);
+    }
+  };
+  // The same result again, where x is not why
+  auto again = [&](int r, int i) {
+    if (r >= a.rows || i >= sh.n || fabsf(to_f<TY>(y[r * a.y_stride + i])) < INFINITY) return;
+    for (int c = 0; c < cluster; ++c)
+      if ((cluster > 1 ? *cluster_pointer(largest + r, c) : largest[r]) >= 0x7f800000u) return;
+    store_by_64_bits<TX, TY>(a, r, i);
   };
   // place[column][16 outputs]
   auto put = [&](float* place, const float (&sum)[NT][4]) {
@@ -607,6 +647,9 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
         }
         store(r, (tile0 + jw) * kTileRows + e % 16, sumv);
       }
+      if (__syncthreads_or(over))
+        for (int z = threadIdx.x; z < tiles * RES; z += kW4Threads)
+          again(z % RES / 16, (tile0 + z / RES) * kTileRows + z % 16);
     } else {
       // tiles in one piece, then the pieces of all ranges of the inputs
       if (units_here == 0)
@@ -626,6 +669,10 @@ __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
         for (int c = 0; c < cluster; ++c) sumv += *cluster_pointer(mains + z, c);
         store(r, (tile0 + z / RES) * kTileRows + e % 16, sumv);
       }
+      if (over)  // this thread's own
+        for (int z = rank * kW4Threads + static_cast<int>(threadIdx.x); z < tiles * RES;
+             z += cluster * kW4Threads)
+          again(z % RES / 16, (tile0 + z / RES) * kTileRows + z % 16);
       cluster_barrier();
     }
     __syncthreads();
