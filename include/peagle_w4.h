@@ -59,7 +59,7 @@ pe_status pe_w4_quantize(const void* w, int32_t dtype, int64_t w_stride, int32_t
  * fp32 ones also to 2^-24 of themselves.  A row with an infinite or NaN
  * element gives infinities and NaN, the other rows are as they would be.
  * Scales are any finite bf16 numbers.  Where a sum leaves fp32's range on the
- * way (never below scales of 2^100), that result is summed again in 64 bits, by
+ * way (never below scales of 2^92), that result is summed again in 64 bits, by
  * one thread: right, but slow where there are many.
  * Made for a few rows: up to 32 cost one pass over the weights, each further
  * 32 another (fewer where 32 rows of x do not fit into the shared memory of

@@ -379,8 +379,8 @@ __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0
 // y[r, i] in 64 bits and from the numbers as they came, by one thread.  For a
 // row of finite x whose sum left fp32's range: it is taken of x brought to 2^13
 // .. 2^15 and times scales of up to 2^128, so it can where the result itself has
-// room (x of 1 with scales above 2^100, smaller x with smaller ones).  No model
-// has such scales; what the others pay is a comparison a result when it is stored
+// room (2^17 inputs of weight -8 at most: with scales above 2^92).  No model has
+// such scales; what the others pay is a comparison a result when it is stored
 // (taking the row's power back before the scale instead costs a multiplication a
 // result and group).
 template <typename TX, typename TY>
