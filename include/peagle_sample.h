@@ -68,8 +68,8 @@ typedef struct {
  * (-inf without a token); dist: NULL, or [rows], what pe_verify takes of a
  * drafter's rows.
  * PE_ERR_INVALID_ARGUMENT: rows or vocab < 1, another dtype, a stride
- * shorter than a row, a null pointer, logits not aligned to their elements,
- * dist not 16-byte aligned.  PE_ERR_UNSUPPORTED: vocab past 393216, rows past
+ * shorter than a row, a null pointer, logits or a vector not aligned to their
+ * elements, dist not 16-byte aligned.  PE_ERR_UNSUPPORTED: vocab past 393216, rows past
  * 2^27. */
 pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logits,
                     int64_t stride, const float* temperature, const int32_t* top_k,

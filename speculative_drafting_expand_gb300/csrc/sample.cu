@@ -1343,6 +1343,11 @@ static bool logits_ok(const void* p, int64_t stride, int32_t vocab, int32_t dtyp
   return p && reinterpret_cast<uintptr_t>(p) % elem == 0 && stride >= vocab;
 }
 static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Vectors of 32-bit numbers, those that are not given (NULL) among them.
+template <typename... P>
+static bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) % 4 == 0) && ...);
+}
 
 }  // namespace pe
 
@@ -1352,7 +1357,7 @@ extern "C" pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const
                                int32_t* tokens, float* logprobs, pe_dist* dist, void* stream) {
   using namespace pe;
   if (rows < 1 || vocab < 1 || !logits_ok(logits, stride, vocab, dtype) || !u || !tokens ||
-      !aligned16(dist))
+      !aligned4(temperature, top_k, top_p, min_p, u, tokens, logprobs) || !aligned16(dist))
     return PE_ERR_INVALID_ARGUMENT;
   if (vocab > kMostVocab || rows > (1 << 27)) return PE_ERR_UNSUPPORTED;
   SampleArgs a = {};
@@ -1387,7 +1392,9 @@ extern "C" pe_status pe_verify(int32_t B, int32_t T, int32_t vocab, int32_t dtyp
                                pe_dist* dist, int32_t* err, void* stream) {
   using namespace pe;
   if (B < 1 || T < B || vocab < 1 || !logits_ok(logits, stride, vocab, dtype) || !ids || !cu_in ||
-      !accept_u || !u || !num_accepted || !sampled_ids || !dist || !aligned16(dist))
+      !accept_u || !u || !num_accepted || !sampled_ids || !dist || !aligned16(dist) ||
+      !aligned4(ids, cu_in, temperature, top_k, top_p, min_p, accept_u, u, num_accepted,
+                sampled_ids, logprobs, err))
     return PE_ERR_INVALID_ARGUMENT;
   if (draft_logits && T > B &&
       (!logits_ok(draft_logits, draft_stride, vocab, dtype) || !draft_dist ||
