@@ -91,7 +91,8 @@ pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logi
  *   sampled drafts: accepted where accept_u * Q(d) < P(d); replaced by a
  *     token drawn from max(P - Q, 0).
  * (As u * total < W(d) and u * Wq(d) * total < W(d) * totalq in fp64; a draft
- * with P(d) = 0 is never accepted, a greedy one with P(d) = 1 always.  For
+ * with P(d) = 0 is never accepted, a greedy one with P(d) = 1 always; accept_u
+ * is taken as it is, and one that is NaN accepts no other draft.  For
  * max(P - Q, 0): with p = W * a, q = Wq * aq in fp32, a = 2^31 / total
  * rounded to fp32, the weights are p - q in fp32, rounded to whole numbers;
  * where they sum to 0, p rounded to whole numbers.)

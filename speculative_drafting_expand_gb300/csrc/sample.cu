@@ -1145,8 +1145,8 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
       }
       const double u = a.accept_u[t];
       if (draft_logits)
-        ok = u * static_cast<double>(wq) * static_cast<double>(P.total) <
-             static_cast<double>(w) * static_cast<double>(totalq);
+        ok = w > 0 && u * static_cast<double>(wq) * static_cast<double>(P.total) <
+                          static_cast<double>(w) * static_cast<double>(totalq);
       else
         ok = w > 0 && (w == P.total || u * static_cast<double>(P.total) < static_cast<double>(w));
     }
