@@ -117,8 +117,8 @@ pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logi
  * it before its end, so that windows that overlap are bad, each of them:
  * num_accepted 0 and sampled_ids -1, its rows are left as they were, and the
  * other windows are judged),
- * PE_DEV_BAD_TOKEN (a draft outside [0, vocab): rejected as one with P = 0,
- * Q = 0).
+ * PE_DEV_BAD_TOKEN (a draft outside [0, vocab), behind a rejected one too:
+ * rejected as one with P = 0, Q = 0).
  * PE_ERR_INVALID_ARGUMENT: B < 1, T < B, vocab < 1, another dtype, a stride
  * shorter than a row, a null or misaligned pointer, draft_logits without
  * draft_dist.  PE_ERR_UNSUPPORTED: vocab past 393216, T past 2^27. */

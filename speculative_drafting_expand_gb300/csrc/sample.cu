@@ -1123,6 +1123,10 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   }
   const T* logits = static_cast<const T*>(a.logits);
   const T* draft_logits = static_cast<const T*>(a.draft_logits);
+  // drafts of no token are recorded wherever they are, judged or not
+  if (rank == 0 && warp == kSampleWarps - 1)
+    for (int t = w0 + lane; t < w1 - 1; t += 32)
+      if (a.ids[t + 1] < 0 || a.ids[t + 1] >= a.V) record_error(a.err, PE_DEV_BAD_TOKEN);
   // every warp finds the first rejection for itself, 32 drafts at a time
   int stop = w1 - 1;
   for (int t0 = w0; t0 < w1 - 1; t0 += 32) {
@@ -1133,9 +1137,7 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
       const pe_dist P = a.dist[t];
       uint32_t w = 0, wq = 0;
       long long totalq = 0;
-      if (d < 0 || d >= a.V) {
-        if (rank == 0 && warp == 0) record_error(a.err, PE_DEV_BAD_TOKEN);
-      } else {
+      if (d >= 0 && d < a.V) {
         w = dist_weight<T>(raw_logit(logits + t * a.stride + d), d, P);
         if (draft_logits && from >= 0 && from < drafts) {
           const pe_dist Q = a.draft_dist[from];

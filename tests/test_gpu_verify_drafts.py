@@ -34,3 +34,38 @@ def test_a_draft_without_probability_is_never_accepted(sampled, accept_u):
                                  torch.full((2,), accept_u, device="cuda"),
                                  torch.tensor([0.5], device="cuda"), top_k=k, **kw)
     assert int(acc) == 0 and 0 <= int(tok) < 3
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+@pytest.mark.parametrize("bad", [-1, 40, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("place", [1, 2, 31, 32, 33, 34, 64, 65, 70])
+def test_drafts_of_no_token_are_recorded_wherever_they_are(sampled, bad, place):
+    """A window of 70 drafts.  At the first place the bad one is judged and
+    rejected; elsewhere the first draft, which has no probability, is."""
+    torch, L = _lib()
+    V, T = 40, 71
+    x = torch.zeros(T, V, device="cuda")
+    x[:, 7] = float("-inf")
+    ids = torch.full((T,), 3, dtype=torch.int32, device="cuda")
+    ids[1] = 7
+    kw = {}
+    if sampled:
+        d = torch.zeros(T - 1, V, device="cuda")
+        kw = dict(draft_logits=d, draft_dist=L.pe_sample(
+            d, torch.rand(T - 1, device="cuda"))[2])
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    au, u = torch.full((T,), 0.5, device="cuda"), torch.tensor([0.5], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sound = L.pe_verify(x, ids, cu, au, u, err=err, **kw)
+    assert int(err) == 0 and int(sound[0]) == 0
+    ids[place] = bad
+    got = L.pe_verify(x, ids, cu, au, u, err=err, **kw)
+    assert int(err) == L.PE_DEV_BAD_TOKEN
+    # 39 equal tokens: the place of u = 0.5 is in the twentieth, and id 7 is none
+    assert int(got[0]) == 0 and int(got[1]) == 20
+    assert int(sound[1]) == 20
+    ids[place] = 3
+    ids[1] = 3
+    err.zero_()
+    L.pe_verify(x, ids, cu, au, u, err=err, **kw)
+    assert int(err) == 0
