@@ -114,9 +114,10 @@ pe_status pe_sample(int32_t rows, int32_t vocab, int32_t dtype, const void* logi
  * they were.
  * Device errors: PE_DEV_BAD_ROW (a window that is empty, not within [0, T), or
  * out of order: an entry of cu_in before it lies behind its start, or one after
- * it before its end, so that windows that overlap are bad, each of them:
- * num_accepted 0 and sampled_ids -1, its rows are left as they were, and the
- * other windows are judged),
+ * it before its end, so that windows that overlap are bad, each of them; or, of
+ * sampled drafts, one whose drafts have no rows t - r within [0, T - B), as may
+ * be beside empty windows: num_accepted 0 and sampled_ids -1, its rows are left
+ * as they were, and the other windows are judged),
  * PE_DEV_BAD_TOKEN (a draft outside [0, vocab), behind a rejected one too:
  * rejected as one with P = 0, Q = 0).
  * PE_ERR_INVALID_ARGUMENT: B < 1, T < B, vocab < 1, another dtype, a stride

@@ -348,11 +348,15 @@ struct SampleShared {
   uint32_t differ[2];
 };
 
-// Whether nothing in cu_in contradicts request r's window [w0, w1): the entries
-// before it lie at or before its start, those after it at or behind its end.
-// Then a bisection finds the window for each of its rows, and no other such
+// Whether request r's window [w0, w1) is judged: it has rows of [0, T), a row of
+// the drafter's for each sampled draft, and nothing in cu_in contradicts it: the
+// entries before it lie at or before its start, those after it at or behind its
+// end.  Then a bisection finds the window for each of its rows, and no other such
 // window has any of them.  By all threads of a CTA.
-__device__ __forceinline__ bool window_in_order(const int32_t* cu_in, int B, int r, int w0, int w1) {
+__device__ __forceinline__ bool window_is_sound(const int32_t* cu_in, int B, int T, int r, int w0,
+                                                int w1, bool sampled) {
+  if (w0 < 0 || w1 <= w0 || w1 > T) return false;
+  if (sampled && w1 - w0 > 1 && (w0 < r || w1 - 2 - r >= T - B)) return false;
   bool bad = false;
   for (int i = threadIdx.x; i <= B; i += kSampleThreads) {
     const int at = cu_in[i];
@@ -524,8 +528,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     }
     q = lo;
     const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
-    if (w0 < 0 || w0 > r || w1 <= r || w1 > a.rows) return;  // the whole cluster
-    if (!window_in_order(a.cu_in, a.B, q, w0, w1)) return;
+    if (w0 > r || w1 <= r ||
+        !window_is_sound(a.cu_in, a.B, a.rows, q, w0, w1, !a.greedy_drafts))
+      return;  // the whole cluster
     judges = r + 1 < w1;
     draft = judges ? a.ids[r + 1] : -1;
   }
@@ -1112,8 +1117,8 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   start_barrier();
   grid_dep_wait();
   grid_dep_launch();
-  const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1], drafts = a.T - a.B;
-  if (w0 < 0 || w1 <= w0 || w1 > a.T || !window_in_order(a.cu_in, a.B, r, w0, w1)) {
+  const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1];
+  if (!window_is_sound(a.cu_in, a.B, a.T, r, w0, w1, a.draft_logits != nullptr)) {
     if (rank == 0 && tid == 0) {
       record_error(a.err, PE_DEV_BAD_ROW);
       a.num_accepted[r] = 0;
@@ -1139,7 +1144,7 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
       long long totalq = 0;
       if (d >= 0 && d < a.V) {
         w = dist_weight<T>(raw_logit(logits + t * a.stride + d), d, P);
-        if (draft_logits && from >= 0 && from < drafts) {
+        if (draft_logits) {
           const pe_dist Q = a.draft_dist[from];
           wq = dist_weight<T>(raw_logit(draft_logits + from * a.draft_stride + d), d, Q);
           totalq = Q.total;
@@ -1163,7 +1168,7 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   int token = P.token;
   bool writes = rank == 0 && tid == 0;
   const int from = stop - r;
-  if (draft_logits && stop < w1 - 1 && P.total > 0 && from >= 0 && from < drafts) {
+  if (draft_logits && stop < w1 - 1 && P.total > 0) {
     // rejected: from what the target has more of than the drafter
     const pe_dist Q = a.draft_dist[from];
     const T* qrow = draft_logits + from * a.draft_stride;

@@ -119,3 +119,53 @@ def test_filters_are_the_windows_own_beside_bad_ones():
     acc, tok, _, dist = L.pe_verify(x, ids, cu, au, torch.full((4,), 0.999, device="cuda"), temp)
     assert acc.cpu().tolist()[:3] == [0, 0, 3] and tok.cpu().tolist()[:2] == [-1, -1]
     assert int(tok[2]) == int(x[3].argmax()) and (dist[:4, 1] == 0).all()
+
+
+@pytest.mark.parametrize("n,T", [(1, 4), (2, 4), (3, 3), (3, 4)])
+def test_sampled_drafts_have_rows_of_the_drafter(n, T):
+    """A window whose drafts have no rows of the drafter is a bad one; the rows
+    of the others are those of the rule, whatever windows lie before."""
+    torch, L = _lib()
+    V = 9
+    x, ids, au = _inputs(torch, T, V)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dx = x + torch.randn(T, V, generator=g, device="cuda")
+    tok, _, dd = L.pe_sample(dx, torch.rand(T, generator=g, device="cuda"))
+    ids[1:] = tok[:-1]
+    cases, got = [], []
+    for cu in itertools.product(range(-1, T + 2) if n < 3 else range(0, T + 1), repeat=n + 1):
+        out = (torch.full((n,), 55, dtype=torch.int32, device="cuda"),
+               torch.full((n,), 66, dtype=torch.int32, device="cuda"),
+               torch.full((T,), 5.0, device="cuda"),
+               torch.full((T, 8), 77, dtype=torch.int32, device="cuda"),
+               torch.zeros(1, dtype=torch.int32, device="cuda"))
+        L.pe_verify(x, ids, torch.tensor(cu, dtype=torch.int32, device="cuda"), au,
+                    torch.full((n,), 0.6, device="cuda"), draft_logits=dx[:T - n],
+                    draft_dist=dd[:T - n], num_accepted=out[0], sampled_ids=out[1],
+                    logprobs=out[2], dist=out[3], err=out[4])
+        cases.append(cu)
+        got.append(out)
+    alone = {}
+    for cu, out in zip(cases, got):
+        acc, tok, lp, dist, err = [t.cpu() for t in out]
+        good = [ok and (cu[r + 1] - cu[r] == 1 or (cu[r] >= r and cu[r + 1] - 2 - r < T - n))
+                for r, ok in enumerate(sound(cu, T))]
+        assert int(err) == (0 if all(good) else L.PE_DEV_BAD_ROW), cu
+        free = np.ones(T, bool)
+        for r, ok in enumerate(good):
+            if not ok:
+                assert (int(acc[r]), int(tok[r])) == (0, -1), (cu, r)
+                continue
+            w = (cu[r], cu[r + 1], r)
+            if w not in alone:
+                one, of = slice(*w[:2]), slice(max(w[0] - r, 0), max(w[0] - r, 0) + w[1] - w[0] - 1)
+                alone[w] = [t.cpu() for t in L.pe_verify(
+                    x[one], ids[one], torch.tensor([0, w[1] - w[0]], dtype=torch.int32,
+                                                   device="cuda"),
+                    au[one].contiguous(), torch.full((1,), 0.6, device="cuda"),
+                    draft_logits=dx[of], draft_dist=dd[of])]
+            a, t, l, d = alone[w]
+            assert int(acc[r]) == int(a) and int(tok[r]) == int(t), (cu, r)
+            assert torch.equal(lp[w[0]:w[1]], l) and torch.equal(dist[w[0]:w[1]], d), (cu, r)
+            free[w[0]:w[1]] = False
+        assert (lp.numpy()[free] == 5.0).all() and (dist.numpy()[free] == 77).all(), cu
