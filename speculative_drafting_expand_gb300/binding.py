@@ -834,6 +834,13 @@ def _op_empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _op_stream(index: int, stream) -> int:
+    """The stream of a call: `stream`, or device `index`'s current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
+
+
 def _op_call(index: int, stream, name, fn, *args) -> None:
     """Call into the library with device `index` current; `stream` None is
     that device's current stream."""
@@ -841,7 +848,7 @@ def _op_call(index: int, stream, name, fn, *args) -> None:
         raise ValueError(f"{name} needs tensors on a GPU")
     torch = _torch()
     C = torch._C
-    s = C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    s = _op_stream(index, stream)
     if C._cuda_getDevice() == index:
         status = fn(*args, s)
     else:
@@ -867,7 +874,9 @@ class W4Weight:
 
     codes uint8 [n, (k + 1) // 2], input 2 j in the low half of byte j; scales
     bfloat16 [n, ceil(k / group)].  The layout is made once, here, on `stream`
-    (None: the current one); codes and scales are not kept."""
+    (None: the current one); codes and scales are not kept.  A product on
+    another stream has to wait for it; the matrix may be dropped as soon as the
+    last product has been called."""
 
     def __init__(self, codes, scales, k: int, group: int, stream=None):
         torch = _torch()
@@ -894,6 +903,7 @@ class W4Weight:
         self.n, self.k, self.group, self.device = n, k, group, device
         self.packed = _op_empty(nbytes, torch.uint8, device, stream)
         self.index = self.packed.get_device()
+        self._of = _op_stream(self.index, stream)
 
     @classmethod
     def quantize(cls, weight, group: int = 32, stream=None) -> "W4Weight":
@@ -929,7 +939,9 @@ def pe_w4_linear(w: W4Weight, x, out=None, out_dtype=None, stream=None):
     ys = _op_rows("out", out, rows, w.n, w.index)
     _op_call(w.index, stream, "pe_w4_linear", lib().pe_w4_linear, w.packed.data_ptr(), w.n, w.k,
              w.group, rows, kind, x.data_ptr(), xs, ok, out.data_ptr(), ys)
-    _op_used(stream, w.packed, x, out)
+    _op_used(stream, x, out)
+    if _op_stream(w.index, stream) != w._of:      # its memory is of another stream
+        _op_used(stream or _torch().cuda.current_stream(w.index), w.packed)
     return out
 
 
