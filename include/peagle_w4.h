@@ -55,8 +55,9 @@ pe_status pe_w4_quantize(const void* w, int32_t dtype, int64_t w_stride, int32_t
  * bf16 -> fp32 or fp32 -> fp32; rows x_stride and y_stride elements apart, y
  * not overlapping x.  Products are exact, sums and scales are in fp32, in an
  * order that depends on the sizes and the device only; y is rounded once.
- * An element of x is right to 2^-38 of the largest of its row or better;
- * fp32 ones also to 2^-24 of themselves.  A row with an infinite or NaN
+ * x is held to 2^-38 of the largest element of its row: exactly down to 2^-30 of
+ * that in bf16 and to 2^-14 in fp32, whose smaller elements have fewer bits than
+ * their 24 (at 2^-24 of the largest 14).  A row with an infinite or NaN
  * element gives infinities and NaN, the other rows are as they would be.
  * Scales are any finite bf16 numbers.  Where a sum leaves fp32's range on the
  * way (never below scales of 2^92), that result is summed again in 64 bits, by

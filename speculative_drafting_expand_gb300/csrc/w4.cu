@@ -274,10 +274,13 @@ __device__ __forceinline__ uint4 load_inputs(const TX* from, int j, int k, bool 
 // reads the last row again; its column of the result is not used.
 // fp16 has bf16's bits and more, but not its range: each row (of this CTA's
 // inputs) is multiplied by the power of two, an even one, that brings its
-// largest to 2^13 .. 2^15, and elements below 2^-27 of that lose bits, at most
-// 2^-25, 2^-38 of the largest.  fp32 x is taken as three fp16 parts, 24 bits
-// above that.  16-bit x is put in place as it is while the largest are found,
-// and turned there, FLY loads of a thread at a time; fp32 x is read twice.
+// largest to 2^13 .. 2^15.  fp16 ends on a grid of 2^-24 there, so what is not on it
+// is off by 2^-25 at most, 2^-38 of the largest: bf16 elements below 2^-30 of that.
+// fp32 x is taken as three fp16 parts, which hold all 24 bits of an element down to
+// 2^-14 of the largest and end on the same grid (to go below it takes a further part
+// on a grid of its own, a third more products).  16-bit x is put in place as it is
+// while the largest are found, and turned there, FLY loads of a thread at a time;
+// fp32 x is read twice.
 template <typename TX, int PARTS, int FLY>
 __device__ __forceinline__ void stage_x(const W4Args& a, uint32_t* xs, int unit0, int units,
                                         uint32_t* largest, float* unscale) {
