@@ -348,21 +348,24 @@ struct SampleShared {
   uint32_t differ[2];
 };
 
-// Whether request r's window [w0, w1) is judged: it has rows of [0, T), a row of
-// the drafter's for each sampled draft, and nothing in cu_in contradicts it: the
-// entries before it lie at or before its start, those after it at or behind its
-// end.  Then a bisection finds the window for each of its rows, and no other such
-// window has any of them.  By all threads of a CTA.
-__device__ __forceinline__ bool window_is_sound(const int32_t* cu_in, int B, int T, int r, int w0,
-                                                int w1, bool sampled) {
-  if (w0 < 0 || w1 <= w0 || w1 > T) return false;
-  if (sampled && w1 - w0 > 1 && (w0 < r || w1 - 2 - r >= T - B)) return false;
+// Request r's window [w0, w1) is judged where it has rows of [0, T) and a row of
+// the drafter's for each sampled draft, and where nothing in cu_in contradicts it:
+// the entries before it lie at or before its start, those after it at or behind
+// its end.  Then a bisection finds the window for each of its rows, and no other
+// such window has any of them.
+__device__ __forceinline__ bool window_fits(int B, int T, int r, int w0, int w1, bool sampled) {
+  return w0 >= 0 && w1 > w0 && w1 <= T &&
+         !(sampled && w1 - w0 > 1 && (w0 < r || w1 - 2 - r >= T - B));
+}
+// Whether a thread's share of cu_in contradicts it.
+__device__ __forceinline__ bool window_contradicted(const int32_t* cu_in, int B, int r, int w0,
+                                                    int w1) {
   bool bad = false;
   for (int i = threadIdx.x; i <= B; i += kSampleThreads) {
     const int at = cu_in[i];
     bad = bad || (i < r && at > w0) || (i > r && at < w1);
   }
-  return !__syncthreads_or(bad);
+  return bad;
 }
 
 // The largest k for which the threads' largest logits are asked: past it the
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
   const int r = blockIdx.x / cluster;
   // the row's request, its filters, and the draft that it judges
   int q = r, draft = -1;
-  bool judges = false;
+  bool judges = false, contradicted = false;
   if (VERIFY) {
     int lo = 0, hi = a.B;  // the last request whose window starts at or before r
     while (hi - lo > 1) {
@@ -528,9 +531,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
     }
     q = lo;
     const int w0 = a.cu_in[q], w1 = a.cu_in[q + 1];
-    if (w0 > r || w1 <= r ||
-        !window_is_sound(a.cu_in, a.B, a.rows, q, w0, w1, !a.greedy_drafts))
+    if (w0 > r || w1 <= r || !window_fits(a.B, a.rows, q, w0, w1, !a.greedy_drafts))
       return;  // the whole cluster
+    contradicted = window_contradicted(a.cu_in, a.B, q, w0, w1);
     judges = r + 1 < w1;
     draft = judges ? a.ids[r + 1] : -1;
   }
@@ -567,8 +570,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows_kernel(
       top = fmaxf(top, largest_of<T>(v[i]));
     }
   }
-  unsigned long long x = float_order_key(top + 0.f), y = 0;
+  unsigned long long x = float_order_key(top + 0.f), y = contradicted;
   cluster_reduce<true>(sh.ex, parity, cluster, rank, x, y);
+  if (VERIFY && y) return;  // the whole cluster
   RowScale sc = {key_float(static_cast<uint32_t>(x)), inv};
   float most = INFINITY;
   if (sc.max == INFINITY) {
@@ -1118,7 +1122,8 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(
   grid_dep_wait();
   grid_dep_launch();
   const int w0 = a.cu_in[r], w1 = a.cu_in[r + 1];
-  if (!window_is_sound(a.cu_in, a.B, a.T, r, w0, w1, a.draft_logits != nullptr)) {
+  if (!window_fits(a.B, a.T, r, w0, w1, a.draft_logits != nullptr) ||
+      __syncthreads_or(window_contradicted(a.cu_in, a.B, r, w0, w1))) {
     if (rank == 0 && tid == 0) {
       record_error(a.err, PE_DEV_BAD_ROW);
       a.num_accepted[r] = 0;
