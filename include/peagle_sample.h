@@ -25,7 +25,10 @@
  * numbers, so they are exact and no order of additions changes a token.
  * A token is drawn from a number u of [0, 1): the first one, in the order of
  * the ids, at which the kept W so far exceed floor(u * total) (both as fp64;
- * u outside [0, 1) is taken as the nearest inside, NaN as 0).
+ * u outside [0, 1) is taken as the nearest inside, NaN as 0).  u has the numbers
+ * that fp32 has, or those that its maker gives it (mostly 2^-24 apart): a token
+ * into whose share of [0, 1) none of them falls is never drawn, so the tail is
+ * drawn from as finely as u is, not as finely as W.
  *
  * Conventions are those of peagle.h: caller-owned device memory, asynchronous
  * on `stream`, host-checkable errors returned before anything is launched, no

@@ -227,10 +227,11 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Pairs of codes - 8 in fp16, exact.  0x6400 is 1024, whose last bit is 1: the
-// low nibble of each half gives 1024 + code, the next one 1024 + 16 code.
+// Pairs of codes - 8 in fp16, exact, by the published method of kernels with 4-bit
+// weights, whose constants follow from the format.  0x6400 is 1024, whose last bit
+// is 1: the low nibble of each half gives 1024 + code, the next one 1024 + 16 code.
 // (bf16 has room for one nibble a half and takes two instructions a pair of
-// additions: 115 instructions a unit instead of 93.)
+// additions: 115 instructions a unit over a launch instead of 103.)
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&a)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -416,12 +417,13 @@ __device__ __noinline__ void store_by_64_bits(const W4Args& a, int r, int i) {
 // Products of 8 columns and not tcgen05 tiles: codes would have to be written to
 // shared memory as 16-bit operands of 128 rows, four times their bytes, for one
 // to eight columns of use.  The codes go from the ring into registers and from
-// there into the product; what bounds that is the issue of instructions, 93 a
-// unit for the codes, the products and the scales (201,088 x 2880 in groups of
-// 32, one row: 66 us, 4.95 TB/s, three quarters of the issue slots in use;
-// 151,936 x 2048 in groups of 128, eight rows: 40 us, 4.2 TB/s).  Small matrices
-// are bound by the way from the launch through x and the ring's first pairs to
-// the meeting (5120 x 2880, one row: 8.5 us).
+// there into the product; what bounds that is the issue of instructions, in three
+// quarters of the slots (201,088 x 2880 in groups of 32, one row: 66 us, 4.92 TB/s,
+// 103 warp instructions a unit over the launch; 151,936 x 2048 in groups of 128,
+// eight rows: 40 us, 4.2 TB/s, 114 a unit).  64 registers, which two CTAs an SM
+// leave a thread, are short: 12 to 76 bytes of them are spilled and loaded again.
+// Small matrices are bound by the way from the launch through x and the ring's
+// first pairs to the meeting (5120 x 2880, one row: 8.6 us).
 template <typename TX, typename TY, int NT, int GROUP>
 __global__ void __launch_bounds__(kW4Threads, W4Tune<NT>::CTAS)
     w4_linear_kernel(const __grid_constant__ W4Args a) {
